@@ -2,7 +2,7 @@
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel with nvcc and the
 objects are linked into one shared library exporting the C ABI of
-``include/hq.h``.  ``--fmad=false`` keeps every floating-point step rounded
+``include/hq.h`` and ``include/hq_kv4.h``.  ``--fmad=false`` keeps every floating-point step rounded
 where the source writes it (fused multiply-adds only where an explicit
 ``__fmaf_rn`` asks for one), which the bit-exact codes depend on.
 
@@ -38,7 +38,7 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
-        os.path.join(CSRC, "*.h")) + [os.path.join(ROOT, "include", "hq.h"), __file__]
+        os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(ROOT, "include", "*.h")) + [__file__]
 
 
 def up_to_date() -> bool:

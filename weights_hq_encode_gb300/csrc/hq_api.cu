@@ -6,6 +6,7 @@
 
 #include <cuda_runtime.h>
 
+#include "../../include/hq_kv4.h"
 #include "hq_fused.h"
 
 namespace {
@@ -469,6 +470,7 @@ const char *hq_status_string(int status) {
     case HQ_ERR_CORRUPT: return "corrupt stream";
     case HQ_ERR_TIMEOUT: return "cross-block wait timed out";
     case HQ_ERR_RANGE: return "input out of range";
+    case HQ_ERR_PAGE: return "sequence, position, length or page out of range";
     default: return status < 0 ? "unknown status" : "several errors";
   }
 }

@@ -1,0 +1,100 @@
+// hq_kv4.h -- arguments of the 4-bit window cache's kernels, shared by their
+// launchers and the C ABI, and the cache's addressing.
+#pragma once
+#include "../../include/hq_kv4.h"
+#include "hq_internal.h"
+
+namespace hq {
+
+constexpr int kUnit = HQ_KV4_UNIT;               // tokens of a unit
+constexpr int kUnitBytes = HQ_KV4_UNIT_BYTES;
+// Byte offsets inside a unit: K codes [16 tokens][64], V codes [8 token
+// pairs][8 chunks of 16 dimensions][2 tokens][8], K scales [16] bf16, V
+// scales [16] bf16.  Dimension d of a row is the low (even d) or high nibble
+// of its byte d / 2.
+constexpr int kUnitV = 1024, kUnitKs = 2048, kUnitVs = 2080;
+
+struct Kv4View {
+  unsigned char *pages;
+  int64_t n_pages;
+  int page_tokens, page_units;
+  int n_kv;
+  const int32_t *table;     // [n_seqs][width] page numbers
+  int n_seqs, width;
+  const uint32_t *signs;    // 128-bit sign mask
+  __host__ __device__ int64_t capacity() const { return (int64_t)width * page_tokens; }
+};
+
+// Rows of K and V entering or leaving the cache: element strides between
+// tokens and between heads, the 128 values of a row contiguous.
+struct Kv4Rows {
+  const void *k, *v;
+  int64_t k_token, k_head, v_token, v_head;
+  int kind;                 // HQ_T_*
+  int vec;                  // every row starts on a 16-byte boundary
+};
+
+struct Kv4RowArgs {
+  Kv4View c;
+  Kv4Rows rows;
+  const int32_t *seq, *pos; // [n_tokens]
+  int64_t n_tokens;
+  uint32_t *status;
+};
+
+struct Kv4AttnArgs {
+  Kv4View c;
+  const int32_t *lengths;   // [n_seqs]
+  const void *q;
+  int64_t q_seq, q_token, q_head;
+  int kind, out_kind;
+  int q_vec;
+  int q_len, Hq, G, R;      // G query heads a KV head, R = q_len * G rows a KV head
+  float scale;              // softmax scale, and the cap of the scores (0: none)
+  float cap;
+  void *out;                // [n_seqs][q_len][Hq][128]
+  float *lse;               // [n_seqs][q_len][Hq] or nullptr
+  const float *mass_in;     // [n_seqs][n_kv][capacity] or nullptr
+  float *mass_out;          // the same, or nullptr: no mass
+  float *z;                 // workspace [n_seqs][n_kv][R][capacity] when mass is wanted
+  float *row_lse;           // workspace [n_seqs][n_kv][R]: log2 of the row's sum, with its maximum
+  uint32_t *status;
+};
+
+struct Kv4EvictArgs {
+  Kv4View src, dst;
+  const int32_t *lengths;
+  const float *mass;        // [n_seqs][n_kv][src capacity]
+  int budget, recent;
+  int32_t *kept;            // [n_seqs][n_kv][budget]
+  int32_t *new_lengths;     // [n_seqs]
+  float *new_mass;          // [n_seqs][n_kv][dst capacity]
+  uint32_t *status;
+};
+
+int launch_kv4_append(const Kv4RowArgs &a, cudaStream_t st);
+int launch_kv4_read(const Kv4RowArgs &a, cudaStream_t st);
+int launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t st);
+int launch_kv4_evict(const Kv4EvictArgs &a, cudaStream_t st);
+
+#ifdef __CUDACC__
+// The page of position `pos` of sequence `seq` (both in range), or -1 when
+// the table names none of the pool's pages.
+__device__ __forceinline__ int64_t kv4_page(const Kv4View &c, int seq, int pos) {
+  const int p = __ldg(c.table + (int64_t)seq * c.width + pos / c.page_tokens);
+  return p >= 0 && p < c.n_pages ? (int64_t)p : -1;
+}
+// The unit of head h that holds position `pos` of a page.
+__device__ __forceinline__ unsigned char *kv4_unit(const Kv4View &c, int64_t page, int h, int pos) {
+  return c.pages + ((page * c.n_kv + h) * c.page_units + pos % c.page_tokens / kUnit) * kUnitBytes;
+}
+// A sequence's length, held to [0, capacity]; *bad when it was outside.
+__device__ __forceinline__ int kv4_length(const Kv4View &c, const int32_t *lengths, int seq, bool *bad) {
+  const int n = __ldg(lengths + seq), cap = c.width * c.page_tokens;
+  *bad = n < 0 || n > cap;
+  return n < 0 ? 0 : n > cap ? cap : n;
+}
+__device__ __forceinline__ float bf16_to_f32(uint32_t bits) { return __uint_as_float(bits << 16); }
+#endif
+
+}  // namespace hq

@@ -1,4 +1,5 @@
-"""Thin Python binding of the C ABI in ``include/hq.h`` (argument marshalling only).
+"""Thin Python binding of the C ABI in ``include/hq.h`` and ``include/hq_kv4.h``
+(argument marshalling only).
 
 Every entry point of the library has a function of the same name here that
 takes torch tensors (device memory and streams come from PyTorch) and passes
@@ -21,13 +22,18 @@ HQ_Z, HQ_A2, HQ_D4, HQ_E8 = 1, 2, 4, 8
 HQ_OUT_BF16, HQ_OUT_F32 = 0, 1
 HQ_TILE, HQ_GROUP_TILES = 128, 32
 HQ_FLAG_WORKSPACE_READY = 1
+HQ_ERR_PAGE = 64
+HQ_T_BF16, HQ_T_F32, HQ_T_F16 = 0, 1, 2
+HQ_KV4_UNIT, HQ_KV4_UNIT_BYTES = 16, 2112
 
 EXPORTED = ("hq_num_groups", "hq_encode_workspace_bytes", "hq_encode", "hq_decode",
             "hq_decode_qk_workspace_bytes", "hq_decode_qk", "hq_make_signs",
             "hq_make_layer_signs", "hq_status_string",
             "hq_encode_noalloc", "hq_payload_bits", "hq_calibrate",
             "hq_decode_attention_workspace_bytes", "hq_decode_attention",
-            "hq_decode_gemm_workspace_bytes", "hq_decode_gemm")
+            "hq_decode_gemm_workspace_bytes", "hq_decode_gemm",
+            "hq_kv4_page_bytes", "hq_kv4_append", "hq_kv4_read",
+            "hq_kv4_attention_workspace_bytes", "hq_kv4_attention", "hq_kv4_evict")
 HQ_NOALLOC_MAX_TILES = 1 << 22
 
 
@@ -43,6 +49,13 @@ class hq_params(ctypes.Structure):
 class hq_calibration(ctypes.Structure):
     _fields_ = [("alpha", ctypes.c_float), ("rice_k", ctypes.c_int32), ("bps", ctypes.c_double),
                 ("feasible", ctypes.c_int32), ("evaluations", ctypes.c_int32)]
+
+
+class hq_kv4_cache(ctypes.Structure):
+    _fields_ = [("d_pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_tokens", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("d_table", ctypes.c_void_p), ("n_seqs", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("d_signs", ctypes.c_void_p)]
 
 
 def library_path() -> str:
@@ -85,6 +98,20 @@ def _load():
     L.hq_decode_gemm_workspace_bytes.argtypes = [i64, i64, ctypes.c_int]
     L.hq_decode_gemm.restype = ctypes.c_int
     L.hq_decode_gemm.argtypes = [vp, vp, u64, vp, i64, i64, vp, ctypes.c_int, vp, vp, sz, vp, vp]
+    L.hq_kv4_page_bytes.restype = sz
+    L.hq_kv4_page_bytes.argtypes = [ctypes.c_int, ctypes.c_int]
+    L.hq_kv4_append.restype = ctypes.c_int
+    L.hq_kv4_append.argtypes = [vp, vp, vp, ctypes.c_int, i64, i64, i64, i64, vp, vp, i64, vp, vp]
+    L.hq_kv4_read.restype = ctypes.c_int
+    L.hq_kv4_read.argtypes = [vp, vp, vp, i64, vp, vp, ctypes.c_int, i64, i64, i64, i64, vp, vp]
+    L.hq_kv4_attention_workspace_bytes.restype = sz
+    L.hq_kv4_attention_workspace_bytes.argtypes = [vp, ctypes.c_int, ctypes.c_int, ctypes.c_int]
+    L.hq_kv4_attention.restype = ctypes.c_int
+    L.hq_kv4_attention.argtypes = [vp, vp, vp, ctypes.c_int, i64, i64, i64, ctypes.c_int,
+                                   ctypes.c_int, ctypes.c_float, ctypes.c_float, vp, ctypes.c_int,
+                                   vp, vp, vp, vp, sz, vp, vp]
+    L.hq_kv4_evict.restype = ctypes.c_int
+    L.hq_kv4_evict.argtypes = [vp, vp, vp, vp, ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp]
     L.hq_make_signs.restype = None
     L.hq_make_signs.argtypes = [u64, u64, vp]
     L.hq_make_layer_signs.restype = None
@@ -242,6 +269,154 @@ def hq_make_layer_signs(seed_d: int, seed_s: int, layer: int):
 
 def hq_status_string(status: int) -> str:
     return _lib.hq_status_string(int(status)).decode()
+
+
+# ------------------------------------------------------------------ 4-bit window cache
+_KINDS = {torch.bfloat16: HQ_T_BF16, torch.float32: HQ_T_F32, torch.float16: HQ_T_F16}
+
+
+def _on(t, cache, name, dtype, shape=None):
+    """The address of a contiguous tensor of the given dtype (and shape) on the cache's device."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor")
+    if t.device != cache._device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache._device}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows_on(t, cache, name, shape):
+    """Address and kind of a tensor of rows: any strides, the last dimension contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _KINDS:
+        raise TypeError(f"{name} must be a bf16, fp16 or fp32 tensor")
+    if t.device != cache._device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache._device}")
+    if tuple(t.shape) != shape or t.stride(-1) != 1:
+        raise ValueError(f"{name} must have the shape {shape} with contiguous rows, "
+                         f"not {tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr(), _KINDS[t.dtype]
+
+
+def _launch(cache, call, stream, *args) -> int:
+    """A library call with the cache's device current, on `stream` or that device's current one."""
+    if stream is None:
+        stream = torch.cuda.current_stream(cache._device)
+    if torch.cuda.current_device() == cache._device.index:
+        return call(*args, stream.cuda_stream)
+    with torch.cuda.device(cache._device):
+        return call(*args, stream.cuda_stream)
+
+
+def hq_kv4_page_bytes(n_kv_heads: int, page_tokens: int) -> int:
+    return int(_lib.hq_kv4_page_bytes(n_kv_heads, page_tokens))
+
+
+def make_kv4_cache(pages: torch.Tensor, table: torch.Tensor, page_tokens: int, n_kv_heads: int,
+                   signs: torch.Tensor) -> hq_kv4_cache:
+    """hq_kv4_cache over a pool of pages (contiguous uint8, a whole number of
+    pages of hq_kv4_page_bytes each), a block table (int32 [n_seqs, width])
+    and a sign mask (4 words, as signs_tensor gives them), all on one device.
+    The tensors are kept alive with it."""
+    page = hq_kv4_page_bytes(n_kv_heads, page_tokens)
+    if page == 0:
+        raise ValueError("page_tokens must be a positive multiple of 16, n_kv_heads positive")
+    for t, name, dtypes in ((pages, "pages", (torch.uint8,)), (table, "table", (torch.int32,)),
+                            (signs, "signs", (torch.int32, torch.uint32))):
+        if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous {dtypes[0]} tensor")
+        if not t.is_cuda or t.device != pages.device:
+            raise ValueError("pages, table and signs must be on one CUDA device")
+    if pages.numel() % page or table.dim() != 2 or signs.numel() != 4:
+        raise ValueError("expected whole pages, a table [n_seqs, width] and 4 words of signs")
+    c = hq_kv4_cache(pages.data_ptr(), pages.numel() // page, page_tokens, n_kv_heads,
+                     table.data_ptr(), table.shape[0], table.shape[1], signs.data_ptr())
+    c._pages, c._table, c._signs, c._device = pages, table, signs, pages.device
+    c._ref = ctypes.byref(c)
+    return c
+
+
+def hq_kv4_append(cache: hq_kv4_cache, k: torch.Tensor, v: torch.Tensor, seq: torch.Tensor,
+                  pos: torch.Tensor, status: torch.Tensor, stream=None) -> int:
+    """Codes k, v [n_tokens, n_kv_heads, 128] (any token and head strides) into the
+    cache at sequences `seq` and positions `pos` (int32 [n_tokens])."""
+    n = seq.numel()
+    shape = (n, cache.n_kv_heads, HQ_TILE)
+    kp, kind = _rows_on(k, cache, "k", shape)
+    vp, vkind = _rows_on(v, cache, "v", shape)
+    if kind != vkind:
+        raise TypeError("k and v must have one dtype")
+    return _launch(cache, _lib.hq_kv4_append, stream, cache._ref, kp, vp, kind, k.stride(0),
+                   k.stride(1), v.stride(0), v.stride(1), _on(seq, cache, "seq", torch.int32),
+                   _on(pos, cache, "pos", torch.int32, tuple(seq.shape)), n,
+                   _on(status, cache, "status", torch.int32))
+
+
+def hq_kv4_read(cache: hq_kv4_cache, seq: torch.Tensor, pos: torch.Tensor, k: torch.Tensor,
+                v: torch.Tensor, status: torch.Tensor, stream=None) -> int:
+    """Writes the rows of tokens (seq, pos) to k, v [n_tokens, n_kv_heads, 128]."""
+    n = seq.numel()
+    shape = (n, cache.n_kv_heads, HQ_TILE)
+    kp, kind = _rows_on(k, cache, "k", shape)
+    vp, vkind = _rows_on(v, cache, "v", shape)
+    if kind != vkind:
+        raise TypeError("k and v must have one dtype")
+    return _launch(cache, _lib.hq_kv4_read, stream, cache._ref,
+                   _on(seq, cache, "seq", torch.int32),
+                   _on(pos, cache, "pos", torch.int32, tuple(seq.shape)), n, kp, vp, kind,
+                   k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                   _on(status, cache, "status", torch.int32))
+
+
+def hq_kv4_attention_workspace_bytes(cache: hq_kv4_cache, q_len: int, Hq: int,
+                                     want_mass: bool = False) -> int:
+    return int(_lib.hq_kv4_attention_workspace_bytes(cache._ref, q_len, Hq, int(want_mass)))
+
+
+def hq_kv4_attention(cache: hq_kv4_cache, lengths: torch.Tensor, q: torch.Tensor, scale: float,
+                     cap: float, out: torch.Tensor, lse, mass_in, mass_out, ws: torch.Tensor,
+                     status: torch.Tensor, stream=None) -> int:
+    """Attention of q [n_seqs, q_len, Hq, 128] (any outer strides) over the cache's
+    sequences of `lengths` tokens: out [n_seqs, q_len, Hq, 128], optionally lse
+    [n_seqs, q_len, Hq] and mass_out = mass_in + the tokens' weights
+    [n_seqs, n_kv_heads, table_width * page_tokens] (either may be None)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise TypeError("q must be a tensor [n_seqs, q_len, Hq, 128]")
+    B, q_len, Hq, _ = q.shape
+    shape = (cache.n_seqs, q_len, Hq, HQ_TILE)
+    qp, kind = _rows_on(q, cache, "q", shape)
+    if not isinstance(out, torch.Tensor) or out.dtype not in _KINDS:
+        raise TypeError("out must be a bf16, fp16 or fp32 tensor")
+    mass_shape = (cache.n_seqs, cache.n_kv_heads, cache.table_width * cache.page_tokens)
+    return _launch(
+        cache, _lib.hq_kv4_attention, stream, cache._ref,
+        _on(lengths, cache, "lengths", torch.int32, (cache.n_seqs,)), qp, kind, q.stride(0),
+        q.stride(1), q.stride(2), q_len, Hq, scale, cap, _on(out, cache, "out", out.dtype, shape),
+        _KINDS[out.dtype],
+        None if lse is None else _on(lse, cache, "lse", torch.float32, shape[:3]),
+        None if mass_in is None else _on(mass_in, cache, "mass_in", torch.float32, mass_shape),
+        None if mass_out is None else _on(mass_out, cache, "mass_out", torch.float32, mass_shape),
+        _on(ws, cache, "ws", torch.uint8), ws.numel(), _on(status, cache, "status", torch.int32))
+
+
+def hq_kv4_evict(src: hq_kv4_cache, lengths: torch.Tensor, mass: torch.Tensor, dst: hq_kv4_cache,
+                 recent: int, kept: torch.Tensor, new_lengths: torch.Tensor,
+                 new_mass: torch.Tensor, status: torch.Tensor, stream=None) -> int:
+    """Moves the tokens that every KV head keeps (budget = kept.shape[2]) to dst's pages."""
+    if dst._device != src._device:
+        raise ValueError("src and dst must be on one device")
+    if not isinstance(kept, torch.Tensor) or kept.dim() != 3:
+        raise TypeError("kept must be an int32 tensor [n_seqs, n_kv_heads, budget]")
+    B, nh, budget = src.n_seqs, src.n_kv_heads, kept.shape[2]
+    return _launch(
+        src, _lib.hq_kv4_evict, stream, src._ref,
+        _on(lengths, src, "lengths", torch.int32, (B,)),
+        _on(mass, src, "mass", torch.float32, (B, nh, src.table_width * src.page_tokens)),
+        dst._ref, budget, recent, _on(kept, src, "kept", torch.int32, (B, nh, budget)),
+        _on(new_lengths, src, "new_lengths", torch.int32, (B,)),
+        _on(new_mass, src, "new_mass", torch.float32,
+            (B, nh, dst.table_width * dst.page_tokens)),
+        _on(status, src, "status", torch.int32))
 
 
 # ------------------------------------------------------------------ conveniences
