@@ -56,6 +56,10 @@ struct Kv4AttnArgs {
   float *lse;               // [n_seqs][q_len][Hq] or nullptr
   const float *mass_in;     // [n_seqs][n_kv][capacity] or nullptr
   float *mass_out;          // the same, or nullptr: no mass
+  int row_tiles;            // tiles of rows a KV head has
+  float *part;              // workspace: sums that several blocks share
+  float *stat;              // workspace: their references and sums of weights
+  int *joins;               // workspace: what each block leaves to be joined
   float *z;                 // workspace [n_seqs][n_kv][R][capacity] when mass is wanted
   float *row_lse;           // workspace [n_seqs][n_kv][R]: log2 of the row's sum, with its maximum
   uint32_t *status;
@@ -71,6 +75,12 @@ struct Kv4EvictArgs {
   float *new_mass;          // [n_seqs][n_kv][dst capacity]
   uint32_t *status;
 };
+
+constexpr int kKv4MaxBlocks = 1024;              // most blocks of one attention launch
+int kv4_row_tiles(int R);
+size_t kv4_part_bytes();
+size_t kv4_stat_bytes();
+size_t kv4_join_bytes();
 
 int launch_kv4_append(const Kv4RowArgs &a, cudaStream_t st);
 int launch_kv4_read(const Kv4RowArgs &a, cudaStream_t st);

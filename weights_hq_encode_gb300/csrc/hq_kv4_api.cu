@@ -23,7 +23,10 @@ bool sizes_ok(const hq_kv4_cache *c) {
   return c && c->n_pages >= 0 && c->n_pages <= INT32_MAX && c->page_tokens > 0 &&
          c->page_tokens % HQ_KV4_UNIT == 0 && c->n_kv_heads > 0 && c->n_kv_heads <= 65535 &&
          c->n_seqs >= 0 && c->n_seqs <= 65535 && c->table_width >= 0 &&
-         (int64_t)c->table_width * c->page_tokens <= kMaxCapacity;
+         (int64_t)c->table_width * c->page_tokens <= kMaxCapacity &&
+         // unit numbers of the pool fit 31 bits
+         (c->n_pages == 0 ||
+          c->n_pages <= INT32_MAX / c->n_kv_heads / (c->page_tokens / HQ_KV4_UNIT));
 }
 
 bool cache_ok(const hq_kv4_cache *c) {
@@ -73,14 +76,17 @@ int rows_call(const hq_kv4_cache *c, const void *k, const void *v, int kind, int
 }
 
 struct AttnSizes {
-  size_t z = 0, row_lse = 0;
-  size_t total() const { return z + row_lse; }
+  size_t part = 0, stat = 0, joins = 0, z = 0, row_lse = 0;
+  size_t total() const { return part + stat + joins + z + row_lse; }
 };
 
 bool attn_sizes(const hq_kv4_cache *c, int q_len, int Hq, int want_mass, AttnSizes *s) {
   if (!sizes_ok(c) || q_len <= 0 || q_len > 65535 || Hq <= 0 || Hq % c->n_kv_heads != 0) return false;
   const int64_t rows = (int64_t)c->n_seqs * q_len * Hq;
   if ((int64_t)q_len * (Hq / c->n_kv_heads) > (1 << 24) || rows > ((int64_t)1 << 31)) return false;
+  s->part = round256(kv4_part_bytes());
+  s->stat = round256(kv4_stat_bytes());
+  s->joins = round256(kv4_join_bytes());
   if (want_mass) {
     const size_t cap = (size_t)c->table_width * c->page_tokens;
     if (cap != 0 && (size_t)rows > ((size_t)1 << 44) / cap) return false;
@@ -117,7 +123,7 @@ int hq_kv4_read(const hq_kv4_cache *c, const int32_t *d_seq, const int32_t *d_po
 
 size_t hq_kv4_attention_workspace_bytes(const hq_kv4_cache *c, int q_len, int Hq, int want_mass) {
   AttnSizes s;
-  return attn_sizes(c, q_len, Hq, want_mass, &s) ? s.total() + 256 : 0;
+  return attn_sizes(c, q_len, Hq, want_mass, &s) ? s.total() : 0;
 }
 
 int hq_kv4_attention(const hq_kv4_cache *c, const int32_t *d_lengths, const void *d_q, int q_kind,
@@ -131,7 +137,7 @@ int hq_kv4_attention(const hq_kv4_cache *c, const int32_t *d_lengths, const void
       !attn_sizes(c, q_len, Hq, d_mass_out != nullptr, &s))
     return HQ_ERR_INVALID;
   if (c->n_seqs == 0) return HQ_OK;
-  if (!d_lengths || !d_q || !d_out || !d_ws || ws_bytes < s.total() + 256 || !aligned(d_ws, 256) ||
+  if (!d_lengths || !d_q || !d_out || !d_ws || ws_bytes < s.total() || !aligned(d_ws, 256) ||
       !aligned(d_out, 16) || !aligned(d_q, size_of(q_kind)) || !aligned(d_lse, 4) ||
       !aligned(d_mass_in, 4) || !aligned(d_mass_out, 4))
     return HQ_ERR_INVALID;
@@ -157,6 +163,13 @@ int hq_kv4_attention(const hq_kv4_cache *c, const int32_t *d_lengths, const void
   a.mass_in = d_mass_in;
   a.mass_out = d_mass_out;
   char *ws = static_cast<char *>(d_ws);
+  a.row_tiles = kv4_row_tiles(a.R);
+  a.part = reinterpret_cast<float *>(ws);
+  ws += s.part;
+  a.stat = reinterpret_cast<float *>(ws);
+  ws += s.stat;
+  a.joins = reinterpret_cast<int *>(ws);
+  ws += s.joins;
   a.z = reinterpret_cast<float *>(ws);
   a.row_lse = reinterpret_cast<float *>(ws + s.z);
   a.status = d_status;

@@ -1,8 +1,8 @@
 // hq_kv4_attn.cu -- attention over the 4-bit window cache, read straight from
 // the codes (include/hq_kv4.h).  The transform moves to the other operand:
-// with y' = H D q / sqrt(128), q . Khat[t] = s_t sum_d y'_d (c_d - 7.5), and
+// with q' = H D q / sqrt(128), q . Khat[t] = s_t sum_d q'_d (c_td - 7.5), and
 // sum_t p_t Vhat[t] = D H (sum_t p_t s_t (c_t - 7.5)) / sqrt(128), one
-// transform per output row.
+// transform per query row and one per output row.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -10,109 +10,600 @@
 #include "hq_device.cuh"
 #include "hq_kv4.h"
 #include "hq_kv4_io.cuh"
+#include "hq_umma.cuh"
 
 namespace hq {
 
+namespace {
+
 constexpr float kInvRoot128 = 0.08838834764831845f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kSimpleThreads = 128;
+constexpr float kLoScale = 2048.0f, kInvLoScale = 0x1p-11f;
+constexpr float kNoMax = -3.0e38f;               // below every finite score
+
+constexpr int kWarps = 4;                        // warps of a block
+constexpr int kAttnThreads = 32 * kWarps;
+constexpr int kStages = 7;                       // units a warp has in its ring
+constexpr int kRowTile = 8;                      // query rows of a block
+constexpr int kRingBytes = kWarps * kStages * kUnitBytes;
+constexpr int kQBytes = 8 * 32 * 16;             // query fragments: 8 K steps x 32 lanes x 16 bytes
+constexpr int kTrBytes = kRowTile * kTrTile * 4;
+constexpr int kAttnSmem = kRingBytes + kQBytes + kTrBytes;
+static_assert(kWarps * kRowTile * kTile * 4 <= kRingBytes, "the warps' sums fit the ring");
+
+// Work of one (sequence, head, row tile) beyond its units, in units: the
+// blocks split the batch into equal pieces of units + kSegmentCost.
+constexpr int kSegmentCost = 8, kMinPiece = 16;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// (x & MASK) | BITS as two fp16 values, less MINUS.
+template <uint32_t MASK, uint32_t BITS, uint32_t MINUS>
+__device__ __forceinline__ uint32_t codes2(uint32_t x) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "n"(MASK), "n"(BITS));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(y), "r"(MINUS));
+  return y;
+}
+// Four pairs of codes less 8 as fp16: pair i is nibble i of the low and of
+// the high half of x.  A nibble under the exponent of 1024 (bits 0-3) or of
+// 64 (bits 4-7) is 1024 + c or 64 + c exactly.
+__device__ __forceinline__ void unpack_pairs(uint32_t x, uint32_t p[4]) {
+  const uint32_t y = x >> 8;
+  p[0] = codes2<0x000F000Fu, 0x64006400u, 0x64086408u>(x);    // 1032
+  p[1] = codes2<0x00F000F0u, 0x54005400u, 0x54805480u>(x);    // 72
+  p[2] = codes2<0x000F000Fu, 0x64006400u, 0x64086408u>(y);
+  p[3] = codes2<0x00F000F0u, 0x54005400u, 0x54805480u>(y);
+}
+__device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+// (lo, hi) -> hi parts and 2^11 times the rests, both fp16 pairs: the parts
+// miss a value by 2^-22 of it, and by 2^-36 where it is below fp16's normal
+// range, so that small values keep their bits beside large ones.
+__device__ __forceinline__ void split2(float lo, float hi, uint32_t &h, uint32_t &rest) {
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+  const float r0 = __fmul_rn(__fsub_rn(lo, f.x), kLoScale), r1 = __fmul_rn(__fsub_rn(hi, f.y), kLoScale);
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(rest) : "f"(r1), "f"(r0));
+}
 
 template <int KIND>
 __device__ __forceinline__ void load_q16(const Kv4AttnArgs &a, int64_t at, int r, float x[16]) {
   load_row16<KIND>(a.q, at, r, a.q_vec != 0, x);
 }
 
-// One query row a block: every warp takes every fourth token, lane l of a
-// warp the dimensions 4 l .. 4 l + 3.
-__global__ void __launch_bounds__(kSimpleThreads) kv4_attn_kernel(Kv4AttnArgs a) {
-  __shared__ __align__(16) float s_tr[4 * kTrTile];
-  __shared__ __align__(16) float s_q[kTile];
-  __shared__ float s_m[4], s_l[4], s_acc[4][kTile];
-  const int hq = blockIdx.x, j = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const int h = hq / a.G, row = j * a.G + hq % a.G, lane = tid & 31, warp = tid >> 5;
-  bool bad;
-  const int len = kv4_length(a.c, a.lengths, b, &bad);
-  if (bad && tid == 0) atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
-  const int n = max(0, len - a.q_len + j + 1);
-  const int r = tid & 7;
+// 16 lanes of one row out, D H x / sqrt(128) applied: the last step of every
+// row.  All 32 lanes of the warp must call it.
+__device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, float x[16], float *tile, int r,
+                                           bool live, int64_t o) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], kInvRoot128);
+  fwht128_t8(x, tile, r);
+  if (!live) return;
   const uint32_t mw = __ldg(a.c.signs + (r >> 1)) >> (16 * (r & 1));
-  if (warp == 0) {
-    float x[16];
-    const int64_t at = b * a.q_seq + j * a.q_token + hq * a.q_head;
-    if (a.kind == HQ_T_F32) load_q16<HQ_T_F32>(a, at, r, x);
-    else if (a.kind == HQ_T_F16) load_q16<HQ_T_F16>(a, at, r, x);
-    else load_q16<HQ_T_BF16>(a, at, r, x);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(__float_as_uint(x[i]) ^ (((mw >> i) & 1u) << 31));
+  if (a.out_kind == HQ_T_F32) store_row16<HQ_T_F32>(a.out, o * kTile, r, true, x);
+  else if (a.out_kind == HQ_T_F16) store_row16<HQ_T_F16>(a.out, o * kTile, r, true, x);
+  else store_row16<HQ_T_BF16>(a.out, o * kTile, r, true, x);
+}
+
+// A row's sums over some of its tokens: l = sum 2^(z - m), and acc (kept
+// beside it) = sum 2^(z + log2 s - mw) (c - 7.5).
+struct RowStat {
+  float m, l, mw, pad;
+};
+
+__device__ __forceinline__ void finish_stats(const Kv4AttnArgs &a, int b, int h, int row, float M, float L) {
+  const float l2 = L == 0.0f ? -INFINITY : __fadd_rn(M, log2f(L));
+  const int j = row / a.G, hq = h * a.G + row % a.G;
+  if (a.lse != nullptr) a.lse[((int64_t)b * a.q_len + j) * a.Hq + hq] = __fmul_rn(l2, kLn2);
+  if (a.mass_out != nullptr) a.row_lse[((int64_t)b * a.c.n_kv + h) * a.R + row] = l2;
+}
+
+// Where a block's piece of the batch begins, and the piece's length: the
+// (sequence, head, row tile) triples laid end to end, each of its units +
+// kSegmentCost, are cut into equal pieces.
+struct Piece {
+  int64_t begin, end;       // of the laid-out batch, this block's piece
+  int64_t size;             // units + costs of a piece
+  int b;                    // sequence at `begin` (n_seqs: nothing left)
+  int64_t b_begin;          // where sequence b begins
+};
+
+__device__ __forceinline__ int units_of(const Kv4AttnArgs &a, int b) {
+  bool bad;
+  const int n = kv4_length(a.c, a.lengths, b, &bad);
+  return (n + kUnit - 1) / kUnit;
+}
+
+__device__ __forceinline__ int64_t span_of(const Kv4AttnArgs &a, int b) {
+  const int nu = units_of(a, b);
+  return nu == 0 ? 0 : (int64_t)a.c.n_kv * a.row_tiles * (nu + kSegmentCost);
+}
+
+__device__ Piece find_piece(const Kv4AttnArgs &a) {
+  __shared__ int64_t s_sum[kWarps];
+  __shared__ int64_t s_begin;
+  __shared__ int s_b;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int B = a.c.n_seqs;
+  Piece p;
+  int64_t total = 0;
+  for (int b = tid; b < B; b += kAttnThreads) total += span_of(a, b);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+  if (lane == 0) s_sum[warp] = total;
+  if (tid == 0) s_b = B;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += s_sum[w];
+  const int64_t even = (total + gridDim.x - 1) / gridDim.x;
+  p.size = even > kMinPiece ? even : kMinPiece;
+  p.begin = (int64_t)blockIdx.x * p.size;
+  p.end = p.begin + p.size < total ? p.begin + p.size : total;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < B && p.begin < p.end; b0 += kAttnThreads) {
+    __syncthreads();
+    const int b = b0 + tid;
+    const int64_t span = b < B ? span_of(a, b) : 0;
+    int64_t incl = span;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) incl += s_sum[w];
+      all += s_sum[w];
+    }
+    const int64_t e = base + incl;
+    if (e - span <= p.begin && p.begin < e) {    // at most one thread of one step
+      s_b = b;
+      s_begin = e - span;
+    }
+    base += all;
+    if (base > p.begin) break;                   // block-uniform
+  }
+  __syncthreads();
+  p.b = s_b;
+  p.b_begin = s_begin;
+  return p;
+}
+
+// Each warp of a block takes every fourth unit of a segment (the units of one
+// sequence and head that fall into the block's piece) through a ring of its
+// own in shared memory, filled by asynchronous copies, and keeps its own sums;
+// the four are added at the segment's end.  A segment that is a whole (sequence, head) is finished here,
+// the others leave their sums for kv4_join_kernel.
+//
+// The products run on mma.sync m16n8k16 with the 8 query rows' high parts as
+// rows 0 .. 7 and their low parts as rows 8 .. 15, so the fp32-level split
+// costs no further instruction and lands in the same thread.  The codes are
+// unpacked in registers, which is why these are not tcgen05 products: their
+// operands would first have to be stored to shared memory as fp16, four times the bytes read.
+template <bool CAP, bool MASS>
+__global__ void __launch_bounds__(kAttnThreads, 3) kv4_attn_kernel(Kv4AttnArgs a) {
+  extern __shared__ __align__(128) unsigned char s_mem[];
+  __shared__ RowStat s_stat[kWarps][kRowTile];
+  __shared__ float4 s_row[kRowTile];             // multiplier of the scores, sum q' / 2, tokens seen
+  __shared__ int s_bad[kWarps][kStages];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n8 = lane >> 2, c4 = lane & 3;       // mma row or column group, and place in it
+  unsigned char *const ring = s_mem + warp * kStages * kUnitBytes;
+  uint4 *const s_q = reinterpret_cast<uint4 *>(s_mem + kRingBytes);
+  float *const s_tr = reinterpret_cast<float *>(s_mem + kRingBytes + kQBytes);
+  const uint32_t ring_a = smem_addr(ring);
+  // copies: 16 bytes a lane and 512-byte quarter; V's chunks are permuted
+  // inside their 128-byte rows so that the reads below touch all banks
+  const uint32_t cp_k = lane * 16, cp_v = kUnitV + (lane >> 3) * 128 + (((lane & 7) ^ (2 * (lane >> 3))) * 16);
+  const uint32_t ld_v = kUnitV + c4 * 128 + ((n8 ^ (2 * c4)) * 16);
+  const Piece piece = find_piece(a);
+  int join_b = 0, join_count = 0, join_pair = 0;
+  int64_t cur = piece.begin;
+  int b = piece.b;
+  int64_t b_begin = piece.b_begin;
+  while (cur < piece.end) {                      // block-uniform throughout
+    const int nu = units_of(a, b), span1 = nu + kSegmentCost;
+    const int64_t b_end = b_begin + (nu == 0 ? 0 : (int64_t)a.c.n_kv * a.row_tiles * span1);
+    if (cur >= b_end) {
+      ++b;
+      b_begin = b_end;
+      continue;
+    }
+    const int pair = (int)((cur - b_begin) / span1);        // head and row tile of sequence b
+    const int64_t at = b_begin + (int64_t)pair * span1;     // where the pair begins
+    const int u_lo = (int)max((int64_t)0, cur - at - kSegmentCost);
+    const int u_hi = (int)min((int64_t)nu, piece.end - at - kSegmentCost);
+    cur = min(at + span1, piece.end);
+    if (u_lo >= u_hi) continue;
+    const int h = pair / a.row_tiles, row0 = (pair % a.row_tiles) * kRowTile;
+    bool bad_len;
+    const int len = kv4_length(a.c, a.lengths, b, &bad_len);
+
+    // ---- this warp's units u_lo + warp, u_lo + warp + 4, ..: the ring's first copies
+    const int mine = (u_hi - u_lo - warp + kWarps - 1) / kWarps;
+    int where_now = -1, where_next = -1;         // unit numbers in the pool of 32 of this warp's units
+    const auto look_up = [&](int first) {
+      const int i = first + lane;
+      if (i >= mine) return -1;
+      const int u = u_lo + warp + kWarps * i, pj = u / a.c.page_units;
+      const int page = __ldg(a.c.table + (int64_t)b * a.c.width + pj);
+      return page >= 0 && page < a.c.n_pages ? (page * a.c.n_kv + h) * a.c.page_units + u - pj * a.c.page_units
+                                             : -1;
+    };
+    int issued = 0;
+    const auto issue = [&]() {                   // the next unit into its stage; one group, maybe empty
+      if (issued < mine) {
+        if ((issued & 31) == 0) {
+          where_now = issued == 0 ? look_up(0) : where_next;
+          where_next = look_up(issued + 32);
+        }
+        const int unit = __shfl_sync(0xffffffffu, where_now, issued & 31);
+        const int stage = issued % kStages;
+        if (unit >= 0) {
+          const unsigned char *src = a.c.pages + (int64_t)unit * kUnitBytes + lane * 16;
+          const uint32_t dst = ring_a + stage * kUnitBytes;
+          cp_async16(dst + cp_k, src);
+          cp_async16(dst + cp_k + 512, src + 512);
+          cp_async16(dst + cp_v, src + kUnitV);
+          cp_async16(dst + cp_v + 512, src + kUnitV + 512);
+          if (lane < 4) cp_async16(dst + kUnitKs + lane * 16, src + kUnitKs);
+        }
+        if (lane == 0) s_bad[warp][stage] = unit < 0;
+        ++issued;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue();
+
+    // ---- the query rows: rotated, scaled by a power of two, split, as mma fragments
+    if (tid < 8 * kRowTile) {
+      const int rr = tid >> 3, r = tid & 7, row = row0 + rr;
+      const bool live = row < a.R;
+      const int j = live ? row / a.G : 0, hq = live ? h * a.G + row % a.G : 0;
+      float x[16];
+      if (live) {
+        const int64_t qa = b * a.q_seq + j * a.q_token + hq * a.q_head;
+        if (a.kind == HQ_T_F32) load_q16<HQ_T_F32>(a, qa, r, x);
+        else if (a.kind == HQ_T_F16) load_q16<HQ_T_F16>(a, qa, r, x);
+        else load_q16<HQ_T_BF16>(a, qa, r, x);
+      }
+      const uint32_t mw = __ldg(a.c.signs + (r >> 1)) >> (16 * (r & 1));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float v = live ? x[i] : 0.0f;
+        x[i] = __fmul_rn(__uint_as_float(__float_as_uint(v) ^ (((mw >> i) & 1u) << 31)), kInvRoot128);
+      }
+      fwht128_t8(x, s_tr + rr * kTrTile, r);
+      float top = 0.0f, sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        top = fmaxf(top, fabsf(x[i]));
+        sum = __fadd_rn(sum, x[i]);
+      }
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+      }
+      const float sc = scale_of(top), inv = inv_scale_of(top);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], sc);
+      // lane r holds words 2 (r & 1), 2 (r & 1) + 1 of the 32 dimensions of fragment lane r / 2
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint4 f;
+          split2(x[8 * w + 2 * i], x[8 * w + 2 * i + 4], f.x, f.y);
+          split2(x[8 * w + 2 * i + 1], x[8 * w + 2 * i + 5], f.z, f.w);
+          s_q[(2 * (2 * (r & 1) + w) + i) * 32 + rr * 4 + (r >> 1)] = f;
+        }
+      }
+      if (r == 0) {
+        const float mul = CAP ? __fmul_rn(__fdiv_rn(a.scale, a.cap), inv) : __fmul_rn(__fmul_rn(a.scale, kLog2e), inv);
+        s_row[rr] = make_float4(mul, __fmul_rn(__fmul_rn(sum, sc), 0.5f),
+                                __int_as_float(max(0, len - a.q_len + j + 1)), 0.0f);
+      }
+    }
+    __syncthreads();
+    uint32_t qa[8][4];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint4 f = s_q[k * 32 + lane];
+      qa[k][0] = f.x; qa[k][1] = f.y; qa[k][2] = f.z; qa[k][3] = f.w;
+    }
+    const float zmul = s_row[n8].x, qhalf = s_row[n8].y;
+    const int seen = __float_as_int(s_row[n8].z), seen_all = len - a.q_len + row0 / a.G + 1;
+    const float cap_l2 = CAP ? __fmul_rn(a.cap, kLog2e) : 0.0f;
+    float *zrow = nullptr;
+    if (MASS && row0 + n8 < a.R)
+      zrow = a.z + (((int64_t)b * a.c.n_kv + h) * a.R + row0 + n8) * a.c.capacity();
+
+    // ---- the units
+    float acc[16][4], m = kNoMax, mw = kNoMax, l = 0.0f, wsum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      x[i] = __fmul_rn(__uint_as_float(__float_as_uint(x[i]) ^ (((mw >> i) & 1u) << 31)), kInvRoot128);
-    fwht128_t8(x, s_tr + (lane >> 3) * kTrTile, r);
-    if (lane < 8)
-      for (int i = 0; i < 16; ++i) s_q[16 * r + i] = x[i];
-  }
-  __syncthreads();
-  float q[4], acc[4] = {0.f, 0.f, 0.f, 0.f}, m = -3.0e38f, l = 0.0f;
-  for (int i = 0; i < 4; ++i) q[i] = s_q[4 * lane + i];
-  const int64_t head = (int64_t)b * a.c.n_kv + h;
-  float *zrow = a.mass_out ? a.z + (head * a.R + row) * a.c.capacity() : nullptr;
-  for (int t = warp; t < n; t += 4) {
-    const int64_t page = kv4_page(a.c, b, t);
-    float z = -INFINITY;
-    if (page >= 0) {
-      const unsigned char *u = kv4_unit(a.c, page, h, t);
-      const int tok = t % kUnit;
-      const uint32_t kw = *reinterpret_cast<const uint16_t *>(u + tok * 64 + 2 * lane);
-      float s = 0.0f;
-      for (int i = 0; i < 4; ++i) s = __fmaf_rn(q[i], (float)((kw >> (4 * i)) & 15u) - 7.5f, s);
-      for (int d = 16; d >= 1; d >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, d));
-      z = __fmul_rn(__fmul_rn(s, bf16_to_f32(reinterpret_cast<const uint16_t *>(u + kUnitKs)[tok])), a.scale);
-      if (a.cap > 0.0f) z = __fmul_rn(a.cap, tanhf(__fdiv_rn(z, a.cap)));
-      z = __fmul_rn(z, kLog2e);
-      const uint32_t vw = *reinterpret_cast<const uint16_t *>(u + kUnitV + (tok >> 1) * 128 + (lane >> 2) * 16 +
-                                                             (tok & 1) * 8 + 2 * (lane & 3));
-      const float mm = fmaxf(m, z), f = exp2f(__fsub_rn(m, mm)), p = exp2f(__fsub_rn(z, mm));
-      const float w = __fmul_rn(p, bf16_to_f32(reinterpret_cast<const uint16_t *>(u + kUnitVs)[tok]));
-      m = mm;
-      l = __fmaf_rn(l, f, p);
-      for (int i = 0; i < 4; ++i)
-        acc[i] = __fmaf_rn(w, (float)((vw >> (4 * i)) & 15u) - 7.5f, __fmul_rn(acc[i], f));
-    } else if (lane == 0) {
-      atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
+    for (int it = 0; it < mine; ++it) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncwarp();                              // unit `it` has come, and unit `it` - 1 is used up
+      issue();
+      const int stage = it % kStages;
+      const uint32_t U = ring_a + stage * kUnitBytes;
+      const int t0 = (u_lo + warp + kWarps * it) * kUnit;
+      const bool bad = s_bad[warp][stage] != 0;
+      float z[2][2], ls[2][2];
+      {
+        float s[2][4];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+        }
+        const uint4 k0 = lds128(U + cp_k), k1 = lds128(U + cp_k + 512);
+        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t p0[4], p1[4];
+          unpack_pairs(w0[j], p0);
+          unpack_pairs(w1[j], p1);
+          mma16816(s[0], qa[2 * j], p0[0], p0[1]);
+          mma16816(s[1], qa[2 * j], p1[0], p1[1]);
+          mma16816(s[0], qa[2 * j + 1], p0[2], p0[3]);
+          mma16816(s[1], qa[2 * j + 1], p1[2], p1[3]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const uint32_t ks = lds32(U + kUnitKs + 16 * nt + 4 * c4), vs = lds32(U + kUnitVs + 16 * nt + 4 * c4);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float sk = e ? __uint_as_float(ks & 0xFFFF0000u) : __uint_as_float(ks << 16);
+            const float sv = e ? __uint_as_float(vs & 0xFFFF0000u) : __uint_as_float(vs << 16);
+            const float d = __fadd_rn(__fmaf_rn(s[nt][2 + e], kInvLoScale, s[nt][e]), qhalf);
+            float y = __fmul_rn(__fmul_rn(d, sk), zmul);
+            if (CAP) {                           // cap tanh(y) = cap (1 - 2 / (1 + e^2y)), odd in y
+              const float t = ex2(__fmul_rn(fabsf(y), 2.0f * kLog2e));
+              y = copysignf(__fmul_rn(cap_l2, __fsub_rn(1.0f, __fdividef(2.0f, __fadd_rn(t, 1.0f)))), y);
+            }
+            z[nt][e] = y;
+            ls[nt][e] = lg2(sv);
+          }
+        }
+      }
+      if (t0 + kUnit > seen_all || bad) {        // warp-uniform: some token is not seen by some row
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (bad || t0 + 8 * nt + 2 * c4 + e >= seen) {
+              z[nt][e] = -INFINITY;
+              ls[nt][e] = 0.0f;
+            }
+        if (bad && lane == 0) atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
+      }
+      if (MASS && zrow != nullptr) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+          *reinterpret_cast<float2 *>(zrow + t0 + 8 * nt + 2 * c4) = make_float2(z[nt][0], z[nt][1]);
+      }
+      // references of the sums: p = 2^(z - m) stays below 2^64 and a weight
+      // w = 2^(z + log2 s - mw) below 2^15 without moving them at every unit
+      float u[2][2], zt = z[0][0], ut = -INFINITY;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          u[nt][e] = __fadd_rn(z[nt][e], ls[nt][e]);
+          zt = fmaxf(zt, z[nt][e]);
+          ut = fmaxf(ut, u[nt][e]);
+        }
+      if (__any_sync(0xffffffffu, __fsub_rn(zt, m) > 64.0f || __fsub_rn(ut, mw) > 15.0f)) {
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+          zt = fmaxf(zt, __shfl_xor_sync(0xffffffffu, zt, d));
+          ut = fmaxf(ut, __shfl_xor_sync(0xffffffffu, ut, d));
+        }
+        const float m2 = fmaxf(m, zt), mw2 = fmaxf(mw, __fsub_rn(ut, 7.0f));
+        const float f = ex2(__fsub_rn(mw, mw2));
+        l = __fmul_rn(l, ex2(__fsub_rn(m, m2)));
+        wsum = __fmul_rn(wsum, f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][e] = __fmul_rn(acc[i][e], f);
+        m = m2;
+        mw = mw2;
+      }
+      uint32_t pa[4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const float w0 = ex2(__fsub_rn(u[nt][0], mw)), w1 = ex2(__fsub_rn(u[nt][1], mw));
+        l = __fadd_rn(l, __fadd_rn(ex2(__fsub_rn(z[nt][0], m)), ex2(__fsub_rn(z[nt][1], m))));
+        wsum = __fadd_rn(wsum, __fadd_rn(w0, w1));
+        split2(w0, w1, pa[2 * nt], pa[2 * nt + 1]);
+      }
+      // V: lane (n8, c4) holds the 16 dimensions of chunk n8 of token pairs c4 and 4 + c4
+      const uint4 v0 = lds128(U + ld_v), v1 = lds128(U + ld_v + 512);
+      const uint32_t a0[2] = {v0.x, v0.y}, b0[2] = {v0.z, v0.w}, a1[2] = {v1.x, v1.y}, b1[2] = {v1.z, v1.w};
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t p0[4], p1[4];
+          unpack_pairs(__byte_perm(a0[w], b0[w], hf ? 0x7632 : 0x5410), p0);
+          unpack_pairs(__byte_perm(a1[w], b1[w], hf ? 0x7632 : 0x5410), p1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma16816(acc[8 * w + 4 * hf + i], pa, p0[i], p1[i]);
+        }
+      }
     }
-    if (zrow != nullptr && lane == 0) zrow[t] = z;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // ---- the block's sums: l and the weights' sum over the row's four lanes, then the four warps
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+      l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, d));
+      wsum = __fadd_rn(wsum, __shfl_xor_sync(0xffffffffu, wsum, d));
+    }
+    __syncthreads();                             // every warp's ring is free
+    float *const s_acc = reinterpret_cast<float *>(s_mem);
+    const float half = __fmul_rn(wsum, 0.5f);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float *dst = s_acc + (warp * kRowTile + n8) * kTile + 16 * (2 * c4 + e);
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        float4 v;
+        v.x = __fadd_rn(__fmaf_rn(acc[i][2 + e], kInvLoScale, acc[i][e]), half);
+        v.y = __fadd_rn(__fmaf_rn(acc[i + 1][2 + e], kInvLoScale, acc[i + 1][e]), half);
+        v.z = __fadd_rn(__fmaf_rn(acc[i + 2][2 + e], kInvLoScale, acc[i + 2][e]), half);
+        v.w = __fadd_rn(__fmaf_rn(acc[i + 3][2 + e], kInvLoScale, acc[i + 3][e]), half);
+        *reinterpret_cast<float4 *>(dst + i) = v;
+      }
+    }
+    if (c4 == 0) s_stat[warp][n8] = RowStat{m, l, mw, 0.0f};
+    __syncthreads();
+    const bool whole = u_lo == 0 && u_hi == nu;
+    if (!whole && u_lo == 0) {                   // begun here, ended by later blocks
+      join_b = b;
+      join_pair = pair;
+      join_count = (int)((at + span1 - 1) / piece.size - blockIdx.x);
+    }
+    if (tid < 8 * kRowTile) {
+      const int rr = tid >> 3, r = tid & 7, row = row0 + rr;
+      float M = kNoMax, MW = kNoMax, L = 0.0f, x[16];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        M = fmaxf(M, s_stat[w][rr].m);
+        MW = fmaxf(MW, s_stat[w][rr].mw);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        L = __fmaf_rn(s_stat[w][rr].l, ex2(__fsub_rn(s_stat[w][rr].m, M)), L);
+        const float f = ex2(__fsub_rn(s_stat[w][rr].mw, MW));
+        const float *src = s_acc + (w * kRowTile + rr) * kTile + 16 * r;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = __fmaf_rn(src[i], f, x[i]);
+      }
+      if (whole) {
+        const bool live = row < a.R;
+        const float f = ex2(__fmul_rn(__fsub_rn(MW, M), 0.5f));
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          x[i] = L == 0.0f ? 0.0f : __fmul_rn(__fmul_rn(__fdiv_rn(x[i], L), f), f);
+        const int j = row / a.G, hq = h * a.G + row % a.G;
+        finish_row(a, x, s_tr + rr * kTrTile, r, live, ((int64_t)b * a.q_len + j) * a.Hq + hq);
+        if (live && r == 0) finish_stats(a, b, h, row, M, L);
+      } else {
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (u_lo == 0 ? 1 : 0);
+        float4 *dst = reinterpret_cast<float4 *>(a.part + (slot * kRowTile + rr) * kTile + 16 * r);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) dst[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+        if (r == 0) reinterpret_cast<float4 *>(a.stat)[slot * kRowTile + rr] = make_float4(M, L, MW, 0.0f);
+      }
+    }
+    __syncthreads();                             // the ring, the rows and the statistics are free
   }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
+  if (tid == 0) {
+    reinterpret_cast<int4 *>(a.joins)[blockIdx.x] = make_int4(join_count, join_b, join_pair, 0);
   }
-  for (int i = 0; i < 4; ++i) s_acc[warp][4 * lane + i] = acc[i];
-  __syncthreads();
-  float M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3])), L = 0.0f;
-  for (int w = 0; w < 4; ++w) L = __fmaf_rn(s_l[w], exp2f(__fsub_rn(s_m[w], M)), L);
-  if (warp == 0) {                               // D H (acc / L) / sqrt(128)
+  // rows of sequences without tokens, and lengths out of range
+  for (int64_t i = (int64_t)blockIdx.x * (kAttnThreads / 8) + (tid >> 3); i < (int64_t)a.c.n_seqs * a.q_len * a.Hq;
+       i += (int64_t)gridDim.x * (kAttnThreads / 8)) {
+    const int sb = (int)(i / ((int64_t)a.q_len * a.Hq));
+    bool bad_len;
+    const int len = kv4_length(a.c, a.lengths, sb, &bad_len);
+    if (bad_len && (tid & 7) == 0) atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
+    if (len > 0) continue;
     float x[16];
-    for (int i = 0; i < 16; ++i) {
-      float v = 0.0f;
-      for (int w = 0; w < 4; ++w)
-        v = __fmaf_rn(s_acc[w][16 * r + i], exp2f(__fsub_rn(s_m[w], M)), v);
-      x[i] = L == 0.0f ? 0.0f : __fmul_rn(__fdiv_rn(v, L), kInvRoot128);
-    }
-    fwht128_t8(x, s_tr + (lane >> 3) * kTrTile, r);
-    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(__float_as_uint(x[i]) ^ (((mw >> i) & 1u) << 31));
-    const int64_t o = ((int64_t)b * a.q_len + j) * a.Hq + hq;
-    if (lane < 8) {
-      if (a.out_kind == HQ_T_F32) store_row16<HQ_T_F32>(a.out, o * kTile, r, true, x);
-      else if (a.out_kind == HQ_T_F16) store_row16<HQ_T_F16>(a.out, o * kTile, r, true, x);
-      else store_row16<HQ_T_BF16>(a.out, o * kTile, r, true, x);
-    }
-    if (lane == 0) {
-      const float l2 = L == 0.0f ? -INFINITY : __fadd_rn(M, log2f(L));
-      if (a.lse != nullptr) a.lse[o] = __fmul_rn(l2, kLn2);
-      if (a.mass_out != nullptr) a.row_lse[head * a.R + row] = l2;
-    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = 0.0f;
+    if (a.out_kind == HQ_T_F32) store_row16<HQ_T_F32>(a.out, i * kTile, tid & 7, true, x);
+    else store_row16<HQ_T_BF16>(a.out, i * kTile, tid & 7, true, x);   // zeros are the same in fp16
+    if ((tid & 7) == 0 && a.lse != nullptr) a.lse[i] = -INFINITY;
   }
 }
 
-// mass_out = mass_in + sum over the head's rows of exp2(z - lse).
+// The sums of a (sequence, head, row tile) that several blocks share, joined
+// in block order: block i of this kernel joins what block i of the other began.
+__global__ void __launch_bounds__(8 * kRowTile) kv4_join_kernel(Kv4AttnArgs a) {
+  __shared__ __align__(16) float s_tr[kRowTile * kTrTile];
+  const int4 job = reinterpret_cast<const int4 *>(a.joins)[blockIdx.x];
+  if (job.x == 0) return;
+  const int tid = threadIdx.x, rr = tid >> 3, r = tid & 7;
+  const int b = job.y, h = job.z / a.row_tiles, row = (job.z % a.row_tiles) * kRowTile + rr;
+  const float4 *stat = reinterpret_cast<const float4 *>(a.stat);
+  const auto slot_of = [&](int i) { return 2 * ((int64_t)blockIdx.x + i) + (i == 0 ? 1 : 0); };
+  float M = kNoMax, MW = kNoMax, L = 0.0f, x[16];
+  for (int i = 0; i <= job.x; ++i) {
+    const float4 s = stat[slot_of(i) * kRowTile + rr];
+    M = fmaxf(M, s.x);
+    MW = fmaxf(MW, s.z);
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+  for (int i = 0; i <= job.x; ++i) {
+    const float4 s = stat[slot_of(i) * kRowTile + rr];
+    L = __fmaf_rn(s.y, ex2(__fsub_rn(s.x, M)), L);
+    const float f = ex2(__fsub_rn(s.z, MW));
+    const float4 *src = reinterpret_cast<const float4 *>(a.part + (slot_of(i) * kRowTile + rr) * kTile + 16 * r);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float4 v = src[c];
+      x[4 * c] = __fmaf_rn(v.x, f, x[4 * c]);
+      x[4 * c + 1] = __fmaf_rn(v.y, f, x[4 * c + 1]);
+      x[4 * c + 2] = __fmaf_rn(v.z, f, x[4 * c + 2]);
+      x[4 * c + 3] = __fmaf_rn(v.w, f, x[4 * c + 3]);
+    }
+  }
+  const float f = ex2(__fmul_rn(__fsub_rn(MW, M), 0.5f));
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    x[i] = L == 0.0f ? 0.0f : __fmul_rn(__fmul_rn(__fdiv_rn(x[i], L), f), f);
+  const bool live = row < a.R;
+  const int j = row / a.G, hq = h * a.G + row % a.G;
+  finish_row(a, x, s_tr + rr * kTrTile, r, live, ((int64_t)b * a.q_len + j) * a.Hq + hq);
+  if (live && r == 0) finish_stats(a, b, h, row, M, L);
+}
+
+// mass_out = mass_in + sum over the head's rows of 2^(z - log2 of the row's sum).
 __global__ void __launch_bounds__(256) kv4_mass_kernel(Kv4AttnArgs a) {
   const int h = blockIdx.y, b = blockIdx.z;
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -122,17 +613,59 @@ __global__ void __launch_bounds__(256) kv4_mass_kernel(Kv4AttnArgs a) {
   const int64_t head = (int64_t)b * a.c.n_kv + h, cap = a.c.capacity();
   float s = 0.0f;
   for (int row = 0; row < a.R; ++row) {
-    if (t > len - a.q_len + row / a.G) continue;
     const float z = a.z[(head * a.R + row) * cap + t];
-    if (z > -INFINITY || z != z) s = __fadd_rn(s, exp2f(__fsub_rn(z, a.row_lse[head * a.R + row])));
+    if (z > -INFINITY || z != z) s = __fadd_rn(s, ex2(__fsub_rn(z, a.row_lse[head * a.R + row])));
   }
   a.mass_out[head * cap + t] = a.mass_in != nullptr ? __fadd_rn(a.mass_in[head * cap + t], s) : s;
 }
 
-int launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t st) {
-  kv4_attn_kernel<<<dim3((unsigned)a.Hq, (unsigned)a.q_len, (unsigned)a.c.n_seqs), kSimpleThreads, 0, st>>>(a);
+// Resident blocks of the attention kernel on the current device (asked once
+// per instance and device).
+template <bool CAP, bool MASS>
+int resident_blocks() {
+  static int cache[64] = {};
+  int dev = 0, sms = 0, per_sm = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (cudaFuncSetAttribute(kv4_attn_kernel<CAP, MASS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kAttnSmem) != cudaSuccess)
+    return 0;
+  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kv4_attn_kernel<CAP, MASS>, kAttnThreads, kAttnSmem);
+  const int n = sms * per_sm;
+  if (dev >= 0 && dev < 64) cache[dev] = n;
+  return n;
+}
+
+template <bool CAP, bool MASS>
+int launch_attn(const Kv4AttnArgs &a, cudaStream_t st) {
+  int grid = resident_blocks<CAP, MASS>();
+  if (grid <= 0) return 1;
+  if (grid > kKv4MaxBlocks) grid = kKv4MaxBlocks;
+  // no more blocks than pieces of the longest batch the table allows
+  const int64_t most = ((a.c.capacity() / kUnit + kSegmentCost) * a.c.n_seqs * a.c.n_kv * a.row_tiles +
+                        kMinPiece - 1) / kMinPiece;
+  if (most < grid) grid = (int)most;
+  kv4_attn_kernel<CAP, MASS><<<grid, kAttnThreads, kAttnSmem, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return 1;
-  if (a.mass_out != nullptr) {
+  kv4_join_kernel<<<grid, 8 * kRowTile, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? 0 : 1;
+}
+
+}  // namespace
+
+int kv4_row_tiles(int R) { return (R + kRowTile - 1) / kRowTile; }
+size_t kv4_part_bytes() { return (size_t)2 * kKv4MaxBlocks * kRowTile * kTile * sizeof(float); }
+size_t kv4_stat_bytes() { return (size_t)2 * kKv4MaxBlocks * kRowTile * sizeof(float4); }
+size_t kv4_join_bytes() { return (size_t)kKv4MaxBlocks * sizeof(int4); }
+
+int launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t st) {
+  const bool mass = a.mass_out != nullptr;
+  int rc;
+  if (a.cap > 0.0f) rc = mass ? launch_attn<true, true>(a, st) : launch_attn<true, false>(a, st);
+  else rc = mass ? launch_attn<false, true>(a, st) : launch_attn<false, false>(a, st);
+  if (rc != 0) return rc;
+  if (mass && a.c.capacity() > 0) {
     kv4_mass_kernel<<<dim3((unsigned)((a.c.capacity() + 255) / 256), (unsigned)a.c.n_kv,
                            (unsigned)a.c.n_seqs), 256, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return 1;
