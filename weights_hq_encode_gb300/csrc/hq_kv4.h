@@ -78,8 +78,8 @@ struct Kv4EvictArgs {
 
 constexpr int kKv4MaxBlocks = 1024;              // most blocks of one attention launch
 int kv4_row_tiles(int R);
-size_t kv4_part_bytes();
-size_t kv4_stat_bytes();
+size_t kv4_part_bytes(int R);
+size_t kv4_stat_bytes(int R);
 size_t kv4_join_bytes();
 
 int launch_kv4_append(const Kv4RowArgs &a, cudaStream_t st);

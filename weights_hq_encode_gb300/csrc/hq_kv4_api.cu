@@ -84,8 +84,8 @@ bool attn_sizes(const hq_kv4_cache *c, int q_len, int Hq, int want_mass, AttnSiz
   if (!sizes_ok(c) || q_len <= 0 || q_len > 65535 || Hq <= 0 || Hq % c->n_kv_heads != 0) return false;
   const int64_t rows = (int64_t)c->n_seqs * q_len * Hq;
   if ((int64_t)q_len * (Hq / c->n_kv_heads) > (1 << 24) || rows > ((int64_t)1 << 31)) return false;
-  s->part = round256(kv4_part_bytes());
-  s->stat = round256(kv4_stat_bytes());
+  s->part = round256(kv4_part_bytes(q_len * (Hq / c->n_kv_heads)));
+  s->stat = round256(kv4_stat_bytes(q_len * (Hq / c->n_kv_heads)));
   s->joins = round256(kv4_join_bytes());
   if (want_mass) {
     const size_t cap = (size_t)c->table_width * c->page_tokens;

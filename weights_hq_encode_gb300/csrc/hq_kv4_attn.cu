@@ -23,13 +23,18 @@ constexpr float kNoMax = -3.0e38f;               // below every finite score
 
 constexpr int kWarps = 4;                        // warps of a block
 constexpr int kAttnThreads = 32 * kWarps;
-constexpr int kStages = 7;                       // units a warp has in its ring
-constexpr int kRowTile = 8;                      // query rows of a block
+constexpr int kStages = 4;                       // units a warp has in its ring
 constexpr int kRingBytes = kWarps * kStages * kUnitBytes;
-constexpr int kQBytes = 8 * 32 * 16;             // query fragments: 8 K steps x 32 lanes x 16 bytes
-constexpr int kTrBytes = kRowTile * kTrTile * 4;
-constexpr int kAttnSmem = kRingBytes + kQBytes + kTrBytes;
-static_assert(kWarps * kRowTile * kTile * 4 <= kRingBytes, "the warps' sums fit the ring");
+// NC column groups of 8: the high and the low parts of 4 query rows each
+template <int NC>
+struct Shape {
+  static constexpr int rows = 4 * NC;            // query rows of a block
+  static constexpr int q_bytes = 8 * NC * 32 * 8;   // query fragments: 8 K steps, 8 bytes a lane
+  static constexpr int sum_bytes = kWarps * rows * kTile * 4;   // the warps' sums, in the ring's place
+  static constexpr int ring = kRingBytes > sum_bytes ? kRingBytes : sum_bytes;
+  static constexpr int smem = ring + q_bytes + rows * kTrTile * 4;
+  static constexpr int blocks = NC == 1 ? 4 : 3; // resident blocks a multiprocessor
+};
 
 // Work of one (sequence, head, row tile) beyond its units, in units: the
 // blocks split the batch into equal pieces of units + kSegmentCost.
@@ -45,30 +50,42 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// (x & MASK) | BITS as two fp16 values, less MINUS.
-template <uint32_t MASK, uint32_t BITS, uint32_t MINUS>
-__device__ __forceinline__ uint32_t codes2(uint32_t x) {
+// The exponents under which a nibble becomes an fp16 value, in registers that
+// the compiler does not fill again at every use.
+struct Magic {
+  uint32_t low, high;       // 1024 (nibble in bits 0-3), 64 (bits 4-7), twice each
+};
+__device__ __forceinline__ Magic make_magic() {
+  Magic g;
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(g.low));
+  asm volatile("mov.b32 %0, 0x54005400;" : "=r"(g.high));
+  return g;
+}
+// (x & MASK) | bits as two fp16 values, less MINUS.
+template <uint32_t MASK, uint32_t MINUS>
+__device__ __forceinline__ uint32_t codes2(uint32_t x, uint32_t bits) {
   uint32_t y;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "n"(MASK), "n"(BITS));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "n"(MASK), "r"(bits));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(y), "r"(MINUS));
   return y;
 }
 // Four pairs of codes less 8 as fp16: pair i is nibble i of the low and of
-// the high half of x.  A nibble under the exponent of 1024 (bits 0-3) or of
-// 64 (bits 4-7) is 1024 + c or 64 + c exactly.
-__device__ __forceinline__ void unpack_pairs(uint32_t x, uint32_t p[4]) {
+// the high half of x.  Under the exponents above a nibble is 1024 + c or
+// 64 + c exactly.
+__device__ __forceinline__ void unpack_pairs(uint32_t x, const Magic &g, uint32_t p[4]) {
   const uint32_t y = x >> 8;
-  p[0] = codes2<0x000F000Fu, 0x64006400u, 0x64086408u>(x);    // 1032
-  p[1] = codes2<0x00F000F0u, 0x54005400u, 0x54805480u>(x);    // 72
-  p[2] = codes2<0x000F000Fu, 0x64006400u, 0x64086408u>(y);
-  p[3] = codes2<0x00F000F0u, 0x54005400u, 0x54805480u>(y);
+  p[0] = codes2<0x000F000Fu, 0x64086408u>(x, g.low);    // 1032
+  p[1] = codes2<0x00F000F0u, 0x54805480u>(x, g.high);   // 72
+  p[2] = codes2<0x000F000Fu, 0x64086408u>(y, g.low);
+  p[3] = codes2<0x00F000F0u, 0x54805480u>(y, g.high);
 }
-__device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -80,10 +97,16 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
+__device__ __forceinline__ float lds_bf16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return __uint_as_float((uint32_t)v << 16);
+}
+// An 8 x 8 matrix of 16-bit values, two a lane, transposed over the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(v));
+  return y;
 }
 // (lo, hi) -> hi parts and 2^11 times the rests, both fp16 pairs: the parts
 // miss a value by 2^-22 of it, and by 2^-36 where it is below fp16's normal
@@ -121,6 +144,13 @@ __device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, float x[16], fl
 struct RowStat {
   float m, l, mw, pad;
 };
+
+// acc / l at its own references: x 2^mw / (l 2^m), zeros where there is no weight.
+__device__ __forceinline__ void normalize(float x[16], float m, float mw, float l) {
+  const float f = ex2(__fmul_rn(__fsub_rn(mw, m), 0.5f));   // in two steps, each within range
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = l == 0.0f ? 0.0f : __fmul_rn(__fmul_rn(__fdiv_rn(x[i], l), f), f);
+}
 
 __device__ __forceinline__ void finish_stats(const Kv4AttnArgs &a, int b, int h, int row, float M, float L) {
   const float l2 = L == 0.0f ? -INFINITY : __fadd_rn(M, log2f(L));
@@ -207,30 +237,37 @@ __device__ Piece find_piece(const Kv4AttnArgs &a) {
 // Each warp of a block takes every fourth unit of a segment (the units of one
 // sequence and head that fall into the block's piece) through a ring of its
 // own in shared memory, filled by asynchronous copies, and keeps its own sums;
-// the four are added at the segment's end.  A segment that is a whole (sequence, head) is finished here,
-// the others leave their sums for kv4_join_kernel.
+// the four are added at the segment's end.  A segment that is a whole
+// (sequence, head) is finished here, the others leave their sums for
+// kv4_join_kernel.
 //
-// The products run on mma.sync m16n8k16 with the 8 query rows' high parts as
-// rows 0 .. 7 and their low parts as rows 8 .. 15, so the fp32-level split
-// costs no further instruction and lands in the same thread.  The codes are
-// unpacked in registers, which is why these are not tcgen05 products: their
-// operands would first have to be stored to shared memory as fp16, four times the bytes read.
-template <bool CAP, bool MASS>
-__global__ void __launch_bounds__(kAttnThreads, 3) kv4_attn_kernel(Kv4AttnArgs a) {
+// The products run on mma.sync m16n8k16, tokens (scores) and dimensions
+// (values) as the 16 rows and query rows as the 8 columns: columns 0 .. 3 the
+// high parts of 4 rows, columns 4 .. 7 their low parts, so that the fp32-level
+// split of 4 rows fills one instruction.  The codes are unpacked in registers,
+// straight into operand fragments; that is why these are not tcgen05
+// products, whose operands would first have to be stored to shared memory as
+// fp16, four times the bytes that were read.
+template <int NC, bool CAP, bool MASS>
+__global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kernel(Kv4AttnArgs a) {
+  constexpr int kRows = Shape<NC>::rows;
   extern __shared__ __align__(128) unsigned char s_mem[];
-  __shared__ RowStat s_stat[kWarps][kRowTile];
-  __shared__ float4 s_row[kRowTile];             // multiplier of the scores, sum q' / 2, tokens seen
-  __shared__ int s_bad[kWarps][kStages];
+  __shared__ RowStat s_stat[kWarps][kRows];
+  __shared__ float s_mul[kRows], s_half[kRows];  // multiplier of the scores, sum q' / 2
+  __shared__ int s_seen[kRows];                  // tokens seen
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n8 = lane >> 2, c4 = lane & 3;       // mma row or column group, and place in it
-  unsigned char *const ring = s_mem + warp * kStages * kUnitBytes;
-  uint4 *const s_q = reinterpret_cast<uint4 *>(s_mem + kRingBytes);
-  float *const s_tr = reinterpret_cast<float *>(s_mem + kRingBytes + kQBytes);
-  const uint32_t ring_a = smem_addr(ring);
+  const int n8 = lane >> 2, c4 = lane & 3;       // fragment row group, and place in it
+  const bool low = c4 >= 2;                      // this lane's columns are low parts
+  const int e0 = 2 * (c4 & 1);                   // its rows of a column group: e0, e0 + 1
+  uint2 *const s_q = reinterpret_cast<uint2 *>(s_mem + Shape<NC>::ring);
+  float *const s_tr = reinterpret_cast<float *>(s_mem + Shape<NC>::ring + Shape<NC>::q_bytes);
+  const uint32_t ring_a = smem_addr(s_mem) + warp * kStages * kUnitBytes;
   // copies: 16 bytes a lane and 512-byte quarter; V's chunks are permuted
   // inside their 128-byte rows so that the reads below touch all banks
   const uint32_t cp_k = lane * 16, cp_v = kUnitV + (lane >> 3) * 128 + (((lane & 7) ^ (2 * (lane >> 3))) * 16);
   const uint32_t ld_v = kUnitV + c4 * 128 + ((n8 ^ (2 * c4)) * 16);
+  const Magic magic = make_magic();
+  const float k_own = low ? kInvLoScale : 1.0f, k_other = low ? 1.0f : kInvLoScale;
   const Piece piece = find_piece(a);
   int join_b = 0, join_count = 0, join_pair = 0;
   int64_t cur = piece.begin;
@@ -250,7 +287,7 @@ __global__ void __launch_bounds__(kAttnThreads, 3) kv4_attn_kernel(Kv4AttnArgs a
     const int u_hi = (int)min((int64_t)nu, piece.end - at - kSegmentCost);
     cur = min(at + span1, piece.end);
     if (u_lo >= u_hi) continue;
-    const int h = pair / a.row_tiles, row0 = (pair % a.row_tiles) * kRowTile;
+    const int h = pair / a.row_tiles, row0 = (pair % a.row_tiles) * kRows;
     bool bad_len;
     const int len = kv4_length(a.c, a.lengths, b, &bad_len);
 
@@ -265,7 +302,8 @@ __global__ void __launch_bounds__(kAttnThreads, 3) kv4_attn_kernel(Kv4AttnArgs a
       return page >= 0 && page < a.c.n_pages ? (page * a.c.n_kv + h) * a.c.page_units + u - pj * a.c.page_units
                                              : -1;
     };
-    int issued = 0;
+    int issued = 0, put = 0;                     // units asked for, and the stage of the next
+    uint32_t bad_stages = 0;                     // stages whose unit has no page
     const auto issue = [&]() {                   // the next unit into its stage; one group, maybe empty
       if (issued < mine) {
         if ((issued & 31) == 0) {
@@ -273,18 +311,20 @@ __global__ void __launch_bounds__(kAttnThreads, 3) kv4_attn_kernel(Kv4AttnArgs a
           where_next = look_up(issued + 32);
         }
         const int unit = __shfl_sync(0xffffffffu, where_now, issued & 31);
-        const int stage = issued % kStages;
+        bad_stages &= ~(1u << put);
         if (unit >= 0) {
           const unsigned char *src = a.c.pages + (int64_t)unit * kUnitBytes + lane * 16;
-          const uint32_t dst = ring_a + stage * kUnitBytes;
+          const uint32_t dst = ring_a + put * kUnitBytes;
           cp_async16(dst + cp_k, src);
           cp_async16(dst + cp_k + 512, src + 512);
           cp_async16(dst + cp_v, src + kUnitV);
           cp_async16(dst + cp_v + 512, src + kUnitV + 512);
           if (lane < 4) cp_async16(dst + kUnitKs + lane * 16, src + kUnitKs);
+        } else {
+          bad_stages |= 1u << put;
         }
-        if (lane == 0) s_bad[warp][stage] = unit < 0;
         ++issued;
+        put = put == kStages - 1 ? 0 : put + 1;
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -292,7 +332,7 @@ __global__ void __launch_bounds__(kAttnThreads, 3) kv4_attn_kernel(Kv4AttnArgs a
     for (int i = 0; i < kStages - 1; ++i) issue();
 
     // ---- the query rows: rotated, scaled by a power of two, split, as mma fragments
-    if (tid < 8 * kRowTile) {
+    if (tid < 8 * kRows) {
       const int rr = tid >> 3, r = tid & 7, row = row0 + rr;
       const bool live = row < a.R;
       const int j = live ? row / a.G : 0, hq = live ? h * a.G + row % a.G : 0;
@@ -324,141 +364,185 @@ __global__ void __launch_bounds__(kAttnThreads, 3) kv4_attn_kernel(Kv4AttnArgs a
       const float sc = scale_of(top), inv = inv_scale_of(top);
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], sc);
-      // lane r holds words 2 (r & 1), 2 (r & 1) + 1 of the 32 dimensions of fragment lane r / 2
+      // lane r holds words 2 (r & 1), 2 (r & 1) + 1 of the 32 dimensions of place r / 2; row rr is
+      // columns rr % 4 (high parts) and rr % 4 + 4 (low parts) of group rr / 4
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          uint4 f;
-          split2(x[8 * w + 2 * i], x[8 * w + 2 * i + 4], f.x, f.y);
-          split2(x[8 * w + 2 * i + 1], x[8 * w + 2 * i + 5], f.z, f.w);
-          s_q[(2 * (2 * (r & 1) + w) + i) * 32 + rr * 4 + (r >> 1)] = f;
+          uint2 hi, lo;
+          split2(x[8 * w + 2 * i], x[8 * w + 2 * i + 4], hi.x, lo.x);
+          split2(x[8 * w + 2 * i + 1], x[8 * w + 2 * i + 5], hi.y, lo.y);
+          uint2 *dst = s_q + ((2 * (2 * (r & 1) + w) + i) * NC + (rr >> 2)) * 32 + (rr & 3) * 4 + (r >> 1);
+          dst[0] = hi;
+          dst[16] = lo;
         }
       }
       if (r == 0) {
-        const float mul = CAP ? __fmul_rn(__fdiv_rn(a.scale, a.cap), inv) : __fmul_rn(__fmul_rn(a.scale, kLog2e), inv);
-        s_row[rr] = make_float4(mul, __fmul_rn(__fmul_rn(sum, sc), 0.5f),
-                                __int_as_float(max(0, len - a.q_len + j + 1)), 0.0f);
+        s_mul[rr] = CAP ? __fmul_rn(__fdiv_rn(a.scale, a.cap), inv) : __fmul_rn(__fmul_rn(a.scale, kLog2e), inv);
+        s_half[rr] = __fmul_rn(__fmul_rn(sum, sc), 0.5f);
+        s_seen[rr] = max(0, len - a.q_len + j + 1);
       }
     }
     __syncthreads();
-    uint32_t qa[8][4];
+    uint2 qb[8][NC];
+    uint64_t zmul[NC];
+    float q0[NC][2];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint4 f = s_q[k * 32 + lane];
-      qa[k][0] = f.x; qa[k][1] = f.y; qa[k][2] = f.z; qa[k][3] = f.w;
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int g = 0; g < NC; ++g) qb[k][g] = s_q[(k * NC + g) * 32 + lane];
+#pragma unroll
+    for (int g = 0; g < NC; ++g) {
+      zmul[g] = pk2(s_mul[4 * g + e0], s_mul[4 * g + e0 + 1]);
+      q0[g][0] = low ? 0.0f : s_half[4 * g + e0];
+      q0[g][1] = low ? 0.0f : s_half[4 * g + e0 + 1];
     }
-    const float zmul = s_row[n8].x, qhalf = s_row[n8].y;
-    const int seen = __float_as_int(s_row[n8].z), seen_all = len - a.q_len + row0 / a.G + 1;
+    const int seen_all = len - a.q_len + row0 / a.G + 1;    // the least of any row here
     const float cap_l2 = CAP ? __fmul_rn(a.cap, kLog2e) : 0.0f;
-    float *zrow = nullptr;
-    if (MASS && row0 + n8 < a.R)
-      zrow = a.z + (((int64_t)b * a.c.n_kv + h) * a.R + row0 + n8) * a.c.capacity();
 
     // ---- the units
-    float acc[16][4], m = kNoMax, mw = kNoMax, l = 0.0f, wsum = 0.0f;
+    float acc[NC][8][4], l[NC][2], wsum[NC][2], m[NC][2], mw[NC][2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int g = 0; g < NC; ++g) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
-    for (int it = 0; it < mine; ++it) {
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[g][i][e] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[g][e] = wsum[g][e] = 0.0f;
+        m[g][e] = mw[g][e] = kNoMax;
+      }
+    }
+    int get = 0;                                 // stage of the next unit to use
+    int t0 = (u_lo + warp) * kUnit;
+    for (int it = 0; it < mine; ++it, t0 += kWarps * kUnit) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();                              // unit `it` has come, and unit `it` - 1 is used up
       issue();
-      const int stage = it % kStages;
-      const uint32_t U = ring_a + stage * kUnitBytes;
-      const int t0 = (u_lo + warp + kWarps * it) * kUnit;
-      const bool bad = s_bad[warp][stage] != 0;
-      float z[2][2], ls[2][2];
-      {
-        float s[2][4];
+      const uint32_t U = ring_a + get * kUnitBytes;
+      const bool bad = (bad_stages >> get) & 1u;
+      get = get == kStages - 1 ? 0 : get + 1;
+      // scores: lane (n8, c4) gets tokens n8 and n8 + 8, columns 2 c4, 2 c4 + 1
+      float s[NC][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-        }
+      for (int g = 0; g < NC; ++g) {
+        s[g][0] = s[g][2] = q0[g][0];
+        s[g][1] = s[g][3] = q0[g][1];
+      }
+      {
         const uint4 k0 = lds128(U + cp_k), k1 = lds128(U + cp_k + 512);
         const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t p0[4], p1[4];
-          unpack_pairs(w0[j], p0);
-          unpack_pairs(w1[j], p1);
-          mma16816(s[0], qa[2 * j], p0[0], p0[1]);
-          mma16816(s[1], qa[2 * j], p1[0], p1[1]);
-          mma16816(s[0], qa[2 * j + 1], p0[2], p0[3]);
-          mma16816(s[1], qa[2 * j + 1], p1[2], p1[3]);
-        }
+          unpack_pairs(w0[j], magic, p0);
+          unpack_pairs(w1[j], magic, p1);
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const uint32_t ks = lds32(U + kUnitKs + 16 * nt + 4 * c4), vs = lds32(U + kUnitVs + 16 * nt + 4 * c4);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float sk = e ? __uint_as_float(ks & 0xFFFF0000u) : __uint_as_float(ks << 16);
-            const float sv = e ? __uint_as_float(vs & 0xFFFF0000u) : __uint_as_float(vs << 16);
-            const float d = __fadd_rn(__fmaf_rn(s[nt][2 + e], kInvLoScale, s[nt][e]), qhalf);
-            float y = __fmul_rn(__fmul_rn(d, sk), zmul);
-            if (CAP) {                           // cap tanh(y) = cap (1 - 2 / (1 + e^2y)), odd in y
-              const float t = ex2(__fmul_rn(fabsf(y), 2.0f * kLog2e));
-              y = copysignf(__fmul_rn(cap_l2, __fsub_rn(1.0f, __fdividef(2.0f, __fadd_rn(t, 1.0f)))), y);
-            }
-            z[nt][e] = y;
-            ls[nt][e] = lg2(sv);
+          for (int g = 0; g < NC; ++g) {
+            mma16816(s[g], p0[0], p1[0], p0[1], p1[1], qb[2 * j][g].x, qb[2 * j][g].y);
+            mma16816(s[g], p0[2], p1[2], p0[3], p1[3], qb[2 * j + 1][g].x, qb[2 * j + 1][g].y);
           }
         }
       }
+      const float sk[2] = {lds_bf16(U + kUnitKs + 2 * n8), lds_bf16(U + kUnitKs + 2 * n8 + 16)};
+      const float ls[2] = {lg2(lds_bf16(U + kUnitVs + 2 * n8)), lg2(lds_bf16(U + kUnitVs + 2 * n8 + 16))};
+      float z[NC][2][2], u[NC][2][2];            // [group][token][row]
+#pragma unroll
+      for (int g = 0; g < NC; ++g)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float o0 = __shfl_xor_sync(0xffffffffu, s[g][2 * t], 2);
+          const float o1 = __shfl_xor_sync(0xffffffffu, s[g][2 * t + 1], 2);
+          const uint64_t d = fma2(pk2(o0, o1), pk2(k_other, k_other),
+                                  mul2(pk2(s[g][2 * t], s[g][2 * t + 1]), pk2(k_own, k_own)));
+          upk2(mul2(mul2(d, pk2(sk[t], sk[t])), zmul[g]), z[g][t][0], z[g][t][1]);
+          if (CAP) {                             // cap tanh(y) = cap (1 - 2 / (1 + e^2|y|)), y's sign
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float y = z[g][t][e], x = ex2(__fmul_rn(fabsf(y), 2.0f * kLog2e));
+              z[g][t][e] = copysignf(
+                  __fmul_rn(cap_l2, __fsub_rn(1.0f, __fdividef(2.0f, __fadd_rn(x, 1.0f)))), y);
+            }
+          }
+          upk2(add2(pk2(z[g][t][0], z[g][t][1]), pk2(ls[t], ls[t])), u[g][t][0], u[g][t][1]);
+        }
       if (t0 + kUnit > seen_all || bad) {        // warp-uniform: some token is not seen by some row
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int g = 0; g < NC; ++g)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (bad || t0 + 8 * nt + 2 * c4 + e >= seen) {
-              z[nt][e] = -INFINITY;
-              ls[nt][e] = 0.0f;
-            }
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (bad || t0 + 8 * t + n8 >= s_seen[4 * g + e0 + e]) z[g][t][e] = u[g][t][e] = -INFINITY;
         if (bad && lane == 0) atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
       }
-      if (MASS && zrow != nullptr) {
+      if (MASS && !low) {
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-          *reinterpret_cast<float2 *>(zrow + t0 + 8 * nt + 2 * c4) = make_float2(z[nt][0], z[nt][1]);
+        for (int g = 0; g < NC; ++g)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = row0 + 4 * g + e0 + e;
+            if (row >= a.R) continue;
+            float *zrow = a.z + (((int64_t)b * a.c.n_kv + h) * a.R + row) * a.c.capacity() + t0 + n8;
+            zrow[0] = z[g][0][e];
+            zrow[8] = z[g][1][e];
+          }
       }
-      // references of the sums: p = 2^(z - m) stays below 2^64 and a weight
-      // w = 2^(z + log2 s - mw) below 2^15 without moving them at every unit
-      float u[2][2], zt = z[0][0], ut = -INFINITY;
+      // p = 2^(z - m) stays below 2^64 and a weight w = 2^(z + log2 s - mw) below 2^15 without
+      // moving the references m and mw at every unit
+      float pe[NC][2][2], we[NC][2][2];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int pass = 0; pass < 2; ++pass) {
+        float pt = kNoMax, wt = kNoMax;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          u[nt][e] = __fadd_rn(z[nt][e], ls[nt][e]);
-          zt = fmaxf(zt, z[nt][e]);
-          ut = fmaxf(ut, u[nt][e]);
+        for (int g = 0; g < NC; ++g)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            upk2(sub2(pk2(z[g][t][0], z[g][t][1]), pk2(m[g][0], m[g][1])), pe[g][t][0], pe[g][t][1]);
+            upk2(sub2(pk2(u[g][t][0], u[g][t][1]), pk2(mw[g][0], mw[g][1])), we[g][t][0], we[g][t][1]);
+            pt = fmaxf(pt, fmaxf(pe[g][t][0], pe[g][t][1]));
+            wt = fmaxf(wt, fmaxf(we[g][t][0], we[g][t][1]));
+          }
+        if (pass == 1 || !__any_sync(0xffffffffu, pt > 64.0f || wt > 15.0f)) break;
+#pragma unroll
+        for (int g = 0; g < NC; ++g) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float zt = fmaxf(z[g][0][e], z[g][1][e]), ut = fmaxf(u[g][0][e], u[g][1][e]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              zt = fmaxf(zt, __shfl_xor_sync(0xffffffffu, zt, d));
+              ut = fmaxf(ut, __shfl_xor_sync(0xffffffffu, ut, d));
+            }
+            const float m2 = fmaxf(m[g][e], zt), mw2 = fmaxf(mw[g][e], __fsub_rn(ut, 7.0f));
+            const float f = ex2(__fsub_rn(mw[g][e], mw2));
+            l[g][e] = __fmul_rn(l[g][e], ex2(__fsub_rn(m[g][e], m2)));
+            wsum[g][e] = __fmul_rn(wsum[g][e], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              acc[g][i][e] = __fmul_rn(acc[g][i][e], f);
+              acc[g][i][2 + e] = __fmul_rn(acc[g][i][2 + e], f);
+            }
+            m[g][e] = m2;
+            mw[g][e] = mw2;
+          }
         }
-      if (__any_sync(0xffffffffu, __fsub_rn(zt, m) > 64.0f || __fsub_rn(ut, mw) > 15.0f)) {
+      }
+      uint32_t pb[NC][2];
 #pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-          zt = fmaxf(zt, __shfl_xor_sync(0xffffffffu, zt, d));
-          ut = fmaxf(ut, __shfl_xor_sync(0xffffffffu, ut, d));
+      for (int g = 0; g < NC; ++g)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float w0 = ex2(we[g][t][0]), w1 = ex2(we[g][t][1]);
+          uint32_t hi, lo;
+          split2(w0, w1, hi, lo);
+          pb[g][t] = transpose8(low ? lo : hi);
+          upk2(add2(pk2(l[g][0], l[g][1]), pk2(ex2(pe[g][t][0]), ex2(pe[g][t][1]))), l[g][0], l[g][1]);
+          upk2(add2(pk2(wsum[g][0], wsum[g][1]), pk2(w0, w1)), wsum[g][0], wsum[g][1]);
         }
-        const float m2 = fmaxf(m, zt), mw2 = fmaxf(mw, __fsub_rn(ut, 7.0f));
-        const float f = ex2(__fsub_rn(mw, mw2));
-        l = __fmul_rn(l, ex2(__fsub_rn(m, m2)));
-        wsum = __fmul_rn(wsum, f);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][e] = __fmul_rn(acc[i][e], f);
-        m = m2;
-        mw = mw2;
-      }
-      uint32_t pa[4];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const float w0 = ex2(__fsub_rn(u[nt][0], mw)), w1 = ex2(__fsub_rn(u[nt][1], mw));
-        l = __fadd_rn(l, __fadd_rn(ex2(__fsub_rn(z[nt][0], m)), ex2(__fsub_rn(z[nt][1], m))));
-        wsum = __fadd_rn(wsum, __fadd_rn(w0, w1));
-        split2(w0, w1, pa[2 * nt], pa[2 * nt + 1]);
-      }
-      // V: lane (n8, c4) holds the 16 dimensions of chunk n8 of token pairs c4 and 4 + c4
+      // values: lane (n8, c4) holds the 16 dimensions of chunk n8 of token pairs c4 and 4 + c4
       const uint4 v0 = lds128(U + ld_v), v1 = lds128(U + ld_v + 512);
       const uint32_t a0[2] = {v0.x, v0.y}, b0[2] = {v0.z, v0.w}, a1[2] = {v1.x, v1.y}, b1[2] = {v1.z, v1.w};
 #pragma unroll
@@ -466,37 +550,47 @@ __global__ void __launch_bounds__(kAttnThreads, 3) kv4_attn_kernel(Kv4AttnArgs a
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           uint32_t p0[4], p1[4];
-          unpack_pairs(__byte_perm(a0[w], b0[w], hf ? 0x7632 : 0x5410), p0);
-          unpack_pairs(__byte_perm(a1[w], b1[w], hf ? 0x7632 : 0x5410), p1);
+          unpack_pairs(__byte_perm(a0[w], b0[w], hf ? 0x7632 : 0x5410), magic, p0);
+          unpack_pairs(__byte_perm(a1[w], b1[w], hf ? 0x7632 : 0x5410), magic, p1);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma16816(acc[8 * w + 4 * hf + i], pa, p0[i], p1[i]);
+          for (int g = 0; g < NC; ++g) {
+            mma16816(acc[g][4 * w + 2 * hf], p0[0], p0[1], p1[0], p1[1], pb[g][0], pb[g][1]);
+            mma16816(acc[g][4 * w + 2 * hf + 1], p0[2], p0[3], p1[2], p1[3], pb[g][0], pb[g][1]);
+          }
         }
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    // ---- the block's sums: l and the weights' sum over the row's four lanes, then the four warps
-#pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-      l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, d));
-      wsum = __fadd_rn(wsum, __shfl_xor_sync(0xffffffffu, wsum, d));
-    }
+    // ---- the block's sums: l and the weights' sum over a row's lanes, then the four warps
     __syncthreads();                             // every warp's ring is free
     float *const s_acc = reinterpret_cast<float *>(s_mem);
-    const float half = __fmul_rn(wsum, 0.5f);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float *dst = s_acc + (warp * kRowTile + n8) * kTile + 16 * (2 * c4 + e);
+    for (int g = 0; g < NC; ++g) {
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        float4 v;
-        v.x = __fadd_rn(__fmaf_rn(acc[i][2 + e], kInvLoScale, acc[i][e]), half);
-        v.y = __fadd_rn(__fmaf_rn(acc[i + 1][2 + e], kInvLoScale, acc[i + 1][e]), half);
-        v.z = __fadd_rn(__fmaf_rn(acc[i + 2][2 + e], kInvLoScale, acc[i + 2][e]), half);
-        v.w = __fadd_rn(__fmaf_rn(acc[i + 3][2 + e], kInvLoScale, acc[i + 3][e]), half);
-        *reinterpret_cast<float4 *>(dst + i) = v;
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          l[g][e] = __fadd_rn(l[g][e], __shfl_xor_sync(0xffffffffu, l[g][e], d));
+          wsum[g][e] = __fadd_rn(wsum[g][e], __shfl_xor_sync(0xffffffffu, wsum[g][e], d));
+        }
+        // dimensions 16 n8 .. + 15 of row e: both lanes of a (high, low) pair form the sums, the
+        // high one stores row e0, the low one row e0 + 1
+        float *dst = s_acc + (warp * kRows + 4 * g + e0 + e) * kTile + 16 * n8;
+        const float half = __fmul_rn(wsum[g][e], 0.5f);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          float v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float own = acc[g][i + (k >> 1)][2 * (k & 1) + e];
+            const float other = __shfl_xor_sync(0xffffffffu, own, 2);
+            v[k] = __fadd_rn(__fmaf_rn(other, k_other, __fmul_rn(own, k_own)), half);
+          }
+          if (low == (e == 1)) *reinterpret_cast<float4 *>(dst + 2 * i) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        if (n8 == 0 && !low) s_stat[warp][4 * g + e0 + e] = RowStat{m[g][e], l[g][e], mw[g][e], 0.0f};
       }
     }
-    if (c4 == 0) s_stat[warp][n8] = RowStat{m, l, mw, 0.0f};
     __syncthreads();
     const bool whole = u_lo == 0 && u_hi == nu;
     if (!whole && u_lo == 0) {                   // begun here, ended by later blocks
@@ -504,7 +598,7 @@ __global__ void __launch_bounds__(kAttnThreads, 3) kv4_attn_kernel(Kv4AttnArgs a
       join_pair = pair;
       join_count = (int)((at + span1 - 1) / piece.size - blockIdx.x);
     }
-    if (tid < 8 * kRowTile) {
+    if (tid < 8 * kRows) {
       const int rr = tid >> 3, r = tid & 7, row = row0 + rr;
       float M = kNoMax, MW = kNoMax, L = 0.0f, x[16];
 #pragma unroll
@@ -518,32 +612,27 @@ __global__ void __launch_bounds__(kAttnThreads, 3) kv4_attn_kernel(Kv4AttnArgs a
       for (int w = 0; w < kWarps; ++w) {
         L = __fmaf_rn(s_stat[w][rr].l, ex2(__fsub_rn(s_stat[w][rr].m, M)), L);
         const float f = ex2(__fsub_rn(s_stat[w][rr].mw, MW));
-        const float *src = s_acc + (w * kRowTile + rr) * kTile + 16 * r;
+        const float *src = s_acc + (w * kRows + rr) * kTile + 16 * r;
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = __fmaf_rn(src[i], f, x[i]);
       }
       if (whole) {
         const bool live = row < a.R;
-        const float f = ex2(__fmul_rn(__fsub_rn(MW, M), 0.5f));
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          x[i] = L == 0.0f ? 0.0f : __fmul_rn(__fmul_rn(__fdiv_rn(x[i], L), f), f);
+        normalize(x, M, MW, L);
         const int j = row / a.G, hq = h * a.G + row % a.G;
         finish_row(a, x, s_tr + rr * kTrTile, r, live, ((int64_t)b * a.q_len + j) * a.Hq + hq);
         if (live && r == 0) finish_stats(a, b, h, row, M, L);
       } else {
         const int64_t slot = 2 * (int64_t)blockIdx.x + (u_lo == 0 ? 1 : 0);
-        float4 *dst = reinterpret_cast<float4 *>(a.part + (slot * kRowTile + rr) * kTile + 16 * r);
+        float4 *dst = reinterpret_cast<float4 *>(a.part + (slot * kRows + rr) * kTile + 16 * r);
 #pragma unroll
         for (int c = 0; c < 4; ++c) dst[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
-        if (r == 0) reinterpret_cast<float4 *>(a.stat)[slot * kRowTile + rr] = make_float4(M, L, MW, 0.0f);
+        if (r == 0) reinterpret_cast<float4 *>(a.stat)[slot * kRows + rr] = make_float4(M, L, MW, 0.0f);
       }
     }
     __syncthreads();                             // the ring, the rows and the statistics are free
   }
-  if (tid == 0) {
-    reinterpret_cast<int4 *>(a.joins)[blockIdx.x] = make_int4(join_count, join_b, join_pair, 0);
-  }
+  if (tid == 0) reinterpret_cast<int4 *>(a.joins)[blockIdx.x] = make_int4(join_count, join_b, join_pair, 0);
   // rows of sequences without tokens, and lengths out of range
   for (int64_t i = (int64_t)blockIdx.x * (kAttnThreads / 8) + (tid >> 3); i < (int64_t)a.c.n_seqs * a.q_len * a.Hq;
        i += (int64_t)gridDim.x * (kAttnThreads / 8)) {
@@ -561,46 +650,63 @@ __global__ void __launch_bounds__(kAttnThreads, 3) kv4_attn_kernel(Kv4AttnArgs a
   }
 }
 
-// The sums of a (sequence, head, row tile) that several blocks share, joined
-// in block order: block i of this kernel joins what block i of the other began.
-__global__ void __launch_bounds__(8 * kRowTile) kv4_join_kernel(Kv4AttnArgs a) {
-  __shared__ __align__(16) float s_tr[kRowTile * kTrTile];
+// The sums of a (sequence, head, row tile) that several blocks share: block
+// (i, row) joins that row of what block i of the attention kernel began.  Each
+// of the four warps adds every fourth block's sums, in order, a lane four
+// dimensions; the four are added in order.
+constexpr int kJoinThreads = 128;
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, int rows) {
+  __shared__ __align__(16) float s_tr[4 * kTrTile];
+  __shared__ __align__(16) float s_x[kJoinThreads / 32][kTile];
+  __shared__ float s_l[kJoinThreads / 32];
   const int4 job = reinterpret_cast<const int4 *>(a.joins)[blockIdx.x];
-  if (job.x == 0) return;
-  const int tid = threadIdx.x, rr = tid >> 3, r = tid & 7;
-  const int b = job.y, h = job.z / a.row_tiles, row = (job.z % a.row_tiles) * kRowTile + rr;
+  const int rr = blockIdx.y, h = job.z / a.row_tiles, row = (job.z % a.row_tiles) * rows + rr;
+  if (job.x == 0 || row >= a.R) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float4 *stat = reinterpret_cast<const float4 *>(a.stat);
   const auto slot_of = [&](int i) { return 2 * ((int64_t)blockIdx.x + i) + (i == 0 ? 1 : 0); };
-  float M = kNoMax, MW = kNoMax, L = 0.0f, x[16];
-  for (int i = 0; i <= job.x; ++i) {
-    const float4 s = stat[slot_of(i) * kRowTile + rr];
+  float M = kNoMax, MW = kNoMax, L = 0.0f;
+  for (int i = lane; i <= job.x; i += 32) {
+    const float4 s = stat[slot_of(i) * rows + rr];
     M = fmaxf(M, s.x);
     MW = fmaxf(MW, s.z);
   }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = 0.0f;
-  for (int i = 0; i <= job.x; ++i) {
-    const float4 s = stat[slot_of(i) * kRowTile + rr];
+  for (int d = 16; d >= 1; d >>= 1) {
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    MW = fmaxf(MW, __shfl_xor_sync(0xffffffffu, MW, d));
+  }
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = warp; i <= job.x; i += kJoinThreads / 32) {
+    const float4 s = stat[slot_of(i) * rows + rr];
+    const float4 v = reinterpret_cast<const float4 *>(a.part + (slot_of(i) * rows + rr) * kTile)[lane];
     L = __fmaf_rn(s.y, ex2(__fsub_rn(s.x, M)), L);
     const float f = ex2(__fsub_rn(s.z, MW));
-    const float4 *src = reinterpret_cast<const float4 *>(a.part + (slot_of(i) * kRowTile + rr) * kTile + 16 * r);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float4 v = src[c];
-      x[4 * c] = __fmaf_rn(v.x, f, x[4 * c]);
-      x[4 * c + 1] = __fmaf_rn(v.y, f, x[4 * c + 1]);
-      x[4 * c + 2] = __fmaf_rn(v.z, f, x[4 * c + 2]);
-      x[4 * c + 3] = __fmaf_rn(v.w, f, x[4 * c + 3]);
-    }
+    x.x = __fmaf_rn(v.x, f, x.x);
+    x.y = __fmaf_rn(v.y, f, x.y);
+    x.z = __fmaf_rn(v.z, f, x.z);
+    x.w = __fmaf_rn(v.w, f, x.w);
   }
-  const float f = ex2(__fmul_rn(__fsub_rn(MW, M), 0.5f));
+  reinterpret_cast<float4 *>(s_x[warp])[lane] = x;
+  if (lane == 0) s_l[warp] = L;
+  __syncthreads();
+  if (warp != 0) return;
+  const int r = lane & 7;
+  float y[16];
+  L = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    x[i] = L == 0.0f ? 0.0f : __fmul_rn(__fmul_rn(__fdiv_rn(x[i], L), f), f);
-  const bool live = row < a.R;
+  for (int i = 0; i < 16; ++i) y[i] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    L = __fadd_rn(L, s_l[w]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = __fadd_rn(y[i], s_x[w][16 * r + i]);
+  }
+  normalize(y, M, MW, L);
   const int j = row / a.G, hq = h * a.G + row % a.G;
-  finish_row(a, x, s_tr + rr * kTrTile, r, live, ((int64_t)b * a.q_len + j) * a.Hq + hq);
-  if (live && r == 0) finish_stats(a, b, h, row, M, L);
+  finish_row(a, y, s_tr + (lane >> 3) * kTrTile, r, lane < 8, ((int64_t)job.y * a.q_len + j) * a.Hq + hq);
+  if (lane == 0) finish_stats(a, job.y, h, row, M, L);
 }
 
 // mass_out = mass_in + sum over the head's rows of 2^(z - log2 of the row's sum).
@@ -621,51 +727,58 @@ __global__ void __launch_bounds__(256) kv4_mass_kernel(Kv4AttnArgs a) {
 
 // Resident blocks of the attention kernel on the current device (asked once
 // per instance and device).
-template <bool CAP, bool MASS>
+template <int NC, bool CAP, bool MASS>
 int resident_blocks() {
   static int cache[64] = {};
   int dev = 0, sms = 0, per_sm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (cudaFuncSetAttribute(kv4_attn_kernel<CAP, MASS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kAttnSmem) != cudaSuccess)
+  if (cudaFuncSetAttribute(kv4_attn_kernel<NC, CAP, MASS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Shape<NC>::smem) != cudaSuccess)
     return 0;
-  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kv4_attn_kernel<CAP, MASS>, kAttnThreads, kAttnSmem);
+  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kv4_attn_kernel<NC, CAP, MASS>, kAttnThreads,
+                                                Shape<NC>::smem);
   const int n = sms * per_sm;
   if (dev >= 0 && dev < 64) cache[dev] = n;
   return n;
 }
 
-template <bool CAP, bool MASS>
+template <int NC, bool CAP, bool MASS>
 int launch_attn(const Kv4AttnArgs &a, cudaStream_t st) {
-  int grid = resident_blocks<CAP, MASS>();
+  int grid = resident_blocks<NC, CAP, MASS>();
   if (grid <= 0) return 1;
   if (grid > kKv4MaxBlocks) grid = kKv4MaxBlocks;
   // no more blocks than pieces of the longest batch the table allows
   const int64_t most = ((a.c.capacity() / kUnit + kSegmentCost) * a.c.n_seqs * a.c.n_kv * a.row_tiles +
                         kMinPiece - 1) / kMinPiece;
   if (most < grid) grid = (int)most;
-  kv4_attn_kernel<CAP, MASS><<<grid, kAttnThreads, kAttnSmem, st>>>(a);
+  kv4_attn_kernel<NC, CAP, MASS><<<grid, kAttnThreads, Shape<NC>::smem, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return 1;
-  kv4_join_kernel<<<grid, 8 * kRowTile, 0, st>>>(a);
+  kv4_join_kernel<<<dim3((unsigned)grid, Shape<NC>::rows), kJoinThreads, 0, st>>>(a, Shape<NC>::rows);
   return cudaGetLastError() == cudaSuccess ? 0 : 1;
 }
 
+template <int NC>
+int launch_rows(const Kv4AttnArgs &a, cudaStream_t st) {
+  const bool mass = a.mass_out != nullptr;
+  if (a.cap > 0.0f) return mass ? launch_attn<NC, true, true>(a, st) : launch_attn<NC, true, false>(a, st);
+  return mass ? launch_attn<NC, false, true>(a, st) : launch_attn<NC, false, false>(a, st);
+}
+
+int row_groups(int R) { return R <= 4 ? 1 : 2; }
+
 }  // namespace
 
-int kv4_row_tiles(int R) { return (R + kRowTile - 1) / kRowTile; }
-size_t kv4_part_bytes() { return (size_t)2 * kKv4MaxBlocks * kRowTile * kTile * sizeof(float); }
-size_t kv4_stat_bytes() { return (size_t)2 * kKv4MaxBlocks * kRowTile * sizeof(float4); }
+int kv4_row_tiles(int R) { return (R + 4 * row_groups(R) - 1) / (4 * row_groups(R)); }
+size_t kv4_part_bytes(int R) { return (size_t)2 * kKv4MaxBlocks * 4 * row_groups(R) * kTile * sizeof(float); }
+size_t kv4_stat_bytes(int R) { return (size_t)2 * kKv4MaxBlocks * 4 * row_groups(R) * sizeof(float4); }
 size_t kv4_join_bytes() { return (size_t)kKv4MaxBlocks * sizeof(int4); }
 
 int launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t st) {
-  const bool mass = a.mass_out != nullptr;
-  int rc;
-  if (a.cap > 0.0f) rc = mass ? launch_attn<true, true>(a, st) : launch_attn<true, false>(a, st);
-  else rc = mass ? launch_attn<false, true>(a, st) : launch_attn<false, false>(a, st);
+  const int rc = row_groups(a.R) == 1 ? launch_rows<1>(a, st) : launch_rows<2>(a, st);
   if (rc != 0) return rc;
-  if (mass && a.c.capacity() > 0) {
+  if (a.mass_out != nullptr && a.c.capacity() > 0) {
     kv4_mass_kernel<<<dim3((unsigned)((a.c.capacity() + 255) / 256), (unsigned)a.c.n_kv,
                            (unsigned)a.c.n_seqs), 256, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return 1;
