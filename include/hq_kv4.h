@@ -123,8 +123,7 @@ size_t hq_kv4_attention_workspace_bytes(const hq_kv4_cache *c, int q_len, int Hq
  *               sequence's length on are left as they were.
  *   d_ws        >= hq_kv4_attention_workspace_bytes(), 256-byte aligned; calls
  *               that may overlap need workspaces of their own
- * d_status is OR-ed with HQ_ERR_PAGE, and with HQ_ERR_TIMEOUT if a copy into
- * shared memory did not complete. */
+ * d_status is OR-ed with HQ_ERR_PAGE. */
 int hq_kv4_attention(const hq_kv4_cache *c, const int32_t *d_lengths, const void *d_q, int q_kind,
                      int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
                      int q_len, int Hq, float scale, float cap, void *d_out, int out_kind,

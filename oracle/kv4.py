@@ -136,17 +136,23 @@ def read32(pages, page, h, t, which, mask):
 
 def attention(pages, table, lengths, q, mask, scale, cap=0.0, mass=None):
     """q [B, q_len, Hq, 128] in 64 bits -> dict of out, lse, mass, and what the error bound
-    goes by: size [B, q_len, Hq, 128] = sum of p |V'| in the transformed domain, and
-    zeta [B, q_len, Hq] = |scale| |q| max |Khat|."""
+    goes by: size [B, q_len, Hq, 128] = sum of p |V'| in the transformed domain, zeta [B, q_len, Hq] =
+    |scale| |q| max |Khat|, and zeta_codes = |scale| |q| max of s max(|c|, 7.5 sqrt(128)), |c| of a
+    row's codes."""
     B, q_len, Hq, _ = q.shape
     nh = pages.shape[1]
     G = Hq // nh
     out, size = np.zeros(q.shape), np.zeros(q.shape)
     lse, zeta = np.full(q.shape[:3], -np.inf), np.zeros(q.shape[:3])
+    zeta_codes = np.zeros(q.shape[:3])
     add = np.zeros((B, nh, table.shape[1] * pages.shape[2] * UNIT))
     for b in range(B):
         n = int(lengths[b])
         K, V = (rotated(pages, table, b, n, w) for w in (0, 1))
+        codes = [raw_rows(pages, table[b, j], 0) for j in range(-(-n // (pages.shape[2] * UNIT)))]
+        S = np.concatenate([s * np.maximum(np.linalg.norm(c.astype(np.float64), axis=-1),
+                                           7.5 * np.sqrt(128.0)) for c, s in codes],
+                           1)[:, :n] if n else np.zeros((nh, 0))
         for j in range(q_len):
             m = n - q_len + j + 1
             if m <= 0:
@@ -163,10 +169,13 @@ def attention(pages, table, lengths, q, mask, scale, cap=0.0, mass=None):
                 out[b, j, hq] = back(p @ V[h, :m], mask)
                 size[b, j, hq] = p @ np.abs(V[h, :m])
                 lse[b, j, hq] = top + np.log(e.sum())
-                zeta[b, j, hq] = abs(scale) * np.linalg.norm(y) * np.linalg.norm(K[h, :m], axis=-1).max()
+                size_q = abs(scale) * np.linalg.norm(y)
+                zeta[b, j, hq] = size_q * np.linalg.norm(K[h, :m], axis=-1).max()
+                zeta_codes[b, j, hq] = size_q * S[h, :m].max()
                 add[b, h, :m] += p
     total = add if mass is None else add + mass
-    return dict(out=out, lse=lse, mass=total, added=add, size=size, zeta=zeta)
+    return dict(out=out, lse=lse, mass=total, added=add, size=size, zeta=zeta,
+                zeta_codes=zeta_codes)
 
 
 def keep(mass, n, budget, recent):

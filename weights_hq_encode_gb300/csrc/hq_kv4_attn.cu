@@ -18,27 +18,33 @@ namespace {
 
 constexpr float kInvRoot128 = 0.08838834764831845f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLoScale = 2048.0f, kInvLoScale = 0x1p-11f;
+constexpr float kLoScale = 2048.0f;
 constexpr float kNoMax = -3.0e38f;               // below every finite score
 
+// A stage of the ring is a tile of 32 tokens: two units.
+constexpr int kTileTokens = 2 * kUnit;
+constexpr int kStageBytes = 2 * kUnitBytes;
 constexpr int kWarps = 4;                        // warps of a block
 constexpr int kAttnThreads = 32 * kWarps;
-constexpr int kStages = 4;                       // units a warp has in its ring
-constexpr int kRingBytes = kWarps * kStages * kUnitBytes;
+constexpr int kStages = 3;                       // tiles a warp has in its ring
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+
 // NC column groups of 8: the high and the low parts of 4 query rows each
 template <int NC>
 struct Shape {
   static constexpr int rows = 4 * NC;            // query rows of a block
+  static constexpr int blocks = NC == 1 ? 4 : 2; // resident blocks a multiprocessor
   static constexpr int q_bytes = 8 * NC * 32 * 8;   // query fragments: 8 K steps, 8 bytes a lane
-  static constexpr int sum_bytes = kWarps * rows * kTile * 4;   // the warps' sums, in the ring's place
-  static constexpr int ring = kRingBytes > sum_bytes ? kRingBytes : sum_bytes;
-  static constexpr int smem = ring + q_bytes + rows * kTrTile * 4;
-  static constexpr int blocks = NC == 1 ? 4 : 3; // resident blocks a multiprocessor
+  static constexpr int smem = kRingBytes + q_bytes + rows * kTrTile * 4;
+  static_assert(kWarps * rows * kTile * 4 <= kRingBytes, "the warps' sums fit the ring");
 };
 
 // Work of one (sequence, head, row tile) beyond its units, in units: the
 // blocks split the batch into equal pieces of units + kSegmentCost.
-constexpr int kSegmentCost = 8, kMinPiece = 16;
+constexpr int kSegmentCost = 8, kMinPiece = 24;
+// A batch whose longest sequence is this short is not split inside sequences:
+// a join would take longer than the units it spreads.
+constexpr int kWholeSpan = 48;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -50,39 +56,44 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// The exponents under which a nibble becomes an fp16 value, in registers that
-// the compiler does not fill again at every use.
-struct Magic {
-  uint32_t low, high;       // 1024 (nibble in bits 0-3), 64 (bits 4-7), twice each
+// Codes as fp16 pairs.  A nibble in bits 0-3 of a half is the subnormal
+// c 2^-24, one in bits 4-7 is c 2^-20, both exact: the scores' products take
+// them as they are (the queries carry the factor 16 and the sum of -7.5).
+// Pair i is nibble i of the low and of the high half of x.
+__device__ __forceinline__ void code_pairs(uint32_t x, uint32_t p[4]) {
+  const uint32_t y = x >> 8;
+  p[0] = x & 0x000F000Fu;
+  p[1] = x & 0x00F000F0u;
+  p[2] = y & 0x000F000Fu;
+  p[3] = y & 0x00F000F0u;
+}
+// The same centred, (c - 7.5) 2^-9 exactly, in one fused multiply-add each:
+// the value side's sums run over many tokens, and a constant in them would
+// grow past what they are to hold.
+struct Centre {
+  uint32_t low, high;       // 2^15 and 2^11, twice each
 };
-__device__ __forceinline__ Magic make_magic() {
-  Magic g;
-  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(g.low));
-  asm volatile("mov.b32 %0, 0x54005400;" : "=r"(g.high));
+__device__ __forceinline__ Centre make_centre() {   // in registers that are not filled again at every use
+  Centre g;
+  asm volatile("mov.b32 %0, 0x78007800;" : "=r"(g.low));
+  asm volatile("mov.b32 %0, 0x68006800;" : "=r"(g.high));
   return g;
 }
-// (x & MASK) | bits as two fp16 values, less MINUS.
-template <uint32_t MASK, uint32_t MINUS>
-__device__ __forceinline__ uint32_t codes2(uint32_t x, uint32_t bits) {
+__device__ __forceinline__ uint32_t centred(uint32_t c, uint32_t factor) {
   uint32_t y;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "n"(MASK), "r"(bits));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(y), "r"(MINUS));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(c), "r"(factor), "r"(0xA380A380u));   // -7.5 2^-9
   return y;
 }
-// Four pairs of codes less 8 as fp16: pair i is nibble i of the low and of
-// the high half of x.  Under the exponents above a nibble is 1024 + c or
-// 64 + c exactly.
-__device__ __forceinline__ void unpack_pairs(uint32_t x, const Magic &g, uint32_t p[4]) {
-  const uint32_t y = x >> 8;
-  p[0] = codes2<0x000F000Fu, 0x64086408u>(x, g.low);    // 1032
-  p[1] = codes2<0x00F000F0u, 0x54805480u>(x, g.high);   // 72
-  p[2] = codes2<0x000F000Fu, 0x64086408u>(y, g.low);
-  p[3] = codes2<0x00F000F0u, 0x54805480u>(y, g.high);
+__device__ __forceinline__ void value_pairs(uint32_t x, const Centre &g, uint32_t p[4]) {
+  code_pairs(x, p);
+  p[0] = centred(p[0], g.low);
+  p[1] = centred(p[1], g.high);
+  p[2] = centred(p[2], g.low);
+  p[3] = centred(p[3], g.high);
 }
 __device__ __forceinline__ void mma16816(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -90,17 +101,9 @@ __device__ __forceinline__ void mma16816(float d[4], uint32_t a0, uint32_t a1, u
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
-__device__ __forceinline__ float lds_bf16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return __uint_as_float((uint32_t)v << 16);
+__device__ __forceinline__ uint4 read16(const unsigned char *p) { return *reinterpret_cast<const uint4 *>(p); }
+__device__ __forceinline__ float read_bf16(const unsigned char *p) {
+  return bf16_to_f32(*reinterpret_cast<const uint16_t *>(p));
 }
 // An 8 x 8 matrix of 16-bit values, two a lane, transposed over the warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -114,7 +117,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 __device__ __forceinline__ void split2(float lo, float hi, uint32_t &h, uint32_t &rest) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
   const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-  const float r0 = __fmul_rn(__fsub_rn(lo, f.x), kLoScale), r1 = __fmul_rn(__fsub_rn(hi, f.y), kLoScale);
+  float r0, r1;                                  // exact: 2^11 x - 2^11 h
+  upk2(fma2(pk2(f.x, f.y), pk2(-kLoScale, -kLoScale), mul2(pk2(lo, hi), pk2(kLoScale, kLoScale))), r0, r1);
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(rest) : "f"(r1), "f"(r0));
 }
 
@@ -180,25 +184,73 @@ __device__ __forceinline__ int64_t span_of(const Kv4AttnArgs &a, int b) {
   return nu == 0 ? 0 : (int64_t)a.c.n_kv * a.row_tiles * (nu + kSegmentCost);
 }
 
+// The walk over a block's piece, segment by segment: the units of one
+// (sequence, head, row tile) that lie in it.  Every warp walks alike.
+struct Segment {
+  int b, pair, u_lo, u_hi, nu;
+  int64_t at_end;           // where the pair ends in the laid-out batch
+};
+struct Walk {
+  int64_t cur, end, b_begin;
+  int b;
+  __device__ __forceinline__ bool next(const Kv4AttnArgs &a, Segment *s) {
+    while (cur < end) {
+      const int nu = units_of(a, b), span1 = nu + kSegmentCost;
+      const int64_t b_end = b_begin + (nu == 0 ? 0 : (int64_t)a.c.n_kv * a.row_tiles * span1);
+      if (cur >= b_end) {
+        ++b;
+        b_begin = b_end;
+        continue;
+      }
+      const int pair = (int)((cur - b_begin) / span1);       // head and row tile of sequence b
+      const int64_t at = b_begin + (int64_t)pair * span1;    // where the pair begins
+      s->b = b;
+      s->pair = pair;
+      s->nu = nu;
+      s->u_lo = (int)max((int64_t)0, cur - at - kSegmentCost);
+      s->u_hi = (int)min((int64_t)nu, end - at - kSegmentCost);
+      s->at_end = at + span1;
+      cur = min(at + span1, end);
+      if (s->u_lo < s->u_hi) return true;
+    }
+    return false;
+  }
+};
+
 __device__ Piece find_piece(const Kv4AttnArgs &a) {
   __shared__ int64_t s_sum[kWarps];
+  __shared__ int s_top[kWarps];
   __shared__ int64_t s_begin;
   __shared__ int s_b;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.c.n_seqs;
   Piece p;
   int64_t total = 0;
-  for (int b = tid; b < B; b += kAttnThreads) total += span_of(a, b);
+  int top = 0;                                   // the longest sequence's span
+  for (int b = tid; b < B; b += kAttnThreads) {
+    total += span_of(a, b);
+    top = max(top, units_of(a, b));
+  }
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-  if (lane == 0) s_sum[warp] = total;
+  for (int d = 16; d >= 1; d >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, d);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+  }
+  if (lane == 0) {
+    s_sum[warp] = total;
+    s_top[warp] = top;
+  }
   if (tid == 0) s_b = B;
   __syncthreads();
   total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += s_sum[w];
-  const int64_t even = (total + gridDim.x - 1) / gridDim.x;
-  p.size = even > kMinPiece ? even : kMinPiece;
+  for (int w = 0; w < kWarps; ++w) {
+    total += s_sum[w];
+    top = max(top, s_top[w]);
+  }
+  top += kSegmentCost;
+  const int64_t even = (total + gridDim.x - 1) / gridDim.x, least = top <= kWholeSpan ? top : kMinPiece;
+  p.size = even > least ? even : least;
   p.begin = (int64_t)blockIdx.x * p.size;
   p.end = p.begin + p.size < total ? p.begin + p.size : total;
   int64_t base = 0;
@@ -234,12 +286,11 @@ __device__ Piece find_piece(const Kv4AttnArgs &a) {
   return p;
 }
 
-// Each warp of a block takes every fourth unit of a segment (the units of one
-// sequence and head that fall into the block's piece) through a ring of its
-// own in shared memory, filled by asynchronous copies, and keeps its own sums;
-// the four are added at the segment's end.  A segment that is a whole
-// (sequence, head) is finished here, the others leave their sums for
-// kv4_join_kernel.
+// A block walks the segments of its piece.  Each of its warps takes every
+// fourth tile of 32 tokens through a ring of its own in shared memory, filled
+// by asynchronous copies, and keeps its own sums; at a segment's end the four
+// are added.  A segment that is a whole (sequence, head, row tile) is finished
+// here, the others leave their sums for kv4_join_kernel.
 //
 // The products run on mma.sync m16n8k16, tokens (scores) and dimensions
 // (values) as the 16 rows and query rows as the 8 columns: columns 0 .. 3 the
@@ -253,75 +304,67 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
   constexpr int kRows = Shape<NC>::rows;
   extern __shared__ __align__(128) unsigned char s_mem[];
   __shared__ RowStat s_stat[kWarps][kRows];
-  __shared__ float s_mul[kRows], s_half[kRows];  // multiplier of the scores, sum q' / 2
+  __shared__ float s_mul[kRows], s_init[kRows];  // multiplier of the scores, their start
   __shared__ int s_seen[kRows];                  // tokens seen
+  uint2 *const s_q = reinterpret_cast<uint2 *>(s_mem + kRingBytes);
+  float *const s_acc = reinterpret_cast<float *>(s_mem);   // in the ring's place
+  float *const s_tr = reinterpret_cast<float *>(s_mem + kRingBytes + Shape<NC>::q_bytes);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned char *const ring = s_mem + warp * kStages * kStageBytes;
+  const uint32_t ring_a = smem_addr(ring);
+  // copies: 16 bytes a lane; V's 16-byte chunks are permuted inside their
+  // 128-byte rows so that the reads of a warp touch all banks
+  const uint32_t cp_v = kUnitV + (lane >> 3) * 128 + (((lane & 7) ^ (2 * (lane >> 3))) * 16);
+  const Piece piece = find_piece(a);
+  Walk walk{piece.begin, piece.end, piece.b_begin, piece.b};
+  Segment seg;
   const int n8 = lane >> 2, c4 = lane & 3;       // fragment row group, and place in it
   const bool low = c4 >= 2;                      // this lane's columns are low parts
   const int e0 = 2 * (c4 & 1);                   // its rows of a column group: e0, e0 + 1
-  uint2 *const s_q = reinterpret_cast<uint2 *>(s_mem + Shape<NC>::ring);
-  float *const s_tr = reinterpret_cast<float *>(s_mem + Shape<NC>::ring + Shape<NC>::q_bytes);
-  const uint32_t ring_a = smem_addr(s_mem) + warp * kStages * kUnitBytes;
-  // copies: 16 bytes a lane and 512-byte quarter; V's chunks are permuted
-  // inside their 128-byte rows so that the reads below touch all banks
-  const uint32_t cp_k = lane * 16, cp_v = kUnitV + (lane >> 3) * 128 + (((lane & 7) ^ (2 * (lane >> 3))) * 16);
   const uint32_t ld_v = kUnitV + c4 * 128 + ((n8 ^ (2 * c4)) * 16);
-  const Magic magic = make_magic();
-  const float k_own = low ? kInvLoScale : 1.0f, k_other = low ? 1.0f : kInvLoScale;
-  const Piece piece = find_piece(a);
+  const Centre centre = make_centre();
+  const float k_own = low ? 0x1p9f : 0x1p20f, k_other = low ? 0x1p20f : 0x1p9f;
   int join_b = 0, join_count = 0, join_pair = 0;
-  int64_t cur = piece.begin;
-  int b = piece.b;
-  int64_t b_begin = piece.b_begin;
-  while (cur < piece.end) {                      // block-uniform throughout
-    const int nu = units_of(a, b), span1 = nu + kSegmentCost;
-    const int64_t b_end = b_begin + (nu == 0 ? 0 : (int64_t)a.c.n_kv * a.row_tiles * span1);
-    if (cur >= b_end) {
-      ++b;
-      b_begin = b_end;
-      continue;
-    }
-    const int pair = (int)((cur - b_begin) / span1);        // head and row tile of sequence b
-    const int64_t at = b_begin + (int64_t)pair * span1;     // where the pair begins
-    const int u_lo = (int)max((int64_t)0, cur - at - kSegmentCost);
-    const int u_hi = (int)min((int64_t)nu, piece.end - at - kSegmentCost);
-    cur = min(at + span1, piece.end);
-    if (u_lo >= u_hi) continue;
-    const int h = pair / a.row_tiles, row0 = (pair % a.row_tiles) * kRows;
+  while (walk.next(a, &seg)) {
+    const int h = seg.pair / a.row_tiles, row0 = (seg.pair % a.row_tiles) * kRows;
     bool bad_len;
-    const int len = kv4_length(a.c, a.lengths, b, &bad_len);
-
-    // ---- this warp's units u_lo + warp, u_lo + warp + 4, ..: the ring's first copies
-    const int mine = (u_hi - u_lo - warp + kWarps - 1) / kWarps;
-    int where_now = -1, where_next = -1;         // unit numbers in the pool of 32 of this warp's units
-    const auto look_up = [&](int first) {
-      const int i = first + lane;
-      if (i >= mine) return -1;
-      const int u = u_lo + warp + kWarps * i, pj = u / a.c.page_units;
-      const int page = __ldg(a.c.table + (int64_t)b * a.c.width + pj);
-      return page >= 0 && page < a.c.n_pages ? (page * a.c.n_kv + h) * a.c.page_units + u - pj * a.c.page_units
-                                             : -1;
-    };
-    int issued = 0, put = 0;                     // units asked for, and the stage of the next
-    uint32_t bad_stages = 0;                     // stages whose unit has no page
-    const auto issue = [&]() {                   // the next unit into its stage; one group, maybe empty
+    const int len = kv4_length(a.c, a.lengths, seg.b, &bad_len);
+    // ---- this warp's tiles warp, warp + 4, ..: the ring's first copies
+    const int mine = ((seg.u_hi - seg.u_lo + 1) / 2 - warp + kWarps - 1) / kWarps;
+    int unit[2] = {-1, -1};                      // unit numbers in the pool of 32 of this warp's tiles
+    int issued = 0, put = 0;                     // tiles asked for, and the stage of the next
+    uint32_t have = 0;                           // two bits a stage: its units were copied
+    const auto issue = [&]() {                   // the next tile into its stage; one group, maybe empty
       if (issued < mine) {
-        if ((issued & 31) == 0) {
-          where_now = issued == 0 ? look_up(0) : where_next;
-          where_next = look_up(issued + 32);
+        if ((issued & 31) == 0) {                // the next 32 tiles' pages, a tile a lane
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int u = seg.u_lo + 2 * (warp + kWarps * (issued + lane)) + k, pj = u / a.c.page_units;
+            unit[k] = -2;                        // behind the segment's end
+            if (u < seg.u_hi) {
+              const int page = __ldg(a.c.table + (int64_t)seg.b * a.c.width + pj);
+              unit[k] = page >= 0 && page < a.c.n_pages
+                            ? (page * a.c.n_kv + h) * a.c.page_units + u - pj * a.c.page_units
+                            : -1;
+            }
+          }
         }
-        const int unit = __shfl_sync(0xffffffffu, where_now, issued & 31);
-        bad_stages &= ~(1u << put);
-        if (unit >= 0) {
-          const unsigned char *src = a.c.pages + (int64_t)unit * kUnitBytes + lane * 16;
-          const uint32_t dst = ring_a + put * kUnitBytes;
-          cp_async16(dst + cp_k, src);
-          cp_async16(dst + cp_k + 512, src + 512);
-          cp_async16(dst + cp_v, src + kUnitV);
-          cp_async16(dst + cp_v + 512, src + kUnitV + 512);
-          if (lane < 4) cp_async16(dst + kUnitKs + lane * 16, src + kUnitKs);
-        } else {
-          bad_stages |= 1u << put;
+        have &= ~(3u << (2 * put));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int un = __shfl_sync(0xffffffffu, unit[k], issued & 31);
+          if (un >= 0) {
+            const unsigned char *src = a.c.pages + (int64_t)un * kUnitBytes + lane * 16;
+            const uint32_t dst = ring_a + put * kStageBytes + k * kUnitBytes;
+            cp_async16(dst + lane * 16, src);
+            cp_async16(dst + lane * 16 + 512, src + 512);
+            cp_async16(dst + cp_v, src + kUnitV);
+            cp_async16(dst + cp_v + 512, src + kUnitV + 512);
+            if (lane < 4) cp_async16(dst + kUnitKs + lane * 16, src + kUnitKs);
+            have |= 1u << (2 * put + k);
+          } else if (un == -1 && lane == 0) {
+            atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
+          }
         }
         ++issued;
         put = put == kStages - 1 ? 0 : put + 1;
@@ -330,7 +373,6 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue();
-
     // ---- the query rows: rotated, scaled by a power of two, split, as mma fragments
     if (tid < 8 * kRows) {
       const int rr = tid >> 3, r = tid & 7, row = row0 + rr;
@@ -338,7 +380,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
       const int j = live ? row / a.G : 0, hq = live ? h * a.G + row % a.G : 0;
       float x[16];
       if (live) {
-        const int64_t qa = b * a.q_seq + j * a.q_token + hq * a.q_head;
+        const int64_t qa = seg.b * a.q_seq + j * a.q_token + hq * a.q_head;
         if (a.kind == HQ_T_F32) load_q16<HQ_T_F32>(a, qa, r, x);
         else if (a.kind == HQ_T_F16) load_q16<HQ_T_F16>(a, qa, r, x);
         else load_q16<HQ_T_BF16>(a, qa, r, x);
@@ -361,9 +403,10 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
       }
-      const float sc = scale_of(top), inv = inv_scale_of(top);
+      const float sc = scale_of(fmaxf(top, 0x1p-100f)), inv = inv_scale_of(fmaxf(top, 0x1p-100f));
+      // dimensions whose codes are c 2^-24 (even nibbles) carry a factor of 16
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], sc);
+      for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], (i & 1) ? sc : __fmul_rn(sc, 16.0f));
       // lane r holds words 2 (r & 1), 2 (r & 1) + 1 of the 32 dimensions of place r / 2; row rr is
       // columns rr % 4 (high parts) and rr % 4 + 4 (low parts) of group rr / 4
 #pragma unroll
@@ -380,7 +423,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
       }
       if (r == 0) {
         s_mul[rr] = CAP ? __fmul_rn(__fdiv_rn(a.scale, a.cap), inv) : __fmul_rn(__fmul_rn(a.scale, kLog2e), inv);
-        s_half[rr] = __fmul_rn(__fmul_rn(sum, sc), 0.5f);
+        s_init[rr] = __fmul_rn(__fmul_rn(sum, sc), -7.5f * 0x1p-20f);
         s_seen[rr] = max(0, len - a.q_len + j + 1);
       }
     }
@@ -395,14 +438,13 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
 #pragma unroll
     for (int g = 0; g < NC; ++g) {
       zmul[g] = pk2(s_mul[4 * g + e0], s_mul[4 * g + e0 + 1]);
-      q0[g][0] = low ? 0.0f : s_half[4 * g + e0];
-      q0[g][1] = low ? 0.0f : s_half[4 * g + e0 + 1];
+      q0[g][0] = low ? 0.0f : s_init[4 * g + e0];
+      q0[g][1] = low ? 0.0f : s_init[4 * g + e0 + 1];
     }
     const int seen_all = len - a.q_len + row0 / a.G + 1;    // the least of any row here
     const float cap_l2 = CAP ? __fmul_rn(a.cap, kLog2e) : 0.0f;
 
-    // ---- the units
-    float acc[NC][8][4], l[NC][2], wsum[NC][2], m[NC][2], mw[NC][2];
+    float acc[NC][8][4], l[NC][2], m[NC][2], mw[NC][2];
 #pragma unroll
     for (int g = 0; g < NC; ++g) {
 #pragma unroll
@@ -411,72 +453,77 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
         for (int e = 0; e < 4; ++e) acc[g][i][e] = 0.0f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        l[g][e] = wsum[g][e] = 0.0f;
+        l[g][e] = 0.0f;
         m[g][e] = mw[g][e] = kNoMax;
       }
     }
-    int get = 0;                                 // stage of the next unit to use
-    int t0 = (u_lo + warp) * kUnit;
-    for (int it = 0; it < mine; ++it, t0 += kWarps * kUnit) {
+    // ---- the tiles
+    int get = 0;                                 // stage of the next tile to use
+    int t0 = (seg.u_lo + 2 * warp) * kUnit;
+    for (int i = 0; i < mine; ++i, t0 += kWarps * kTileTokens) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      __syncwarp();                              // unit `it` has come, and unit `it` - 1 is used up
+      __syncwarp();                              // tile i has come, and tile i - 1 is used up
       issue();
-      const uint32_t U = ring_a + get * kUnitBytes;
-      const bool bad = (bad_stages >> get) & 1u;
+      const unsigned char *const U = ring + get * kStageBytes;
+      const uint32_t got = (have >> (2 * get)) & 3u;
       get = get == kStages - 1 ? 0 : get + 1;
-      // scores: lane (n8, c4) gets tokens n8 and n8 + 8, columns 2 c4, 2 c4 + 1
-      float s[NC][4];
+      // scores: lane (n8, c4) gets tokens n8 and n8 + 8 of a unit, columns 2 c4, 2 c4 + 1
+      float z[2][NC][2][2], u[2][NC][2][2];      // [unit][group][token][row]
 #pragma unroll
-      for (int g = 0; g < NC; ++g) {
-        s[g][0] = s[g][2] = q0[g][0];
-        s[g][1] = s[g][3] = q0[g][1];
-      }
-      {
-        const uint4 k0 = lds128(U + cp_k), k1 = lds128(U + cp_k + 512);
+      for (int un = 0; un < 2; ++un) {
+        const unsigned char *const V = U + un * kUnitBytes;
+        float s[NC][4];
+#pragma unroll
+        for (int g = 0; g < NC; ++g) {
+          s[g][0] = s[g][2] = q0[g][0];
+          s[g][1] = s[g][3] = q0[g][1];
+        }
+        const uint4 k0 = read16(V + lane * 16), k1 = read16(V + lane * 16 + 512);
         const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t p0[4], p1[4];
-          unpack_pairs(w0[j], magic, p0);
-          unpack_pairs(w1[j], magic, p1);
+          code_pairs(w0[j], p0);
+          code_pairs(w1[j], p1);
 #pragma unroll
           for (int g = 0; g < NC; ++g) {
             mma16816(s[g], p0[0], p1[0], p0[1], p1[1], qb[2 * j][g].x, qb[2 * j][g].y);
             mma16816(s[g], p0[2], p1[2], p0[3], p1[3], qb[2 * j + 1][g].x, qb[2 * j + 1][g].y);
           }
         }
-      }
-      const float sk[2] = {lds_bf16(U + kUnitKs + 2 * n8), lds_bf16(U + kUnitKs + 2 * n8 + 16)};
-      const float ls[2] = {lg2(lds_bf16(U + kUnitVs + 2 * n8)), lg2(lds_bf16(U + kUnitVs + 2 * n8 + 16))};
-      float z[NC][2][2], u[NC][2][2];            // [group][token][row]
-#pragma unroll
-      for (int g = 0; g < NC; ++g)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float o0 = __shfl_xor_sync(0xffffffffu, s[g][2 * t], 2);
-          const float o1 = __shfl_xor_sync(0xffffffffu, s[g][2 * t + 1], 2);
-          const uint64_t d = fma2(pk2(o0, o1), pk2(k_other, k_other),
-                                  mul2(pk2(s[g][2 * t], s[g][2 * t + 1]), pk2(k_own, k_own)));
-          upk2(mul2(mul2(d, pk2(sk[t], sk[t])), zmul[g]), z[g][t][0], z[g][t][1]);
-          if (CAP) {                             // cap tanh(y) = cap (1 - 2 / (1 + e^2|y|)), y's sign
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float y = z[g][t][e], x = ex2(__fmul_rn(fabsf(y), 2.0f * kLog2e));
-              z[g][t][e] = copysignf(
-                  __fmul_rn(cap_l2, __fsub_rn(1.0f, __fdividef(2.0f, __fadd_rn(x, 1.0f)))), y);
-            }
-          }
-          upk2(add2(pk2(z[g][t][0], z[g][t][1]), pk2(ls[t], ls[t])), u[g][t][0], u[g][t][1]);
-        }
-      if (t0 + kUnit > seen_all || bad) {        // warp-uniform: some token is not seen by some row
+        const float sk[2] = {read_bf16(V + kUnitKs + 2 * n8), read_bf16(V + kUnitKs + 2 * n8 + 16)};
+        const float ls[2] = {lg2(read_bf16(V + kUnitVs + 2 * n8)), lg2(read_bf16(V + kUnitVs + 2 * n8 + 16))};
 #pragma unroll
         for (int g = 0; g < NC; ++g)
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < 2; ++t) {
+            const float o0 = __shfl_xor_sync(0xffffffffu, s[g][2 * t], 2);
+            const float o1 = __shfl_xor_sync(0xffffffffu, s[g][2 * t + 1], 2);
+            const uint64_t d = fma2(pk2(o0, o1), pk2(k_other, k_other),
+                                    mul2(pk2(s[g][2 * t], s[g][2 * t + 1]), pk2(k_own, k_own)));
+            upk2(mul2(mul2(d, pk2(sk[t], sk[t])), zmul[g]), z[un][g][t][0], z[un][g][t][1]);
+            if (CAP) {                           // cap tanh(y) = cap (1 - 2 / (1 + e^2|y|)), y's sign
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (bad || t0 + 8 * t + n8 >= s_seen[4 * g + e0 + e]) z[g][t][e] = u[g][t][e] = -INFINITY;
-        if (bad && lane == 0) atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
+              for (int e = 0; e < 2; ++e) {
+                const float y = z[un][g][t][e], x = ex2(__fmul_rn(fabsf(y), 2.0f * kLog2e));
+                z[un][g][t][e] = copysignf(
+                    __fmul_rn(cap_l2, __fsub_rn(1.0f, __fdividef(2.0f, __fadd_rn(x, 1.0f)))), y);
+              }
+            }
+            upk2(add2(pk2(z[un][g][t][0], z[un][g][t][1]), pk2(ls[t], ls[t])), u[un][g][t][0], u[un][g][t][1]);
+          }
+      }
+      if (t0 + kTileTokens > seen_all || got != 3u) {       // warp-uniform: not every row sees every token
+#pragma unroll
+        for (int un = 0; un < 2; ++un)
+#pragma unroll
+          for (int g = 0; g < NC; ++g)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (!((got >> un) & 1u) || t0 + kUnit * un + 8 * t + n8 >= s_seen[4 * g + e0 + e])
+                  z[un][g][t][e] = u[un][g][t][e] = -INFINITY;
       }
       if (MASS && !low) {
 #pragma unroll
@@ -485,32 +532,41 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
           for (int e = 0; e < 2; ++e) {
             const int row = row0 + 4 * g + e0 + e;
             if (row >= a.R) continue;
-            float *zrow = a.z + (((int64_t)b * a.c.n_kv + h) * a.R + row) * a.c.capacity() + t0 + n8;
-            zrow[0] = z[g][0][e];
-            zrow[8] = z[g][1][e];
+            float *zrow = a.z + (((int64_t)seg.b * a.c.n_kv + h) * a.R + row) * a.c.capacity() + t0 + n8;
+#pragma unroll
+            for (int un = 0; un < 2; ++un)
+              if (t0 + kUnit * un < seg.u_hi * kUnit) {
+                zrow[kUnit * un] = z[un][g][0][e];
+                zrow[kUnit * un + 8] = z[un][g][1][e];
+              }
           }
       }
       // p = 2^(z - m) stays below 2^64 and a weight w = 2^(z + log2 s - mw) below 2^15 without
-      // moving the references m and mw at every unit
-      float pe[NC][2][2], we[NC][2][2];
+      // moving the references m and mw at every tile
+      float pe[2][NC][2][2], we[2][NC][2][2];
 #pragma unroll
       for (int pass = 0; pass < 2; ++pass) {
         float pt = kNoMax, wt = kNoMax;
 #pragma unroll
-        for (int g = 0; g < NC; ++g)
+        for (int un = 0; un < 2; ++un)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            upk2(sub2(pk2(z[g][t][0], z[g][t][1]), pk2(m[g][0], m[g][1])), pe[g][t][0], pe[g][t][1]);
-            upk2(sub2(pk2(u[g][t][0], u[g][t][1]), pk2(mw[g][0], mw[g][1])), we[g][t][0], we[g][t][1]);
-            pt = fmaxf(pt, fmaxf(pe[g][t][0], pe[g][t][1]));
-            wt = fmaxf(wt, fmaxf(we[g][t][0], we[g][t][1]));
-          }
+          for (int g = 0; g < NC; ++g)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              upk2(sub2(pk2(z[un][g][t][0], z[un][g][t][1]), pk2(m[g][0], m[g][1])), pe[un][g][t][0],
+                   pe[un][g][t][1]);
+              upk2(sub2(pk2(u[un][g][t][0], u[un][g][t][1]), pk2(mw[g][0], mw[g][1])), we[un][g][t][0],
+                   we[un][g][t][1]);
+              pt = fmaxf(pt, fmaxf(pe[un][g][t][0], pe[un][g][t][1]));
+              wt = fmaxf(wt, fmaxf(we[un][g][t][0], we[un][g][t][1]));
+            }
         if (pass == 1 || !__any_sync(0xffffffffu, pt > 64.0f || wt > 15.0f)) break;
 #pragma unroll
         for (int g = 0; g < NC; ++g) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float zt = fmaxf(z[g][0][e], z[g][1][e]), ut = fmaxf(u[g][0][e], u[g][1][e]);
+            float zt = fmaxf(fmaxf(z[0][g][0][e], z[0][g][1][e]), fmaxf(z[1][g][0][e], z[1][g][1][e]));
+            float ut = fmaxf(fmaxf(u[0][g][0][e], u[0][g][1][e]), fmaxf(u[1][g][0][e], u[1][g][1][e]));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
               zt = fmaxf(zt, __shfl_xor_sync(0xffffffffu, zt, d));
@@ -519,84 +575,81 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
             const float m2 = fmaxf(m[g][e], zt), mw2 = fmaxf(mw[g][e], __fsub_rn(ut, 7.0f));
             const float f = ex2(__fsub_rn(mw[g][e], mw2));
             l[g][e] = __fmul_rn(l[g][e], ex2(__fsub_rn(m[g][e], m2)));
-            wsum[g][e] = __fmul_rn(wsum[g][e], f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              acc[g][i][e] = __fmul_rn(acc[g][i][e], f);
-              acc[g][i][2 + e] = __fmul_rn(acc[g][i][2 + e], f);
+            for (int k = 0; k < 8; ++k) {
+              acc[g][k][e] = __fmul_rn(acc[g][k][e], f);
+              acc[g][k][2 + e] = __fmul_rn(acc[g][k][2 + e], f);
             }
             m[g][e] = m2;
             mw[g][e] = mw2;
           }
         }
       }
-      uint32_t pb[NC][2];
 #pragma unroll
-      for (int g = 0; g < NC; ++g)
+      for (int un = 0; un < 2; ++un) {
+        uint32_t pb[NC][2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float w0 = ex2(we[g][t][0]), w1 = ex2(we[g][t][1]);
-          uint32_t hi, lo;
-          split2(w0, w1, hi, lo);
-          pb[g][t] = transpose8(low ? lo : hi);
-          upk2(add2(pk2(l[g][0], l[g][1]), pk2(ex2(pe[g][t][0]), ex2(pe[g][t][1]))), l[g][0], l[g][1]);
-          upk2(add2(pk2(wsum[g][0], wsum[g][1]), pk2(w0, w1)), wsum[g][0], wsum[g][1]);
-        }
-      // values: lane (n8, c4) holds the 16 dimensions of chunk n8 of token pairs c4 and 4 + c4
-      const uint4 v0 = lds128(U + ld_v), v1 = lds128(U + ld_v + 512);
-      const uint32_t a0[2] = {v0.x, v0.y}, b0[2] = {v0.z, v0.w}, a1[2] = {v1.x, v1.y}, b1[2] = {v1.z, v1.w};
+        for (int g = 0; g < NC; ++g)
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
+          for (int t = 0; t < 2; ++t) {
+            uint32_t hi, lo;
+            split2(ex2(we[un][g][t][0]), ex2(we[un][g][t][1]), hi, lo);
+            pb[g][t] = transpose8(low ? lo : hi);
+            upk2(add2(pk2(l[g][0], l[g][1]), pk2(ex2(pe[un][g][t][0]), ex2(pe[un][g][t][1]))), l[g][0], l[g][1]);
+          }
+        // values: lane (n8, c4) holds the 16 dimensions of chunk n8 of token pairs c4 and 4 + c4
+        const unsigned char *const V = U + un * kUnitBytes + ld_v;
+        const uint4 v0 = read16(V), v1 = read16(V + 512);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t p0[4], p1[4];
-          unpack_pairs(__byte_perm(a0[w], b0[w], hf ? 0x7632 : 0x5410), magic, p0);
-          unpack_pairs(__byte_perm(a1[w], b1[w], hf ? 0x7632 : 0x5410), magic, p1);
+        for (int w = 0; w < 2; ++w) {
 #pragma unroll
-          for (int g = 0; g < NC; ++g) {
-            mma16816(acc[g][4 * w + 2 * hf], p0[0], p0[1], p1[0], p1[1], pb[g][0], pb[g][1]);
-            mma16816(acc[g][4 * w + 2 * hf + 1], p0[2], p0[3], p1[2], p1[3], pb[g][0], pb[g][1]);
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t p0[4], p1[4];
+            const uint32_t pick = hf ? 0x7632u : 0x5410u;
+            value_pairs(__byte_perm(w ? v0.y : v0.x, w ? v0.w : v0.z, pick), centre, p0);
+            value_pairs(__byte_perm(w ? v1.y : v1.x, w ? v1.w : v1.z, pick), centre, p1);
+#pragma unroll
+            for (int g = 0; g < NC; ++g) {
+              mma16816(acc[g][4 * w + 2 * hf], p0[0], p0[1], p1[0], p1[1], pb[g][0], pb[g][1]);
+              mma16816(acc[g][4 * w + 2 * hf + 1], p0[2], p0[3], p1[2], p1[3], pb[g][0], pb[g][1]);
+            }
           }
         }
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    // ---- the block's sums: l and the weights' sum over a row's lanes, then the four warps
     __syncthreads();                             // every warp's ring is free
-    float *const s_acc = reinterpret_cast<float *>(s_mem);
+    // ---- the block's sums: l over a row's lanes, then the warps
 #pragma unroll
     for (int g = 0; g < NC; ++g) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          l[g][e] = __fadd_rn(l[g][e], __shfl_xor_sync(0xffffffffu, l[g][e], d));
-          wsum[g][e] = __fadd_rn(wsum[g][e], __shfl_xor_sync(0xffffffffu, wsum[g][e], d));
-        }
+        for (int d = 4; d < 32; d <<= 1) l[g][e] = __fadd_rn(l[g][e], __shfl_xor_sync(0xffffffffu, l[g][e], d));
         // dimensions 16 n8 .. + 15 of row e: both lanes of a (high, low) pair form the sums, the
-        // high one stores row e0, the low one row e0 + 1
+        // high one stores row e0, the low one row e0 + 1; acc is 2^-9 of them
         float *dst = s_acc + (warp * kRows + 4 * g + e0 + e) * kTile + 16 * n8;
-        const float half = __fmul_rn(wsum[g][e], 0.5f);
+        const float f_own = low ? 0.25f : 512.0f, f_other = low ? 512.0f : 0.25f;
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
+        for (int k = 0; k < 8; k += 2) {
           float v[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float own = acc[g][i + (k >> 1)][2 * (k & 1) + e];
+          for (int d = 0; d < 4; ++d) {
+            const float own = acc[g][k + (d >> 1)][2 * (d & 1) + e];
             const float other = __shfl_xor_sync(0xffffffffu, own, 2);
-            v[k] = __fadd_rn(__fmaf_rn(other, k_other, __fmul_rn(own, k_own)), half);
+            v[d] = __fmaf_rn(other, f_other, __fmul_rn(own, f_own));
           }
-          if (low == (e == 1)) *reinterpret_cast<float4 *>(dst + 2 * i) = make_float4(v[0], v[1], v[2], v[3]);
+          if (low == (e == 1)) *reinterpret_cast<float4 *>(dst + 2 * k) = make_float4(v[0], v[1], v[2], v[3]);
         }
         if (n8 == 0 && !low) s_stat[warp][4 * g + e0 + e] = RowStat{m[g][e], l[g][e], mw[g][e], 0.0f};
       }
     }
     __syncthreads();
-    const bool whole = u_lo == 0 && u_hi == nu;
-    if (!whole && u_lo == 0) {                   // begun here, ended by later blocks
-      join_b = b;
-      join_pair = pair;
-      join_count = (int)((at + span1 - 1) / piece.size - blockIdx.x);
+    const bool whole = seg.u_lo == 0 && seg.u_hi == seg.nu;
+    if (!whole && seg.u_lo == 0) {               // begun here, ended by later blocks
+      join_b = seg.b;
+      join_pair = seg.pair;
+      join_count = (int)((seg.at_end - 1) / piece.size - blockIdx.x);
     }
     if (tid < 8 * kRows) {
       const int rr = tid >> 3, r = tid & 7, row = row0 + rr;
@@ -607,35 +660,35 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
         MW = fmaxf(MW, s_stat[w][rr].mw);
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+      for (int k = 0; k < 16; ++k) x[k] = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         L = __fmaf_rn(s_stat[w][rr].l, ex2(__fsub_rn(s_stat[w][rr].m, M)), L);
         const float f = ex2(__fsub_rn(s_stat[w][rr].mw, MW));
         const float *src = s_acc + (w * kRows + rr) * kTile + 16 * r;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = __fmaf_rn(src[i], f, x[i]);
+        for (int k = 0; k < 16; ++k) x[k] = __fmaf_rn(src[k], f, x[k]);
       }
       if (whole) {
         const bool live = row < a.R;
         normalize(x, M, MW, L);
         const int j = row / a.G, hq = h * a.G + row % a.G;
-        finish_row(a, x, s_tr + rr * kTrTile, r, live, ((int64_t)b * a.q_len + j) * a.Hq + hq);
-        if (live && r == 0) finish_stats(a, b, h, row, M, L);
+        finish_row(a, x, s_tr + rr * kTrTile, r, live, ((int64_t)seg.b * a.q_len + j) * a.Hq + hq);
+        if (live && r == 0) finish_stats(a, seg.b, h, row, M, L);
       } else {
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (u_lo == 0 ? 1 : 0);
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (seg.u_lo == 0 ? 1 : 0);
         float4 *dst = reinterpret_cast<float4 *>(a.part + (slot * kRows + rr) * kTile + 16 * r);
 #pragma unroll
         for (int c = 0; c < 4; ++c) dst[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
         if (r == 0) reinterpret_cast<float4 *>(a.stat)[slot * kRows + rr] = make_float4(M, L, MW, 0.0f);
       }
     }
-    __syncthreads();                             // the ring, the rows and the statistics are free
+    __syncthreads();                             // the ring and the statistics are free
   }
   if (tid == 0) reinterpret_cast<int4 *>(a.joins)[blockIdx.x] = make_int4(join_count, join_b, join_pair, 0);
   // rows of sequences without tokens, and lengths out of range
-  for (int64_t i = (int64_t)blockIdx.x * (kAttnThreads / 8) + (tid >> 3); i < (int64_t)a.c.n_seqs * a.q_len * a.Hq;
-       i += (int64_t)gridDim.x * (kAttnThreads / 8)) {
+  for (int64_t i = (int64_t)blockIdx.x * (kWarps * 4) + (tid >> 3); i < (int64_t)a.c.n_seqs * a.q_len * a.Hq;
+       i += (int64_t)gridDim.x * (kWarps * 4)) {
     const int sb = (int)(i / ((int64_t)a.q_len * a.Hq));
     bool bad_len;
     const int len = kv4_length(a.c, a.lengths, sb, &bad_len);
