@@ -101,6 +101,25 @@ __device__ __forceinline__ void mma16816(float d[4], uint32_t a0, uint32_t a1, u
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// A unit's codes, if its number is one: 16 bytes a lane and 512-byte quarter.
+__device__ __forceinline__ void cp_async_codes(int unit, uint32_t k, uint32_t v, const void *src) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ge.s32 p, %0, 0;\n\t"
+      "@p cp.async.cg.shared.global [%1], [%3], 16;\n\t"
+      "@p cp.async.cg.shared.global [%1 + 512], [%3 + 512], 16;\n\t"
+      "@p cp.async.cg.shared.global [%2], [%3 + 1024], 16;\n\t"
+      "@p cp.async.cg.shared.global [%2 + 512], [%3 + 1536], 16;\n\t}" ::"r"(unit),
+      "r"(k), "r"(v), "l"(src)
+      : "memory");
+}
+// The same from the start (c0, c1) for both row halves.
+__device__ __forceinline__ void mma16816_from(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1, float c0, float c1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %10, %11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
 __device__ __forceinline__ uint4 read16(const unsigned char *p) { return *reinterpret_cast<const uint4 *>(p); }
 __device__ __forceinline__ float read_bf16(const unsigned char *p) {
   return bf16_to_f32(*reinterpret_cast<const uint16_t *>(p));
@@ -130,12 +149,11 @@ __device__ __forceinline__ void load_q16(const Kv4AttnArgs &a, int64_t at, int r
 // 16 lanes of one row out, D H x / sqrt(128) applied: the last step of every
 // row.  All 32 lanes of the warp must call it.
 __device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, float x[16], float *tile, int r,
-                                           bool live, int64_t o) {
+                                           uint32_t mw, bool live, int64_t o) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], kInvRoot128);
   fwht128_t8(x, tile, r);
   if (!live) return;
-  const uint32_t mw = __ldg(a.c.signs + (r >> 1)) >> (16 * (r & 1));
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(__float_as_uint(x[i]) ^ (((mw >> i) & 1u) << 31));
   if (a.out_kind == HQ_T_F32) store_row16<HQ_T_F32>(a.out, o * kTile, r, true, x);
@@ -144,7 +162,7 @@ __device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, float x[16], fl
 }
 
 // A row's sums over some of its tokens: l = sum 2^(z - m), and acc (kept
-// beside it) = sum 2^(z + log2 s - mw) (c - 7.5).
+// beside it) = sum 2^(z - mw) s (c - 7.5).
 struct RowStat {
   float m, l, mw, pad;
 };
@@ -152,8 +170,9 @@ struct RowStat {
 // acc / l at its own references: x 2^mw / (l 2^m), zeros where there is no weight.
 __device__ __forceinline__ void normalize(float x[16], float m, float mw, float l) {
   const float f = ex2(__fmul_rn(__fsub_rn(mw, m), 0.5f));   // in two steps, each within range
+  const float g = l == 0.0f ? 0.0f : __fmul_rn(__fdiv_rn(1.0f, l), f);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = l == 0.0f ? 0.0f : __fmul_rn(__fmul_rn(__fdiv_rn(x[i], l), f), f);
+  for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], g), f);
 }
 
 __device__ __forceinline__ void finish_stats(const Kv4AttnArgs &a, int b, int h, int row, float M, float L) {
@@ -161,6 +180,10 @@ __device__ __forceinline__ void finish_stats(const Kv4AttnArgs &a, int b, int h,
   const int j = row / a.G, hq = h * a.G + row % a.G;
   if (a.lse != nullptr) a.lse[((int64_t)b * a.q_len + j) * a.Hq + hq] = __fmul_rn(l2, kLn2);
   if (a.mass_out != nullptr) a.row_lse[((int64_t)b * a.c.n_kv + h) * a.R + row] = l2;
+}
+
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {   // both positive
+  return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
 // Where a block's piece of the batch begins, and the piece's length: the
@@ -202,7 +225,7 @@ struct Walk {
         b_begin = b_end;
         continue;
       }
-      const int pair = (int)((cur - b_begin) / span1);       // head and row tile of sequence b
+      const int pair = (int)divide(cur - b_begin, span1);       // head and row tile of sequence b
       const int64_t at = b_begin + (int64_t)pair * span1;    // where the pair begins
       s->b = b;
       s->pair = pair;
@@ -225,6 +248,26 @@ __device__ Piece find_piece(const Kv4AttnArgs &a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.c.n_seqs;
   Piece p;
+  if (B <= 32) {                                 // every warp by itself, a sequence a lane
+    const int64_t span = lane < B ? span_of(a, lane) : 0;
+    int top = lane < B ? units_of(a, lane) + kSegmentCost : 0;
+    int64_t incl = span;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
+    const int64_t even = divide(total + gridDim.x - 1, gridDim.x), least = top <= kWholeSpan ? top : kMinPiece;
+    p.size = even > least ? even : least;
+    p.begin = (int64_t)blockIdx.x * p.size;
+    p.end = p.begin + p.size < total ? p.begin + p.size : total;
+    p.b = __popc(__ballot_sync(0xffffffffu, incl <= p.begin));   // sequences that end before
+    if (p.b > 31) p.b = 31;
+    p.b_begin = __shfl_sync(0xffffffffu, incl - span, p.b);
+    return p;
+  }
   int64_t total = 0;
   int top = 0;                                   // the longest sequence's span
   for (int b = tid; b < B; b += kAttnThreads) {
@@ -249,7 +292,7 @@ __device__ Piece find_piece(const Kv4AttnArgs &a) {
     top = max(top, s_top[w]);
   }
   top += kSegmentCost;
-  const int64_t even = (total + gridDim.x - 1) / gridDim.x, least = top <= kWholeSpan ? top : kMinPiece;
+  const int64_t even = divide(total + gridDim.x - 1, gridDim.x), least = top <= kWholeSpan ? top : kMinPiece;
   p.size = even > least ? even : least;
   p.begin = (int64_t)blockIdx.x * p.size;
   p.end = p.begin + p.size < total ? p.begin + p.size : total;
@@ -315,6 +358,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
   // copies: 16 bytes a lane; V's 16-byte chunks are permuted inside their
   // 128-byte rows so that the reads of a warp touch all banks
   const uint32_t cp_v = kUnitV + (lane >> 3) * 128 + (((lane & 7) ^ (2 * (lane >> 3))) * 16);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t sign_bits = __ldg(a.c.signs + ((tid & 7) >> 1)) >> (16 * (tid & 1));
   const Piece piece = find_piece(a);
   Walk walk{piece.begin, piece.end, piece.b_begin, piece.b};
   Segment seg;
@@ -329,67 +374,66 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
     const int h = seg.pair / a.row_tiles, row0 = (seg.pair % a.row_tiles) * kRows;
     bool bad_len;
     const int len = kv4_length(a.c, a.lengths, seg.b, &bad_len);
-    // ---- this warp's tiles warp, warp + 4, ..: the ring's first copies
+    // ---- the query rows' loads, then this warp's first tiles (warp, warp + 4, ..) into its ring
+    const int rr = tid >> 3, r = tid & 7, row = row0 + rr;     // of the first 8 kRows threads
+    const bool live = rr < kRows && row < a.R;
+    const int row_j = live ? row / a.G : 0, row_hq = live ? h * a.G + row - row_j * a.G : 0;
+    float x[16];
+    if (live) {
+      const int64_t qa = seg.b * a.q_seq + row_j * a.q_token + row_hq * a.q_head;
+      if (a.kind == HQ_T_F32) load_q16<HQ_T_F32>(a, qa, r, x);
+      else if (a.kind == HQ_T_F16) load_q16<HQ_T_F16>(a, qa, r, x);
+      else load_q16<HQ_T_BF16>(a, qa, r, x);
+    }
     const int mine = ((seg.u_hi - seg.u_lo + 1) / 2 - warp + kWarps - 1) / kWarps;
     int unit[2] = {-1, -1};                      // unit numbers in the pool of 32 of this warp's tiles
-    int issued = 0, put = 0;                     // tiles asked for, and the stage of the next
-    uint32_t have = 0;                           // two bits a stage: its units were copied
-    const auto issue = [&]() {                   // the next tile into its stage; one group, maybe empty
+    int issued = 0;                              // tiles asked for
+    uint32_t put = 0;                            // byte offset of the next one's stage
+    const auto issue = [&]() -> uint32_t {       // the next tile into its stage; one group, maybe empty
+      uint32_t got = 0;                          // bit i: unit i has a page
       if (issued < mine) {
         if ((issued & 31) == 0) {                // the next 32 tiles' pages, a tile a lane
+          bool bad = false;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int u = seg.u_lo + 2 * (warp + kWarps * (issued + lane)) + k, pj = u / a.c.page_units;
-            unit[k] = -2;                        // behind the segment's end
+            unit[k] = -1;
             if (u < seg.u_hi) {
               const int page = __ldg(a.c.table + (int64_t)seg.b * a.c.width + pj);
-              unit[k] = page >= 0 && page < a.c.n_pages
-                            ? (page * a.c.n_kv + h) * a.c.page_units + u - pj * a.c.page_units
-                            : -1;
+              if (page >= 0 && page < a.c.n_pages)
+                unit[k] = (page * a.c.n_kv + h) * a.c.page_units + u - pj * a.c.page_units;
+              else bad = true;
             }
           }
+          if (bad) atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
         }
-        have &= ~(3u << (2 * put));
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int un = __shfl_sync(0xffffffffu, unit[k], issued & 31);
-          if (un >= 0) {
-            const unsigned char *src = a.c.pages + (int64_t)un * kUnitBytes + lane * 16;
-            const uint32_t dst = ring_a + put * kStageBytes + k * kUnitBytes;
-            cp_async16(dst + lane * 16, src);
-            cp_async16(dst + lane * 16 + 512, src + 512);
-            cp_async16(dst + cp_v, src + kUnitV);
-            cp_async16(dst + cp_v + 512, src + kUnitV + 512);
-            if (lane < 4) cp_async16(dst + kUnitKs + lane * 16, src + kUnitKs);
-            have |= 1u << (2 * put + k);
-          } else if (un == -1 && lane == 0) {
-            atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
-          }
-        }
+        const int ua = __shfl_sync(0xffffffffu, unit[0], issued & 31);
+        const int ub = __shfl_sync(0xffffffffu, unit[1], issued & 31);
+        const unsigned char *base = a.c.pages + lane * 16;
+        const uint32_t k = ring_a + put + lane * 16, v = ring_a + put + cp_v;
+        cp_async_codes(ua, k, v, base + (int64_t)ua * kUnitBytes);
+        cp_async_codes(ub, k + kUnitBytes, v + kUnitBytes, base + (int64_t)ub * kUnitBytes);
+        const int us = lane < 4 ? ua : ub;       // scales: four lanes a unit
+        if (lane < 8 && us >= 0)
+          cp_async16(ring_a + put + kUnitKs + lane * 16 + (lane < 4 ? 0 : kUnitBytes - 64),
+                     base + (int64_t)us * kUnitBytes + kUnitKs - (lane < 4 ? 0 : 64));
+        got = (ua >= 0 ? 1u : 0u) | (ub >= 0 ? 2u : 0u);
         ++issued;
-        put = put == kStages - 1 ? 0 : put + 1;
+        put += kStageBytes;
+        if (put == kStages * kStageBytes) put = 0;
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
+      return got;
     };
+    uint32_t have = 0;                           // two bits a tile in the ring, the oldest lowest
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue();
+    for (int i = 0; i < kStages - 1; ++i) have |= issue() << (2 * i);
     // ---- the query rows: rotated, scaled by a power of two, split, as mma fragments
     if (tid < 8 * kRows) {
-      const int rr = tid >> 3, r = tid & 7, row = row0 + rr;
-      const bool live = row < a.R;
-      const int j = live ? row / a.G : 0, hq = live ? h * a.G + row % a.G : 0;
-      float x[16];
-      if (live) {
-        const int64_t qa = seg.b * a.q_seq + j * a.q_token + hq * a.q_head;
-        if (a.kind == HQ_T_F32) load_q16<HQ_T_F32>(a, qa, r, x);
-        else if (a.kind == HQ_T_F16) load_q16<HQ_T_F16>(a, qa, r, x);
-        else load_q16<HQ_T_BF16>(a, qa, r, x);
-      }
-      const uint32_t mw = __ldg(a.c.signs + (r >> 1)) >> (16 * (r & 1));
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float v = live ? x[i] : 0.0f;
-        x[i] = __fmul_rn(__uint_as_float(__float_as_uint(v) ^ (((mw >> i) & 1u) << 31)), kInvRoot128);
+        x[i] = __fmul_rn(__uint_as_float(__float_as_uint(v) ^ (((sign_bits >> i) & 1u) << 31)), kInvRoot128);
       }
       fwht128_t8(x, s_tr + rr * kTrTile, r);
       float top = 0.0f, sum = 0.0f;
@@ -424,7 +468,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
       if (r == 0) {
         s_mul[rr] = CAP ? __fmul_rn(__fdiv_rn(a.scale, a.cap), inv) : __fmul_rn(__fmul_rn(a.scale, kLog2e), inv);
         s_init[rr] = __fmul_rn(__fmul_rn(sum, sc), -7.5f * 0x1p-20f);
-        s_seen[rr] = max(0, len - a.q_len + j + 1);
+        s_seen[rr] = max(0, len - a.q_len + row_j + 1);
       }
     }
     __syncthreads();
@@ -444,7 +488,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
     const int seen_all = len - a.q_len + row0 / a.G + 1;    // the least of any row here
     const float cap_l2 = CAP ? __fmul_rn(a.cap, kLog2e) : 0.0f;
 
-    float acc[NC][8][4], l[NC][2], m[NC][2], mw[NC][2];
+    // sums: l of 2^(z - m), acc of 2^(z - m) s (c - 7.5) 2^-9 f, f a power of two a row
+    float acc[NC][8][4], l[NC][2], m[NC][2], f[NC][2];
 #pragma unroll
     for (int g = 0; g < NC; ++g) {
 #pragma unroll
@@ -454,30 +499,28 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         l[g][e] = 0.0f;
-        m[g][e] = mw[g][e] = kNoMax;
+        m[g][e] = kNoMax;
+        f[g][e] = 1.0f;
       }
     }
     // ---- the tiles
-    int get = 0;                                 // stage of the next tile to use
+    uint32_t get = 0;                            // byte offset of the next tile's stage
     int t0 = (seg.u_lo + 2 * warp) * kUnit;
     for (int i = 0; i < mine; ++i, t0 += kWarps * kTileTokens) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();                              // tile i has come, and tile i - 1 is used up
-      issue();
-      const unsigned char *const U = ring + get * kStageBytes;
-      const uint32_t got = (have >> (2 * get)) & 3u;
-      get = get == kStages - 1 ? 0 : get + 1;
+      have |= issue() << (2 * (kStages - 1));
+      const unsigned char *const U = ring + get;
+      const uint32_t got = have & 3u;
+      have >>= 2;
+      get += kStageBytes;
+      if (get == kStages * kStageBytes) get = 0;
       // scores: lane (n8, c4) gets tokens n8 and n8 + 8 of a unit, columns 2 c4, 2 c4 + 1
-      float z[2][NC][2][2], u[2][NC][2][2];      // [unit][group][token][row]
+      float z[2][NC][2][2], sv[2][2];            // [unit][group][token][row], V's scales
 #pragma unroll
       for (int un = 0; un < 2; ++un) {
         const unsigned char *const V = U + un * kUnitBytes;
         float s[NC][4];
-#pragma unroll
-        for (int g = 0; g < NC; ++g) {
-          s[g][0] = s[g][2] = q0[g][0];
-          s[g][1] = s[g][3] = q0[g][1];
-        }
         const uint4 k0 = read16(V + lane * 16), k1 = read16(V + lane * 16 + 512);
         const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
@@ -487,52 +530,60 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
           code_pairs(w1[j], p1);
 #pragma unroll
           for (int g = 0; g < NC; ++g) {
-            mma16816(s[g], p0[0], p1[0], p0[1], p1[1], qb[2 * j][g].x, qb[2 * j][g].y);
+            if (j == 0)
+              mma16816_from(s[g], p0[0], p1[0], p0[1], p1[1], qb[0][g].x, qb[0][g].y, q0[g][0], q0[g][1]);
+            else
+              mma16816(s[g], p0[0], p1[0], p0[1], p1[1], qb[2 * j][g].x, qb[2 * j][g].y);
             mma16816(s[g], p0[2], p1[2], p0[3], p1[3], qb[2 * j + 1][g].x, qb[2 * j + 1][g].y);
           }
         }
         const float sk[2] = {read_bf16(V + kUnitKs + 2 * n8), read_bf16(V + kUnitKs + 2 * n8 + 16)};
-        const float ls[2] = {lg2(read_bf16(V + kUnitVs + 2 * n8)), lg2(read_bf16(V + kUnitVs + 2 * n8 + 16))};
+        sv[un][0] = read_bf16(V + kUnitVs + 2 * n8);
+        sv[un][1] = read_bf16(V + kUnitVs + 2 * n8 + 16);
 #pragma unroll
         for (int g = 0; g < NC; ++g)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const float o0 = __shfl_xor_sync(0xffffffffu, s[g][2 * t], 2);
             const float o1 = __shfl_xor_sync(0xffffffffu, s[g][2 * t + 1], 2);
+            // powers of two: both lanes of a (high, low) pair get the same sum, bit for bit, as their
+            // two parts of one weight have to add up
             const uint64_t d = fma2(pk2(o0, o1), pk2(k_other, k_other),
                                     mul2(pk2(s[g][2 * t], s[g][2 * t + 1]), pk2(k_own, k_own)));
             upk2(mul2(mul2(d, pk2(sk[t], sk[t])), zmul[g]), z[un][g][t][0], z[un][g][t][1]);
             if (CAP) {                           // cap tanh(y) = cap (1 - 2 / (1 + e^2|y|)), y's sign
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float y = z[un][g][t][e], x = ex2(__fmul_rn(fabsf(y), 2.0f * kLog2e));
+                const float y = z[un][g][t][e], ey = ex2(__fmul_rn(fabsf(y), 2.0f * kLog2e));
                 z[un][g][t][e] = copysignf(
-                    __fmul_rn(cap_l2, __fsub_rn(1.0f, __fdividef(2.0f, __fadd_rn(x, 1.0f)))), y);
+                    __fmul_rn(cap_l2, __fsub_rn(1.0f, __fdividef(2.0f, __fadd_rn(ey, 1.0f)))), y);
               }
             }
-            upk2(add2(pk2(z[un][g][t][0], z[un][g][t][1]), pk2(ls[t], ls[t])), u[un][g][t][0], u[un][g][t][1]);
           }
       }
       if (t0 + kTileTokens > seen_all || got != 3u) {       // warp-uniform: not every row sees every token
 #pragma unroll
         for (int un = 0; un < 2; ++un)
 #pragma unroll
-          for (int g = 0; g < NC; ++g)
+          for (int t = 0; t < 2; ++t) {
+            const int at = t0 + kUnit * un + 8 * t + n8;
+            const bool none = !((got >> un) & 1u) || at >= len;
+            if (none) sv[un][t] = 0.0f;          // what lies there is no scale
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int g = 0; g < NC; ++g)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                if (!((got >> un) & 1u) || t0 + kUnit * un + 8 * t + n8 >= s_seen[4 * g + e0 + e])
-                  z[un][g][t][e] = u[un][g][t][e] = -INFINITY;
+                if (none || at >= s_seen[4 * g + e0 + e]) z[un][g][t][e] = -INFINITY;
+          }
       }
       if (MASS && !low) {
 #pragma unroll
         for (int g = 0; g < NC; ++g)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int row = row0 + 4 * g + e0 + e;
-            if (row >= a.R) continue;
-            float *zrow = a.z + (((int64_t)seg.b * a.c.n_kv + h) * a.R + row) * a.c.capacity() + t0 + n8;
+            const int zr = row0 + 4 * g + e0 + e;
+            if (zr >= a.R) continue;
+            float *zrow = a.z + (((int64_t)seg.b * a.c.n_kv + h) * a.R + zr) * a.c.capacity() + t0 + n8;
 #pragma unroll
             for (int un = 0; un < 2; ++un)
               if (t0 + kUnit * un < seg.u_hi * kUnit) {
@@ -541,47 +592,53 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
               }
           }
       }
-      // p = 2^(z - m) stays below 2^64 and a weight w = 2^(z + log2 s - mw) below 2^15 without
-      // moving the references m and mw at every tile
-      float pe[2][NC][2][2], we[2][NC][2][2];
+      // The references m (a whole number) and f move only when a score is more than 4 above m, or a
+      // weight 2^(z - m) s f could pass 2^15: f holds the row's largest weight so far near 2^7.
+      float zt = kNoMax, ft = 0.0f;
 #pragma unroll
-      for (int pass = 0; pass < 2; ++pass) {
-        float pt = kNoMax, wt = kNoMax;
+      for (int g = 0; g < NC; ++g)
 #pragma unroll
-        for (int un = 0; un < 2; ++un)
-#pragma unroll
-          for (int g = 0; g < NC; ++g)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              upk2(sub2(pk2(z[un][g][t][0], z[un][g][t][1]), pk2(m[g][0], m[g][1])), pe[un][g][t][0],
-                   pe[un][g][t][1]);
-              upk2(sub2(pk2(u[un][g][t][0], u[un][g][t][1]), pk2(mw[g][0], mw[g][1])), we[un][g][t][0],
-                   we[un][g][t][1]);
-              pt = fmaxf(pt, fmaxf(pe[un][g][t][0], pe[un][g][t][1]));
-              wt = fmaxf(wt, fmaxf(we[un][g][t][0], we[un][g][t][1]));
-            }
-        if (pass == 1 || !__any_sync(0xffffffffu, pt > 64.0f || wt > 15.0f)) break;
+        for (int e = 0; e < 2; ++e) {
+          const float top = fmaxf(fmaxf(z[0][g][0][e], z[0][g][1][e]), fmaxf(z[1][g][0][e], z[1][g][1][e]));
+          zt = fmaxf(zt, __fsub_rn(top, m[g][e]));
+          ft = fmaxf(ft, f[g][e]);
+        }
+      const float st = fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[1][0], sv[1][1]));
+      if (__any_sync(0xffffffffu, zt > 4.0f || __fmul_rn(st, ft) > 2048.0f)) {
+        const float ls[2][2] = {{lg2(sv[0][0]), lg2(sv[0][1])}, {lg2(sv[1][0]), lg2(sv[1][1])}};
 #pragma unroll
         for (int g = 0; g < NC; ++g) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float zt = fmaxf(fmaxf(z[0][g][0][e], z[0][g][1][e]), fmaxf(z[1][g][0][e], z[1][g][1][e]));
-            float ut = fmaxf(fmaxf(u[0][g][0][e], u[0][g][1][e]), fmaxf(u[1][g][0][e], u[1][g][1][e]));
+            float mt = kNoMax, ut = kNoMax;
+#pragma unroll
+            for (int un = 0; un < 2; ++un)
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                mt = fmaxf(mt, z[un][g][t][e]);
+                ut = fmaxf(ut, __fadd_rn(z[un][g][t][e], ls[un][t]));
+              }
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
-              zt = fmaxf(zt, __shfl_xor_sync(0xffffffffu, zt, d));
+              mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, d));
               ut = fmaxf(ut, __shfl_xor_sync(0xffffffffu, ut, d));
             }
-            const float m2 = fmaxf(m[g][e], zt), mw2 = fmaxf(mw[g][e], __fsub_rn(ut, 7.0f));
-            const float f = ex2(__fsub_rn(mw[g][e], mw2));
-            l[g][e] = __fmul_rn(l[g][e], ex2(__fsub_rn(m[g][e], m2)));
+            // log2 f = 7 + m - the largest z + log2 s, that one rounded up
+            const float lf = (float)((int)(__float_as_uint(f[g][e]) >> 23) - 127);
+            const float m2 = fmaxf(m[g][e], ceilf(mt));
+            const float u2 = fmaxf(__fadd_rn(__fsub_rn(m[g][e], lf), 7.0f), ceilf(ut));
+            const float l2 = fminf(fmaxf(__fadd_rn(__fsub_rn(m2, u2), 7.0f), -120.0f), 120.0f);
+            const float f2 = __uint_as_float((uint32_t)((int)l2 + 127) << 23);
+            const float down = ex2(__fsub_rn(m[g][e], m2));
+            const float by = ex2(__fadd_rn(__fsub_rn(m[g][e], m2), __fsub_rn(l2, lf)));
+            l[g][e] = __fmul_rn(l[g][e], down);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              acc[g][k][e] = __fmul_rn(acc[g][k][e], f);
-              acc[g][k][2 + e] = __fmul_rn(acc[g][k][2 + e], f);
+              acc[g][k][e] = __fmul_rn(acc[g][k][e], by);
+              acc[g][k][2 + e] = __fmul_rn(acc[g][k][2 + e], by);
             }
             m[g][e] = m2;
-            mw[g][e] = mw2;
+            f[g][e] = f2;
           }
         }
       }
@@ -592,10 +649,14 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
         for (int g = 0; g < NC; ++g)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
+            float p0, p1, w0, w1;
+            upk2(sub2(pk2(z[un][g][t][0], z[un][g][t][1]), pk2(m[g][0], m[g][1])), p0, p1);
+            const uint64_t p = pk2(ex2(p0), ex2(p1));
+            upk2(add2(pk2(l[g][0], l[g][1]), p), l[g][0], l[g][1]);
+            upk2(mul2(mul2(p, pk2(sv[un][t], sv[un][t])), pk2(f[g][0], f[g][1])), w0, w1);
             uint32_t hi, lo;
-            split2(ex2(we[un][g][t][0]), ex2(we[un][g][t][1]), hi, lo);
+            split2(w0, w1, hi, lo);
             pb[g][t] = transpose8(low ? lo : hi);
-            upk2(add2(pk2(l[g][0], l[g][1]), pk2(ex2(pe[un][g][t][0]), ex2(pe[un][g][t][1]))), l[g][0], l[g][1]);
           }
         // values: lane (n8, c4) holds the 16 dimensions of chunk n8 of token pairs c4 and 4 + c4
         const unsigned char *const V = U + un * kUnitBytes + ld_v;
@@ -641,7 +702,9 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
           }
           if (low == (e == 1)) *reinterpret_cast<float4 *>(dst + 2 * k) = make_float4(v[0], v[1], v[2], v[3]);
         }
-        if (n8 == 0 && !low) s_stat[warp][4 * g + e0 + e] = RowStat{m[g][e], l[g][e], mw[g][e], 0.0f};
+        if (n8 == 0 && !low)
+          s_stat[warp][4 * g + e0 + e] =
+              RowStat{m[g][e], l[g][e], __fsub_rn(m[g][e], (float)((int)(__float_as_uint(f[g][e]) >> 23) - 127)), 0.0f};
       }
     }
     __syncthreads();
@@ -649,11 +712,10 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
     if (!whole && seg.u_lo == 0) {               // begun here, ended by later blocks
       join_b = seg.b;
       join_pair = seg.pair;
-      join_count = (int)((seg.at_end - 1) / piece.size - blockIdx.x);
+      join_count = (int)(divide(seg.at_end - 1, piece.size) - blockIdx.x);
     }
     if (tid < 8 * kRows) {
-      const int rr = tid >> 3, r = tid & 7, row = row0 + rr;
-      float M = kNoMax, MW = kNoMax, L = 0.0f, x[16];
+      float M = kNoMax, MW = kNoMax, L = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         M = fmaxf(M, s_stat[w][rr].m);
@@ -664,16 +726,21 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         L = __fmaf_rn(s_stat[w][rr].l, ex2(__fsub_rn(s_stat[w][rr].m, M)), L);
-        const float f = ex2(__fsub_rn(s_stat[w][rr].mw, MW));
-        const float *src = s_acc + (w * kRows + rr) * kTile + 16 * r;
+        const float by = ex2(__fsub_rn(s_stat[w][rr].mw, MW));
+        const float4 *src = reinterpret_cast<const float4 *>(s_acc + (w * kRows + rr) * kTile + 16 * r);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = __fmaf_rn(src[k], f, x[k]);
+        for (int k = 0; k < 4; ++k) {
+          const float4 v = src[k];
+          x[4 * k] = __fmaf_rn(v.x, by, x[4 * k]);
+          x[4 * k + 1] = __fmaf_rn(v.y, by, x[4 * k + 1]);
+          x[4 * k + 2] = __fmaf_rn(v.z, by, x[4 * k + 2]);
+          x[4 * k + 3] = __fmaf_rn(v.w, by, x[4 * k + 3]);
+        }
       }
       if (whole) {
-        const bool live = row < a.R;
         normalize(x, M, MW, L);
-        const int j = row / a.G, hq = h * a.G + row % a.G;
-        finish_row(a, x, s_tr + rr * kTrTile, r, live, ((int64_t)seg.b * a.q_len + j) * a.Hq + hq);
+        finish_row(a, x, s_tr + rr * kTrTile, r, sign_bits, live,
+                   ((int64_t)seg.b * a.q_len + row_j) * a.Hq + row_hq);
         if (live && r == 0) finish_stats(a, seg.b, h, row, M, L);
       } else {
         const int64_t slot = 2 * (int64_t)blockIdx.x + (seg.u_lo == 0 ? 1 : 0);
@@ -687,19 +754,20 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
   }
   if (tid == 0) reinterpret_cast<int4 *>(a.joins)[blockIdx.x] = make_int4(join_count, join_b, join_pair, 0);
   // rows of sequences without tokens, and lengths out of range
-  for (int64_t i = (int64_t)blockIdx.x * (kWarps * 4) + (tid >> 3); i < (int64_t)a.c.n_seqs * a.q_len * a.Hq;
-       i += (int64_t)gridDim.x * (kWarps * 4)) {
-    const int sb = (int)(i / ((int64_t)a.q_len * a.Hq));
+  for (int sb = blockIdx.x; sb < a.c.n_seqs; sb += gridDim.x) {
     bool bad_len;
     const int len = kv4_length(a.c, a.lengths, sb, &bad_len);
-    if (bad_len && (tid & 7) == 0) atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
+    if (bad_len && tid == 0) atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
     if (len > 0) continue;
-    float x[16];
+    const int64_t first = (int64_t)sb * a.q_len * a.Hq;
+    for (int64_t i = tid >> 3; i < (int64_t)a.q_len * a.Hq; i += kAttnThreads / 8) {
+      float zero[16];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] = 0.0f;
-    if (a.out_kind == HQ_T_F32) store_row16<HQ_T_F32>(a.out, i * kTile, tid & 7, true, x);
-    else store_row16<HQ_T_BF16>(a.out, i * kTile, tid & 7, true, x);   // zeros are the same in fp16
-    if ((tid & 7) == 0 && a.lse != nullptr) a.lse[i] = -INFINITY;
+      for (int k = 0; k < 16; ++k) zero[k] = 0.0f;
+      if (a.out_kind == HQ_T_F32) store_row16<HQ_T_F32>(a.out, (first + i) * kTile, tid & 7, true, zero);
+      else store_row16<HQ_T_BF16>(a.out, (first + i) * kTile, tid & 7, true, zero);   // the same in fp16
+      if ((tid & 7) == 0 && a.lse != nullptr) a.lse[first + i] = -INFINITY;
+    }
   }
 }
 
@@ -712,6 +780,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, i
   __shared__ __align__(16) float s_tr[4 * kTrTile];
   __shared__ __align__(16) float s_x[kJoinThreads / 32][kTile];
   __shared__ float s_l[kJoinThreads / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");          // launched while that kernel runs
   const int4 job = reinterpret_cast<const int4 *>(a.joins)[blockIdx.x];
   const int rr = blockIdx.y, h = job.z / a.row_tiles, row = (job.z % a.row_tiles) * rows + rr;
   if (job.x == 0 || row >= a.R) return;
@@ -758,7 +827,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, i
   }
   normalize(y, M, MW, L);
   const int j = row / a.G, hq = h * a.G + row % a.G;
-  finish_row(a, y, s_tr + (lane >> 3) * kTrTile, r, lane < 8, ((int64_t)job.y * a.q_len + j) * a.Hq + hq);
+  const uint32_t sign_bits = __ldg(a.c.signs + (r >> 1)) >> (16 * (r & 1));
+  finish_row(a, y, s_tr + (lane >> 3) * kTrTile, r, sign_bits, lane < 8, ((int64_t)job.y * a.q_len + j) * a.Hq + hq);
   if (lane == 0) finish_stats(a, job.y, h, row, M, L);
 }
 
@@ -768,6 +838,7 @@ __global__ void __launch_bounds__(256) kv4_mass_kernel(Kv4AttnArgs a) {
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
   bool bad;
   const int len = kv4_length(a.c, a.lengths, b, &bad);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (t >= len) return;
   const int64_t head = (int64_t)b * a.c.n_kv + h, cap = a.c.capacity();
   float s = 0.0f;
@@ -797,19 +868,36 @@ int resident_blocks() {
   return n;
 }
 
+// A launch that may begin while the one before it in the stream still runs;
+// its kernel waits for that one's end before it reads what that one wrote.
+template <class... Params, class... Args>
+int launch_behind(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t st, Args... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...) == cudaSuccess ? 0 : 1;
+}
+
 template <int NC, bool CAP, bool MASS>
 int launch_attn(const Kv4AttnArgs &a, cudaStream_t st) {
   int grid = resident_blocks<NC, CAP, MASS>();
   if (grid <= 0) return 1;
   if (grid > kKv4MaxBlocks) grid = kKv4MaxBlocks;
   // no more blocks than pieces of the longest batch the table allows
-  const int64_t most = ((a.c.capacity() / kUnit + kSegmentCost) * a.c.n_seqs * a.c.n_kv * a.row_tiles +
-                        kMinPiece - 1) / kMinPiece;
+  const int64_t pairs = (int64_t)a.c.n_seqs * a.c.n_kv * a.row_tiles;
+  int64_t most = ((a.c.capacity() / kUnit + kSegmentCost) * pairs + kMinPiece - 1) / kMinPiece;
+  if (most < pairs) most = pairs;
   if (most < grid) grid = (int)most;
   kv4_attn_kernel<NC, CAP, MASS><<<grid, kAttnThreads, Shape<NC>::smem, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return 1;
-  kv4_join_kernel<<<dim3((unsigned)grid, Shape<NC>::rows), kJoinThreads, 0, st>>>(a, Shape<NC>::rows);
-  return cudaGetLastError() == cudaSuccess ? 0 : 1;
+  return launch_behind(kv4_join_kernel, dim3((unsigned)grid, Shape<NC>::rows), kJoinThreads, st, a,
+                       (int)Shape<NC>::rows);
 }
 
 template <int NC>
@@ -831,11 +919,9 @@ size_t kv4_join_bytes() { return (size_t)kKv4MaxBlocks * sizeof(int4); }
 int launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t st) {
   const int rc = row_groups(a.R) == 1 ? launch_rows<1>(a, st) : launch_rows<2>(a, st);
   if (rc != 0) return rc;
-  if (a.mass_out != nullptr && a.c.capacity() > 0) {
-    kv4_mass_kernel<<<dim3((unsigned)((a.c.capacity() + 255) / 256), (unsigned)a.c.n_kv,
-                           (unsigned)a.c.n_seqs), 256, 0, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return 1;
-  }
+  if (a.mass_out != nullptr && a.c.capacity() > 0)
+    return launch_behind(kv4_mass_kernel, dim3((unsigned)((a.c.capacity() + 255) / 256), (unsigned)a.c.n_kv,
+                                               (unsigned)a.c.n_seqs), 256, st, a);
   return 0;
 }
 
