@@ -138,13 +138,13 @@ def attention(pages, table, lengths, q, mask, scale, cap=0.0, mass=None):
     """q [B, q_len, Hq, 128] in 64 bits -> dict of out, lse, mass, and what the error bound
     goes by: size [B, q_len, Hq, 128] = sum of p |V'| in the transformed domain, zeta [B, q_len, Hq] =
     |scale| |q| max |Khat|, and zeta_codes = |scale| |q| max of s max(|c|, 7.5 sqrt(128)), |c| of a
-    row's codes."""
+    row's codes, and scales = sum of p s over V's scales."""
     B, q_len, Hq, _ = q.shape
     nh = pages.shape[1]
     G = Hq // nh
     out, size = np.zeros(q.shape), np.zeros(q.shape)
     lse, zeta = np.full(q.shape[:3], -np.inf), np.zeros(q.shape[:3])
-    zeta_codes = np.zeros(q.shape[:3])
+    zeta_codes, scales = np.zeros(q.shape[:3]), np.zeros(q.shape[:3])
     add = np.zeros((B, nh, table.shape[1] * pages.shape[2] * UNIT))
     for b in range(B):
         n = int(lengths[b])
@@ -153,6 +153,8 @@ def attention(pages, table, lengths, q, mask, scale, cap=0.0, mass=None):
         S = np.concatenate([s * np.maximum(np.linalg.norm(c.astype(np.float64), axis=-1),
                                            7.5 * np.sqrt(128.0)) for c, s in codes],
                            1)[:, :n] if n else np.zeros((nh, 0))
+        sv = [raw_rows(pages, table[b, j], 1)[1] for j in range(-(-n // (pages.shape[2] * UNIT)))]
+        sv = np.concatenate(sv, 1)[:, :n].astype(np.float64) if n else np.zeros((nh, 0))
         for j in range(q_len):
             m = n - q_len + j + 1
             if m <= 0:
@@ -168,6 +170,7 @@ def attention(pages, table, lengths, q, mask, scale, cap=0.0, mass=None):
                 p = e / e.sum()
                 out[b, j, hq] = back(p @ V[h, :m], mask)
                 size[b, j, hq] = p @ np.abs(V[h, :m])
+                scales[b, j, hq] = p @ sv[h, :m]
                 lse[b, j, hq] = top + np.log(e.sum())
                 size_q = abs(scale) * np.linalg.norm(y)
                 zeta[b, j, hq] = size_q * np.linalg.norm(K[h, :m], axis=-1).max()
@@ -175,7 +178,7 @@ def attention(pages, table, lengths, q, mask, scale, cap=0.0, mass=None):
                 add[b, h, :m] += p
     total = add if mass is None else add + mass
     return dict(out=out, lse=lse, mass=total, added=add, size=size, zeta=zeta,
-                zeta_codes=zeta_codes)
+                zeta_codes=zeta_codes, scales=scales)
 
 
 def keep(mass, n, budget, recent):

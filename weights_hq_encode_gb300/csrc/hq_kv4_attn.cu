@@ -33,7 +33,7 @@ constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 template <int NC>
 struct Shape {
   static constexpr int rows = 4 * NC;            // query rows of a block
-  static constexpr int blocks = NC == 1 ? 4 : 2; // resident blocks a multiprocessor
+  static constexpr int blocks = NC == 1 ? 3 : 2; // resident blocks a multiprocessor
   static constexpr int q_bytes = 8 * NC * 32 * 8;   // query fragments: 8 K steps, 8 bytes a lane
   static constexpr int smem = kRingBytes + q_bytes + rows * kTrTile * 4;
   static_assert(kWarps * rows * kTile * 4 <= kRingBytes, "the warps' sums fit the ring");
@@ -56,40 +56,31 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Codes as fp16 pairs.  A nibble in bits 0-3 of a half is the subnormal
-// c 2^-24, one in bits 4-7 is c 2^-20, both exact: the scores' products take
-// them as they are (the queries carry the factor 16 and the sum of -7.5).
-// Pair i is nibble i of the low and of the high half of x.
+// Codes as fp16 pairs.  The low bits of a half are a subnormal number of units
+// 2^-24, exact as an operand: pairs of a byte's low nibble, c_e, and of whole
+// bytes, c_e + 16 c_o, two instructions each instead of a mask, an exponent and a
+// subtraction for every pair.  The other side sorts them out: a score takes
+// q_e - q_o / 16 with c_e and q_o / 16 with the byte, a value's odd dimension is
+// (byte's sum - even sum) / 16.
+// Pairs i = 0, 1 come from bytes 0 and 2 of x, i = 2, 3 from bytes 1 and 3.
 __device__ __forceinline__ void code_pairs(uint32_t x, uint32_t p[4]) {
-  const uint32_t y = x >> 8;
   p[0] = x & 0x000F000Fu;
-  p[1] = x & 0x00F000F0u;
-  p[2] = y & 0x000F000Fu;
-  p[3] = y & 0x00F000F0u;
+  p[1] = x & 0x00FF00FFu;
+  p[3] = __byte_perm(x, 0u, 0x4341);
+  p[2] = p[3] & 0x000F000Fu;
 }
-// The same centred, (c - 7.5) 2^-9 exactly, in one fused multiply-add each:
-// the value side's sums run over many tokens, and a constant in them would
-// grow past what they are to hold.
-struct Centre {
-  uint32_t low, high;       // 2^15 and 2^11, twice each
-};
-__device__ __forceinline__ Centre make_centre() {   // in registers that are not filled again at every use
-  Centre g;
-  asm volatile("mov.b32 %0, 0x78007800;" : "=r"(g.low));
-  asm volatile("mov.b32 %0, 0x68006800;" : "=r"(g.high));
-  return g;
-}
-__device__ __forceinline__ uint32_t centred(uint32_t c, uint32_t factor) {
+// The same centred, in units of 2^-9: c_e - 7.5 and c_e + 16 c_o - 127.5, exactly.
+__device__ __forceinline__ uint32_t centred(uint32_t c, uint32_t factor, uint32_t minus) {
   uint32_t y;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(c), "r"(factor), "r"(0xA380A380u));   // -7.5 2^-9
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(c), "r"(factor), "r"(minus));
   return y;
 }
-__device__ __forceinline__ void value_pairs(uint32_t x, const Centre &g, uint32_t p[4]) {
+__device__ __forceinline__ void value_pairs(uint32_t x, uint32_t factor, uint32_t p[4]) {
   code_pairs(x, p);
-  p[0] = centred(p[0], g.low);
-  p[1] = centred(p[1], g.high);
-  p[2] = centred(p[2], g.low);
-  p[3] = centred(p[3], g.high);
+  p[0] = centred(p[0], factor, 0xA380A380u);
+  p[1] = centred(p[1], factor, 0xB3F8B3F8u);
+  p[2] = centred(p[2], factor, 0xA380A380u);
+  p[3] = centred(p[3], factor, 0xB3F8B3F8u);
 }
 __device__ __forceinline__ void mma16816(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -98,27 +89,35 @@ __device__ __forceinline__ void mma16816(float d[4], uint32_t a0, uint32_t a1, u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Copies of the stream: read once, so they go first when L2 needs room, and
+// the code, tables and queries of the next launches stay there.
+__device__ __forceinline__ uint64_t stream_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
+               : "memory");
 }
 // A unit's codes, if its number is one: 16 bytes a lane and 512-byte quarter.
-__device__ __forceinline__ void cp_async_codes(int unit, uint32_t k, uint32_t v, const void *src) {
+__device__ __forceinline__ void cp_async_codes(int unit, uint32_t k, uint32_t v, const void *src, uint64_t policy) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ge.s32 p, %0, 0;\n\t"
-      "@p cp.async.cg.shared.global [%1], [%3], 16;\n\t"
-      "@p cp.async.cg.shared.global [%1 + 512], [%3 + 512], 16;\n\t"
-      "@p cp.async.cg.shared.global [%2], [%3 + 1024], 16;\n\t"
-      "@p cp.async.cg.shared.global [%2 + 512], [%3 + 1536], 16;\n\t}" ::"r"(unit),
-      "r"(k), "r"(v), "l"(src)
+      "@p cp.async.cg.shared.global.L2::cache_hint [%1], [%3], 16, %4;\n\t"
+      "@p cp.async.cg.shared.global.L2::cache_hint [%1 + 512], [%3 + 512], 16, %4;\n\t"
+      "@p cp.async.cg.shared.global.L2::cache_hint [%2], [%3 + 1024], 16, %4;\n\t"
+      "@p cp.async.cg.shared.global.L2::cache_hint [%2 + 512], [%3 + 1536], 16, %4;\n\t}" ::"r"(unit),
+      "r"(k), "r"(v), "l"(src), "l"(policy)
       : "memory");
 }
-// The same from the start (c0, c1) for both row halves.
+// The same from the start c.
 __device__ __forceinline__ void mma16816_from(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1, float c0, float c1) {
+                                              uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%10, %11, %10, %11};"
+      "{%8, %9}, {%10, %11, %12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 __device__ __forceinline__ uint4 read16(const unsigned char *p) { return *reinterpret_cast<const uint4 *>(p); }
 __device__ __forceinline__ float read_bf16(const unsigned char *p) {
@@ -367,7 +366,9 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
   const bool low = c4 >= 2;                      // this lane's columns are low parts
   const int e0 = 2 * (c4 & 1);                   // its rows of a column group: e0, e0 + 1
   const uint32_t ld_v = kUnitV + c4 * 128 + ((n8 ^ (2 * c4)) * 16);
-  const Centre centre = make_centre();
+  const uint64_t policy = stream_policy();
+  uint32_t factor;                               // 2^15, twice
+  asm volatile("mov.b32 %0, 0x78007800;" : "=r"(factor));
   const float k_own = low ? 0x1p9f : 0x1p20f, k_other = low ? 0x1p20f : 0x1p9f;
   int join_b = 0, join_count = 0, join_pair = 0;
   while (walk.next(a, &seg)) {
@@ -411,12 +412,12 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
         const int ub = __shfl_sync(0xffffffffu, unit[1], issued & 31);
         const unsigned char *base = a.c.pages + lane * 16;
         const uint32_t k = ring_a + put + lane * 16, v = ring_a + put + cp_v;
-        cp_async_codes(ua, k, v, base + (int64_t)ua * kUnitBytes);
-        cp_async_codes(ub, k + kUnitBytes, v + kUnitBytes, base + (int64_t)ub * kUnitBytes);
+        cp_async_codes(ua, k, v, base + (int64_t)ua * kUnitBytes, policy);
+        cp_async_codes(ub, k + kUnitBytes, v + kUnitBytes, base + (int64_t)ub * kUnitBytes, policy);
         const int us = lane < 4 ? ua : ub;       // scales: four lanes a unit
         if (lane < 8 && us >= 0)
           cp_async16(ring_a + put + kUnitKs + lane * 16 + (lane < 4 ? 0 : kUnitBytes - 64),
-                     base + (int64_t)us * kUnitBytes + kUnitKs - (lane < 4 ? 0 : 64));
+                     base + (int64_t)us * kUnitBytes + kUnitKs - (lane < 4 ? 0 : 64), policy);
         got = (ua >= 0 ? 1u : 0u) | (ub >= 0 ? 2u : 0u);
         ++issued;
         put += kStageBytes;
@@ -448,9 +449,12 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
         sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
       }
       const float sc = scale_of(fmaxf(top, 0x1p-100f)), inv = inv_scale_of(fmaxf(top, 0x1p-100f));
-      // dimensions whose codes are c 2^-24 (even nibbles) carry a factor of 16
+      // 16 q_e - q_o beside an even dimension's code, q_o beside the byte of both
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], (i & 1) ? sc : __fmul_rn(sc, 16.0f));
+      for (int i = 0; i < 16; i += 2) {
+        x[i + 1] = __fmul_rn(x[i + 1], sc);
+        x[i] = __fmaf_rn(__fmul_rn(x[i], sc), 16.0f, -x[i + 1]);
+      }
       // lane r holds words 2 (r & 1), 2 (r & 1) + 1 of the 32 dimensions of place r / 2; row rr is
       // columns rr % 4 (high parts) and rr % 4 + 4 (low parts) of group rr / 4
 #pragma unroll
@@ -488,7 +492,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
     const int seen_all = len - a.q_len + row0 / a.G + 1;    // the least of any row here
     const float cap_l2 = CAP ? __fmul_rn(a.cap, kLog2e) : 0.0f;
 
-    // sums: l of 2^(z - m), acc of 2^(z - m) s (c - 7.5) 2^-9 f, f a power of two a row
+    // sums: l of 2^(z - m), acc of w (c - 7.5) 2^-24, w = 2^(z - m) s f, f a power of two a row;
+    // acc of odd dimensions with 16 times theirs and the even one's before them
     float acc[NC][8][4], l[NC][2], m[NC][2], f[NC][2];
 #pragma unroll
     for (int g = 0; g < NC; ++g) {
@@ -531,7 +536,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
 #pragma unroll
           for (int g = 0; g < NC; ++g) {
             if (j == 0)
-              mma16816_from(s[g], p0[0], p1[0], p0[1], p1[1], qb[0][g].x, qb[0][g].y, q0[g][0], q0[g][1]);
+              mma16816_from(s[g], p0[0], p1[0], p0[1], p1[1], qb[0][g].x, qb[0][g].y, q0[g][0], q0[g][1],
+                            q0[g][0], q0[g][1]);
             else
               mma16816(s[g], p0[0], p1[0], p0[1], p1[1], qb[2 * j][g].x, qb[2 * j][g].y);
             mma16816(s[g], p0[2], p1[2], p0[3], p1[3], qb[2 * j + 1][g].x, qb[2 * j + 1][g].y);
@@ -642,9 +648,9 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
           }
         }
       }
+      uint32_t pb[2][NC][2];
 #pragma unroll
-      for (int un = 0; un < 2; ++un) {
-        uint32_t pb[NC][2];
+      for (int un = 0; un < 2; ++un)
 #pragma unroll
         for (int g = 0; g < NC; ++g)
 #pragma unroll
@@ -656,25 +662,29 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
             upk2(mul2(mul2(p, pk2(sv[un][t], sv[un][t])), pk2(f[g][0], f[g][1])), w0, w1);
             uint32_t hi, lo;
             split2(w0, w1, hi, lo);
-            pb[g][t] = transpose8(low ? lo : hi);
+            pb[un][g][t] = transpose8(low ? lo : hi);
           }
-        // values: lane (n8, c4) holds the 16 dimensions of chunk n8 of token pairs c4 and 4 + c4
-        const unsigned char *const V = U + un * kUnitBytes + ld_v;
-        const uint4 v0 = read16(V), v1 = read16(V + 512);
+      // lane (n8, c4) holds the 16 dimensions of chunk n8 of token pairs c4 and 4 + c4
+      const uint4 v00 = read16(U + ld_v), v01 = read16(U + ld_v + 512);
+      const uint4 v10 = read16(U + kUnitBytes + ld_v), v11 = read16(U + kUnitBytes + ld_v + 512);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
+      for (int w = 0; w < 2; ++w) {
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t p0[4], p1[4];
-            const uint32_t pick = hf ? 0x7632u : 0x5410u;
-            value_pairs(__byte_perm(w ? v0.y : v0.x, w ? v0.w : v0.z, pick), centre, p0);
-            value_pairs(__byte_perm(w ? v1.y : v1.x, w ? v1.w : v1.z, pick), centre, p1);
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t p00[4], p01[4], p10[4], p11[4];
+          const uint32_t pick = hf ? 0x7632u : 0x5410u;
+          value_pairs(__byte_perm(w ? v00.y : v00.x, w ? v00.w : v00.z, pick), factor, p00);
+          value_pairs(__byte_perm(w ? v01.y : v01.x, w ? v01.w : v01.z, pick), factor, p01);
+          value_pairs(__byte_perm(w ? v10.y : v10.x, w ? v10.w : v10.z, pick), factor, p10);
+          value_pairs(__byte_perm(w ? v11.y : v11.x, w ? v11.w : v11.z, pick), factor, p11);
 #pragma unroll
-            for (int g = 0; g < NC; ++g) {
-              mma16816(acc[g][4 * w + 2 * hf], p0[0], p0[1], p1[0], p1[1], pb[g][0], pb[g][1]);
-              mma16816(acc[g][4 * w + 2 * hf + 1], p0[2], p0[3], p1[2], p1[3], pb[g][0], pb[g][1]);
+          for (int g = 0; g < NC; ++g)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float *sum = acc[g][4 * w + 2 * hf + j];
+              mma16816(sum, p00[2 * j], p00[2 * j + 1], p01[2 * j], p01[2 * j + 1], pb[0][g][0], pb[0][g][1]);
+              mma16816(sum, p10[2 * j], p10[2 * j + 1], p11[2 * j], p11[2 * j + 1], pb[1][g][0], pb[1][g][1]);
             }
-          }
         }
       }
     }
@@ -688,7 +698,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[g][e] = __fadd_rn(l[g][e], __shfl_xor_sync(0xffffffffu, l[g][e], d));
         // dimensions 16 n8 .. + 15 of row e: both lanes of a (high, low) pair form the sums, the
-        // high one stores row e0, the low one row e0 + 1; acc is 2^-9 of them
+        // high one stores row e0, the low one row e0 + 1
         float *dst = s_acc + (warp * kRows + 4 * g + e0 + e) * kTile + 16 * n8;
         const float f_own = low ? 0.25f : 512.0f, f_other = low ? 512.0f : 0.25f;
 #pragma unroll
@@ -699,6 +709,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
             const float own = acc[g][k + (d >> 1)][2 * (d & 1) + e];
             const float other = __shfl_xor_sync(0xffffffffu, own, 2);
             v[d] = __fmaf_rn(other, f_other, __fmul_rn(own, f_own));
+            if (d & 1) v[d] = __fmul_rn(__fsub_rn(v[d], v[d - 1]), 0.0625f);
           }
           if (low == (e == 1)) *reinterpret_cast<float4 *>(dst + 2 * k) = make_float4(v[0], v[1], v[2], v[3]);
         }
@@ -773,9 +784,9 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
 
 // The sums of a (sequence, head, row tile) that several blocks share: block
 // (i, row) joins that row of what block i of the attention kernel began.  Each
-// of the four warps adds every fourth block's sums, in order, a lane four
-// dimensions; the four are added in order.
-constexpr int kJoinThreads = 128;
+// of the warps adds every eighth block's sums, in order, a lane four
+// dimensions; the eight are added in order.
+constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, int rows) {
   __shared__ __align__(16) float s_tr[4 * kTrTile];
   __shared__ __align__(16) float s_x[kJoinThreads / 32][kTile];
