@@ -53,12 +53,14 @@ enum { HQ_T_BF16 = 0, HQ_T_F32 = 1, HQ_T_F16 = 2 };
 #define HQ_KV4_UNIT_BYTES 2112
 
 /* A pool of pages and the block table through which a call sees it.
- *   d_pages       [n_pages][n_kv_heads][page_tokens / 16][2112] bytes, 16-byte aligned
+ *   d_pages       [n_pages][n_kv_heads][page_tokens / 16][2112] bytes, 16-byte
+ *                 aligned; n_pages >= 1
  *   page_tokens   a positive multiple of 16
  *   d_table       [n_seqs][table_width] int32 page numbers; entries past a
  *                 sequence's length are not read
  *   d_signs       [4] uint32: the sign mask of every tile (hq_make_layer_signs)
- * table_width * page_tokens, a sequence's capacity, is at most 2^30. */
+ * table_width * page_tokens, a sequence's capacity, is at most 2^30, and the
+ * pool holds fewer than 2^28 units (527 GB). */
 typedef struct hq_kv4_cache {
   void *d_pages;
   int64_t n_pages;

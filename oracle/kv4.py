@@ -131,7 +131,7 @@ def read32(pages, page, h, t, which, mask):
     """One row as the fp32 steps of hq_kv4_read give it."""
     c, s = raw_rows(pages, page, which)
     sf = F32(s[h, t]) * F32(0.08838834764831845)
-    return fwht((c[h, t].astype(F32) - F32(7.5)) * sf) * signs_of(mask).astype(F32)
+    return fwht(c[h, t].astype(F32) - F32(7.5)) * signs_of(mask).astype(F32) * sf     # exact sums
 
 
 def attention(pages, table, lengths, q, mask, scale, cap=0.0, mass=None):

@@ -102,7 +102,7 @@ def cache(hq, **kw):
 
 
 BAD_CACHES = [dict(page_tokens=24), dict(page_tokens=0), dict(page_tokens=-16), dict(n_kv_heads=0),
-              dict(n_pages=-1), dict(n_seqs=-1), dict(n_seqs=70000), dict(table_width=-1),
+              dict(n_pages=-1), dict(n_pages=0), dict(n_pages=1 << 28), dict(n_seqs=-1), dict(n_seqs=70000), dict(table_width=-1),
               dict(table_width=1 << 26), dict(d_pages=None), dict(d_pages=FAKE + 8),
               dict(d_table=None), dict(d_signs=None), dict(d_table=FAKE + 2)]
 

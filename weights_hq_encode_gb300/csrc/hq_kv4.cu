@@ -1,14 +1,12 @@
 // hq_kv4.cu -- the 4-bit window cache's writes, reads and evictions
-// (include/hq_kv4.h states the format).  All of them are bound by memory: a
-// token of one head is 132 bytes in the cache and 2 x 128 values outside it.
-// 8 lanes hold a row as the codec's kernels do (lane r: dimensions 16 r ..
-// 16 r + 15), so that the transform is the codec's, its stages in the codec's
-// order, and a lane's 16 codes are the 8 bytes it stores.
+// (include/hq_kv4.h states the format).  All of them move rows: a token of one
+// head is 132 bytes in the cache and 2 x 128 values outside it.
 #include <cuda_runtime.h>
 
 #include "hq_device.cuh"
 #include "hq_kv4.h"
 #include "hq_kv4_io.cuh"
+#include "hq_launch.cuh"
 
 namespace hq {
 
@@ -22,103 +20,213 @@ __device__ __forceinline__ int kv4_chunk(int which, int tok, int r) {
   return which == 0 ? tok * 64 + r * 8 : kUnitV + (tok >> 1) * 128 + r * 16 + (tok & 1) * 8;
 }
 
-// One row a group of 8 lanes: blockIdx.y 0 codes K, 1 codes V.
-template <int KIND>
-__global__ void __launch_bounds__(kRowsThreads) kv4_append_kernel(Kv4RowArgs a) {
-  __shared__ __align__(16) float s_tr[(kRowsThreads / 8) * kTrTile];
-  const int tl = threadIdx.x >> 3, r = threadIdx.x & 7, which = blockIdx.y;
-  const int64_t row = (int64_t)blockIdx.x * (kRowsThreads / 8) + tl;
-  const int64_t i = row / a.c.n_kv;
-  const int h = (int)(row - i * a.c.n_kv);
-  int64_t page = -1;
-  int pos = 0;
-  if (i < a.n_tokens) {                          // every lane stays for the transform
-    const int seq = __ldg(a.seq + i);
-    pos = __ldg(a.pos + i);
-    if (seq >= 0) {
-      if (seq < a.c.n_seqs && pos >= 0 && pos < a.c.capacity()) page = kv4_page(a.c, seq, pos);
-      if (page < 0 && r == 0) atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
-    }
-  }
-  float x[16];
-  if (page >= 0) {
-    const int64_t at = which == 0 ? i * a.rows.k_token + h * a.rows.k_head
-                                  : i * a.rows.v_token + h * a.rows.v_head;
-    load_row16<KIND>(which == 0 ? a.rows.k : a.rows.v, at, r, a.rows.vec != 0, x);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = 0.0f;
-  }
-  const uint32_t mw = __ldg(a.c.signs + (r >> 1)) >> (16 * (r & 1));
-#pragma unroll
-  for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(__float_as_uint(x[j]) ^ (((mw >> j) & 1u) << 31));
-  fwht128_t8(x, s_tr + tl * kTrTile, r);
-  // the largest magnitude as an integer: an infinity or a NaN is above every finite value
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-#pragma unroll
-  for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-  if (page < 0) return;
-  const bool finite = top < 0x7F800000u;
-  if (!finite && r == 0) atomicOr(a.status, (uint32_t)HQ_ERR_RANGE);
-  __nv_bfloat16 s = __float2bfloat16_rn(finite ? __fmul_rn(__uint_as_float(top), kAbsToScale) : 0.0f);
-  float sf = __bfloat162float(s);
-  if (sf < 0x1p-126f) sf = 0.0f;                 // no subnormal scales: the row is zero
-  const float inv = sf > 0.0f ? __fdiv_rn(1.0f, __fmul_rn(sf, kRoot128)) : 0.0f;
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float t = floorf(__fadd_rn(__fmul_rn(sf > 0.0f ? x[j] : 0.0f, inv), 8.0f));
-    w[j >> 3] |= (uint32_t)fminf(fmaxf(t, 0.0f), 15.0f) << (4 * (j & 7));
-  }
-  unsigned char *unit = kv4_unit(a.c, page, h, pos);
-  const int tok = pos % kUnit;
-  *reinterpret_cast<uint2 *>(unit + kv4_chunk(which, tok, r)) = make_uint2(w[0], w[1]);
-  if (r == 0)
-    reinterpret_cast<uint16_t *>(unit + (which == 0 ? kUnitKs : kUnitVs))[tok] =
-        (uint16_t)(__float_as_uint(sf) >> 16);
+// Two values' codes added up into 4-bit fields: floor(fl(fl(z inv) + 8)), the
+// floor by a sum with 2^23 rounded towards zero.  |z| inv is at most 7.5
+// (1 + 2^-8) and a few units, so the codes are 0 .. 15 as they are.
+__device__ __forceinline__ void add_codes(uint32_t &w, float z0, float z1, uint64_t inv, int at) {
+  uint64_t t = add2(mul2(pk2(z0, z1), inv), pk2(8.0f, 8.0f));
+  asm("add.rz.f32x2 %0, %1, %2;" : "=l"(t) : "l"(t), "l"(pk2(8388608.0f, 8388608.0f)));
+  float a, b;
+  upk2(t, a, b);
+  w += (__float_as_uint(a) << (4 * at)) + (__float_as_uint(b) << (4 * at + 4));
 }
 
+// Codes K and V rows, 8 lanes an entry as the codec's kernels hold a tile
+// (lane r: dimensions 16 r .. 16 r + 15), so that the transform is the codec's,
+// its stages in the codec's order, and a lane's 16 codes are the 8 bytes it
+// stores.  Bound by instructions: about 220 a warp for 4 rows.
 template <int KIND>
-__global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(Kv4RowArgs a) {
+__global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(Kv4RowArgs a) {
   __shared__ __align__(16) float s_tr[(kRowsThreads / 8) * kTrTile];
-  const int tl = threadIdx.x >> 3, r = threadIdx.x & 7, which = blockIdx.y;
-  const int64_t row = (int64_t)blockIdx.x * (kRowsThreads / 8) + tl;
-  const int64_t i = row / a.c.n_kv;
-  const int h = (int)(row - i * a.c.n_kv);
-  bool live = i < a.n_tokens;                    // every lane stays for the transform
-  uint2 w = make_uint2(0x88888888u, 0x88888888u);
-  float s = 0.0f;
-  if (live) {
+  follow_launch();
+  const int tl = threadIdx.x >> 3, r = threadIdx.x & 7;
+  const int64_t entry = (int64_t)blockIdx.x * (kRowsThreads / 8) + tl;
+  const int64_t i = kv4_divide(entry, a.c.n_kv, a.c.kv_shift);
+  const int h = (int)(entry - i * a.c.n_kv);
+  Row16<KIND> rows[2];
+  uint32_t place = kNoPlace;
+  if (i < a.n_tokens) {                          // every lane stays for the transform
+    rows[0].load(a.rows.k, i * a.rows.k_token + h * a.rows.k_head, r, a.rows.vec != 0);
+    rows[1].load(a.rows.v, i * a.rows.v_token + h * a.rows.v_head, r, a.rows.vec != 0);
     const int seq = __ldg(a.seq + i), pos = __ldg(a.pos + i);
-    live = seq >= 0;
-    if (live) {
-      int64_t page = -1;
-      if (seq < a.c.n_seqs && pos >= 0 && pos < a.c.capacity()) page = kv4_page(a.c, seq, pos);
-      if (page >= 0) {
-        const unsigned char *unit = kv4_unit(a.c, page, h, pos);
-        const int tok = pos % kUnit;
-        w = *reinterpret_cast<const uint2 *>(unit + kv4_chunk(which, tok, r));
-        s = bf16_to_f32(reinterpret_cast<const uint16_t *>(unit + (which == 0 ? kUnitKs : kUnitVs))[tok]);
-      } else if (r == 0) {
+    if (seq >= 0) {
+      place = kv4_place(a.c, seq, pos, h);
+      if (place == kNoPlace && r == 0) atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
+    }
+  } else {
+    rows[0].zero();
+    rows[1].zero();
+  }
+  const uint32_t mw = __ldg(a.c.signs + (r >> 1)) >> (16 * (r & 1));
+  unsigned char *const unit = kv4_unit(a.c, place);
+  const int tok = place % kUnit;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float y[16];
+    rows[which].get(mw, y);
+    fwht128_t8(y, s_tr + tl * kTrTile, r);
+    // the largest magnitude as an integer: an infinity or a NaN is above every finite value
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const bool finite = top < 0x7F800000u;
+    float sf = finite ? __bfloat162float(__float2bfloat16_rn(__fmul_rn(__uint_as_float(top), kAbsToScale))) : 0.0f;
+    if (sf < 0x1p-126f) sf = 0.0f;               // no subnormal scales: the row is zero
+    const float inv = sf > 0.0f ? __fdiv_rn(1.0f, __fmul_rn(sf, kRoot128)) : 0.0f;
+    const uint64_t inv2 = pk2(inv, inv);
+    // 2^23's own bits, shifted to every field of a word
+    constexpr uint32_t kOnes = 0x4B000000u * 0x11111111u;
+    uint32_t w[2] = {0u - kOnes, 0u - kOnes};
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) add_codes(w[j >> 3], y[j], y[j + 1], inv2, j & 7);
+    if (place == kNoPlace) continue;
+    if (sf == 0.0f) w[0] = w[1] = 0x88888888u;
+    *reinterpret_cast<uint2 *>(unit + kv4_chunk(which, tok, r)) = make_uint2(w[0], w[1]);
+    if (r == 0) {
+      if (!finite) atomicOr(a.status, (uint32_t)HQ_ERR_RANGE);
+      reinterpret_cast<uint16_t *>(unit + (which == 0 ? kUnitKs : kUnitVs))[tok] =
+          (uint16_t)(__float_as_uint(sf) >> 16);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- reading
+// +1 or -1 of the Hadamard matrix as fp16, entries (i, j) and (i, k).
+__device__ __forceinline__ uint32_t signs_f16(int i, int j, int k) {
+  return (0x3C00u | ((uint32_t)(__popc(i & j) & 1) << 15)) | (0x3C000000u | ((uint32_t)(__popc(i & k) & 1) << 31));
+}
+
+// Writes a row's 4 values of this lane, dimensions d, d + 1 and d + 64, d + 65.
+template <int KIND>
+__device__ __forceinline__ void store4(void *base, int64_t at, bool vec, const float v[4], const uint32_t flip[4]) {
+  if constexpr (KIND == HQ_T_F32) {
+    float x[4], *p = static_cast<float *>(base) + at;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(__float_as_uint(v[j]) ^ flip[j]);
+    if (vec) {
+      *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+      *reinterpret_cast<float2 *>(p + 64) = make_float2(x[2], x[3]);
+    } else {
+      p[0] = x[0]; p[1] = x[1]; p[64] = x[2]; p[65] = x[3];
+    }
+  } else {
+    uint16_t *p = static_cast<uint16_t *>(base) + at;
+    const uint32_t lo = round_pair<KIND>(v[0], v[1]) ^ (flip[0] >> 16 | flip[1]);
+    const uint32_t hi = round_pair<KIND>(v[2], v[3]) ^ (flip[2] >> 16 | flip[3]);
+    if (vec) {
+      *reinterpret_cast<uint32_t *>(p) = lo;
+      *reinterpret_cast<uint32_t *>(p + 64) = hi;
+    } else {
+      p[0] = (uint16_t)lo; p[1] = (uint16_t)(lo >> 16); p[64] = (uint16_t)hi; p[65] = (uint16_t)(hi >> 16);
+    }
+  }
+}
+
+// Values of K and V rows, up to 32 (token, head) entries a warp.  With d = 8 a + b the
+// matrix is H16 x H8, and a row's codes are a 16 x 8 matrix X: H16 X is one
+// mma.sync m16n8k16, (H16 X) H8 one m16n8k8 of the first one's result.  All of it is
+// exact (+-1 times half-integers, sums below 2^10 in fp16 and fp32), so the
+// one rounding is that of the product with the scale; and a lane ends with
+// dimensions 8 n8 + 2 c4 and the next, and the same + 64: whole 128-byte
+// stores.  The codec's transform in registers and shared memory instead was bound
+// by its 330 instructions for 4 rows (68 us for 262144 entries to bf16, 25 of
+// them the memory's).
+constexpr int kReadBatch = 4;                    // entries of a warp at a time
+template <int KIND>
+__global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(Kv4RowArgs a, int per_warp) {
+  follow_launch();
+  const int lane = threadIdx.x & 31, n8 = lane >> 2, c4 = lane & 3;
+  const int64_t first = ((int64_t)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5)) * per_warp;
+  const int64_t entries = a.n_tokens * a.c.n_kv;
+  if (first >= entries) return;
+  // an entry a lane: its place, its scales and where its rows go
+  uint32_t place = 0;
+  bool writes = false;
+  int64_t k_at = 0, v_at = 0;
+  float ks = 0.0f, vs = 0.0f;
+  if (lane < per_warp && first + lane < entries) {
+    const int64_t i = kv4_divide(first + lane, a.c.n_kv, a.c.kv_shift);
+    const int h = (int)(first + lane - i * a.c.n_kv);
+    const int seq = __ldg(a.seq + i), pos = __ldg(a.pos + i);
+    writes = seq >= 0;                           // no padding token
+    if (writes) {
+      place = kv4_place(a.c, seq, pos, h);
+      k_at = i * a.rows.k_token + h * a.rows.k_head;
+      v_at = i * a.rows.v_token + h * a.rows.v_head;
+      if (place == kNoPlace) {
         atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
+        place = 0;                               // the pool's first row, times a scale of 0
+      } else {
+        const unsigned char *unit = kv4_unit(a.c, place);
+        ks = bf16_to_f32(reinterpret_cast<const uint16_t *>(unit + kUnitKs)[place % kUnit]);
+        vs = bf16_to_f32(reinterpret_cast<const uint16_t *>(unit + kUnitVs)[place % kUnit]);
+        ks = __fmul_rn(__fmul_rn(ks, kInvRoot128), 512.0f);    // codes come in units of 2^-9
+        vs = __fmul_rn(__fmul_rn(vs, kInvRoot128), 512.0f);
       }
     }
   }
-  s = __fmul_rn(s, kInvRoot128);                 // before the sums, so that they stay in range
-  float x[16];
+  const uint32_t live = __ballot_sync(0xffffffffu, writes);
+  // rows n8 and n8 + 8 of H16 (its columns in the order of the words below), columns of H8
+  const uint32_t h0 = signs_f16(n8, 4 * c4, 4 * c4 + 1), h1 = signs_f16(n8 + 8, 4 * c4, 4 * c4 + 1);
+  const uint32_t h2 = signs_f16(n8, 4 * c4 + 2, 4 * c4 + 3), h3 = signs_f16(n8 + 8, 4 * c4 + 2, 4 * c4 + 3);
+  const uint32_t g0 = signs_f16(n8, 2 * c4, 2 * c4 + 1);
+  // nibble n8 of a word: byte n8 / 2, as a subnormal of 2^-24 or 2^-20, centred to (c - 7.5) 2^-9
+  const uint32_t sel = (uint32_t)(n8 >> 1) | ((uint32_t)(n8 >> 1) + 4u) << 8;   // into bytes 0 and 2
+  const uint32_t mask = (n8 & 1) ? 0x00F000F0u : 0x000F000Fu, factor = (n8 & 1) ? 0x68006800u : 0x78007800u;
+  const int d = 8 * n8 + 2 * c4;
+  uint32_t flip[4];
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
-    x[j] = __fmul_rn((float)(int)(((j < 8 ? w.x : w.y) >> (4 * (j & 7))) & 15u) - 7.5f, s);
-  fwht128_t8(x, s_tr + tl * kTrTile, r);
-  if (!live) return;
-  const uint32_t mw = __ldg(a.c.signs + (r >> 1)) >> (16 * (r & 1));
+  for (int j = 0; j < 4; ++j) {
+    const int dj = d + (j & 1) + 64 * (j >> 1);
+    flip[j] = ((__ldg(a.c.signs + (dj >> 5)) >> (dj & 31)) & 1u) << 31;
+  }
+  const bool same = a.rows.k_token == a.rows.v_token && a.rows.k_head == a.rows.v_head;
+  const uint32_t k_off = 16 * c4, v_off = kUnitV + 32 * c4;
+#pragma unroll 1
+  for (int e0 = 0; e0 < 32 && (live >> e0) != 0; e0 += kReadBatch) {
+    // words 4 c4 .. 4 c4 + 3 (8 dimensions each) of every entry's K and V
+    uint4 k[kReadBatch];
+    uint2 lo[kReadBatch], hi[kReadBatch];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(__float_as_uint(x[j]) ^ (((mw >> j) & 1u) << 31));
-  const int64_t at = which == 0 ? i * a.rows.k_token + h * a.rows.k_head
-                                : i * a.rows.v_token + h * a.rows.v_head;
-  store_row16<KIND>(const_cast<void *>(which == 0 ? a.rows.k : a.rows.v), at, r, a.rows.vec != 0, x);
+    for (int e = 0; e < kReadBatch; ++e) {
+      const uint32_t p = __shfl_sync(0xffffffffu, place, e0 + e), tok = p % kUnit;
+      const unsigned char *unit = kv4_unit(a.c, p) + tok * 64;
+      k[e] = *reinterpret_cast<const uint4 *>(unit + k_off);
+      const uint2 *v = reinterpret_cast<const uint2 *>(unit + v_off - (tok & 1) * 56);   // pairs are 128 bytes apart
+      lo[e] = v[0];
+      hi[e] = v[2];
+    }
+#pragma unroll
+    for (int e = 0; e < kReadBatch; ++e) {
+      if (!((live >> (e0 + e)) & 1u)) continue;  // warp-uniform
+      const int64_t to_k = __shfl_sync(0xffffffffu, k_at, e0 + e) + d;
+      const int64_t to_v = same ? to_k : __shfl_sync(0xffffffffu, v_at, e0 + e) + d;
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        const uint4 w = which == 0 ? k[e] : make_uint4(lo[e].x, lo[e].y, hi[e].x, hi[e].y);
+        const float s = __shfl_sync(0xffffffffu, which == 0 ? ks : vs, e0 + e);
+        uint32_t b0 = __byte_perm(w.x, w.y, sel) & mask, b1 = __byte_perm(w.z, w.w, sel) & mask;
+        asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(b0) : "r"(factor), "r"(0xA380A380u));
+        asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(b1) : "r"(factor), "r"(0xA380A380u));
+        float t[4], x[4];
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+            "{%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(t[0]), "=f"(t[1]), "=f"(t[2]), "=f"(t[3])
+            : "r"(h0), "r"(h1), "r"(h2), "r"(h3), "r"(b0), "r"(b1), "f"(0.0f));
+        const uint32_t t0 = round_pair<HQ_T_F16>(t[0], t[1]), t1 = round_pair<HQ_T_F16>(t[2], t[3]);   // exact
+        asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, "
+            "{%7, %7, %7, %7};"
+            : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+            : "r"(t0), "r"(t1), "r"(g0), "f"(0.0f));
+        upk2(mul2(pk2(x[0], x[1]), pk2(s, s)), x[0], x[1]);
+        upk2(mul2(pk2(x[2], x[3]), pk2(s, s)), x[2], x[3]);
+        store4<KIND>(const_cast<void *>(which == 0 ? a.rows.k : a.rows.v), which == 0 ? to_k : to_v,
+                     a.rows.vec != 0, x, flip);
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------- eviction
@@ -163,6 +271,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
   __shared__ uint32_t s_hist[kSelBins];
   __shared__ uint32_t s_w[64];
   __shared__ uint32_t s_digit, s_above;
+  follow_launch();
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   bool bad;
   const int n = kv4_length(a.src, a.lengths, b, &bad);
@@ -233,66 +342,92 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
   }
 }
 
-// Rows and masses of the kept positions: 8 lanes a row.
-__global__ void __launch_bounds__(kRowsThreads) kv4_move_kernel(Kv4EvictArgs a) {
-  const int r = threadIdx.x & 7, h = blockIdx.y, b = blockIdx.z;
-  const int i = blockIdx.x * (kRowsThreads / 8) + (threadIdx.x >> 3);
+// Rows and masses of the kept positions, up to 32 a warp: a lane looks one up,
+// moves its scales and its mass; then 8 lanes a row move the codes, all rows'
+// loads before the first store.
+__global__ void __launch_bounds__(kRowsThreads) kv4_move_kernel(Kv4EvictArgs a, int per_warp) {
+  follow_launch();
+  const int lane = threadIdx.x & 31, r = lane & 7, h = blockIdx.y, b = blockIdx.z;
+  const int first = (blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5)) * per_warp, i = first + lane;
   bool bad;
-  const int n = kv4_length(a.src, a.lengths, b, &bad);
-  if (i >= min(n, a.budget)) return;
+  const int n = min(kv4_length(a.src, a.lengths, b, &bad), a.budget);
+  if (first >= n) return;
   const int64_t head = (int64_t)b * a.src.n_kv + h;
-  const int t = a.kept[head * a.budget + i];
-  if (r == 0) a.new_mass[head * a.dst.capacity() + i] = __ldg(a.mass + head * a.src.capacity() + t);
-  const int64_t from = kv4_page(a.src, b, t), to = kv4_page(a.dst, b, i);
-  if (from < 0 || to < 0) {
-    if (r == 0) atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
-    return;
+  uint32_t from = kNoPlace, to = kNoPlace;
+  if (lane < per_warp && i < n) {
+    const int t = a.kept[head * a.budget + i];
+    from = kv4_place(a.src, b, t, h);
+    to = kv4_place(a.dst, b, i, h);
+    a.new_mass[head * a.dst.capacity() + i] = __ldg(a.mass + head * a.src.capacity() + t);
+    if (from == kNoPlace || to == kNoPlace) {
+      atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
+      from = to = kNoPlace;
+    } else {
+      const uint16_t *s = reinterpret_cast<const uint16_t *>(kv4_unit(a.src, from) + kUnitKs) + from % kUnit;
+      uint16_t *d = reinterpret_cast<uint16_t *>(kv4_unit(a.dst, to) + kUnitKs) + to % kUnit;
+      const uint16_t ks = s[0], vs = s[kUnit];
+      d[0] = ks;
+      d[kUnit] = vs;
+    }
   }
-  const unsigned char *su = kv4_unit(a.src, from, h, t);
-  unsigned char *du = kv4_unit(a.dst, to, h, i);
-  const int st = t % kUnit, dt = i % kUnit;
+  uint2 k[8], v[8];
 #pragma unroll
-  for (int which = 0; which < 2; ++which)
-    *reinterpret_cast<uint2 *>(du + kv4_chunk(which, dt, r)) =
-        *reinterpret_cast<const uint2 *>(su + kv4_chunk(which, st, r));
-  if (r < 2)
-    reinterpret_cast<uint16_t *>(du + kUnitKs + 32 * r)[dt] =
-        reinterpret_cast<const uint16_t *>(su + kUnitKs + 32 * r)[st];
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t p = __shfl_sync(0xffffffffu, from, 4 * e + (lane >> 3));
+    if (p == kNoPlace) continue;
+    const unsigned char *unit = kv4_unit(a.src, p);
+    k[e] = *reinterpret_cast<const uint2 *>(unit + kv4_chunk(0, p % kUnit, r));
+    v[e] = *reinterpret_cast<const uint2 *>(unit + kv4_chunk(1, p % kUnit, r));
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t p = __shfl_sync(0xffffffffu, to, 4 * e + (lane >> 3));
+    if (p == kNoPlace) continue;
+    unsigned char *unit = kv4_unit(a.dst, p);
+    *reinterpret_cast<uint2 *>(unit + kv4_chunk(0, p % kUnit, r)) = k[e];
+    *reinterpret_cast<uint2 *>(unit + kv4_chunk(1, p % kUnit, r)) = v[e];
+  }
 }
 
 // ---------------------------------------------------------------- launches
-static dim3 rows_grid(const Kv4RowArgs &a) {
-  return dim3((unsigned)((a.n_tokens * a.c.n_kv + kRowsThreads / 8 - 1) / (kRowsThreads / 8)), 2);
+int launch_kv4_append(const Kv4RowArgs &a, cudaStream_t st) {
+  const dim3 grid((unsigned)((a.n_tokens * a.c.n_kv + kRowsThreads / 8 - 1) / (kRowsThreads / 8)));
+  switch (a.rows.kind) {
+    case HQ_T_F32: return launch_behind(kv4_append_kernel<HQ_T_F32>, grid, kRowsThreads, 0, st, a);
+    case HQ_T_F16: return launch_behind(kv4_append_kernel<HQ_T_F16>, grid, kRowsThreads, 0, st, a);
+    default: return launch_behind(kv4_append_kernel<HQ_T_BF16>, grid, kRowsThreads, 0, st, a);
+  }
 }
 
-int launch_kv4_append(const Kv4RowArgs &a, cudaStream_t st) {
-  const dim3 grid = rows_grid(a);
-  switch (a.rows.kind) {
-    case HQ_T_F32: kv4_append_kernel<HQ_T_F32><<<grid, kRowsThreads, 0, st>>>(a); break;
-    case HQ_T_F16: kv4_append_kernel<HQ_T_F16><<<grid, kRowsThreads, 0, st>>>(a); break;
-    default: kv4_append_kernel<HQ_T_BF16><<<grid, kRowsThreads, 0, st>>>(a); break;
-  }
-  return cudaGetLastError() == cudaSuccess ? 0 : 1;
+// Rows a warp takes, a power of two from `least` to 32: as many as leave work
+// for 16 warps a multiprocessor (few rows a warp for short calls, whose time is
+// that of one warp's chain of loads; many for long ones, whose look-ups are
+// then one a lane).
+static int rows_a_warp(int64_t rows, int least) {
+  int per = 32;
+  while (per > least && rows < (int64_t)per * 16 * 152) per /= 2;
+  return per;
 }
 
 int launch_kv4_read(const Kv4RowArgs &a, cudaStream_t st) {
-  const dim3 grid = rows_grid(a);
+  const int64_t entries = a.n_tokens * a.c.n_kv;
+  const int per = rows_a_warp(entries, 1), block = kRowsThreads / 32 * per;
+  const dim3 grid((unsigned)((entries + block - 1) / block));
   switch (a.rows.kind) {
-    case HQ_T_F32: kv4_read_kernel<HQ_T_F32><<<grid, kRowsThreads, 0, st>>>(a); break;
-    case HQ_T_F16: kv4_read_kernel<HQ_T_F16><<<grid, kRowsThreads, 0, st>>>(a); break;
-    default: kv4_read_kernel<HQ_T_BF16><<<grid, kRowsThreads, 0, st>>>(a); break;
+    case HQ_T_F32: return launch_behind(kv4_read_kernel<HQ_T_F32>, grid, kRowsThreads, 0, st, a, per);
+    case HQ_T_F16: return launch_behind(kv4_read_kernel<HQ_T_F16>, grid, kRowsThreads, 0, st, a, per);
+    default: return launch_behind(kv4_read_kernel<HQ_T_BF16>, grid, kRowsThreads, 0, st, a, per);
   }
-  return cudaGetLastError() == cudaSuccess ? 0 : 1;
 }
 
 int launch_kv4_evict(const Kv4EvictArgs &a, cudaStream_t st) {
-  kv4_select_kernel<<<dim3((unsigned)a.src.n_kv, (unsigned)a.src.n_seqs), kSelThreads, 0, st>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return 1;
+  if (launch_behind(kv4_select_kernel, dim3((unsigned)a.src.n_kv, (unsigned)a.src.n_seqs), kSelThreads, 0, st, a) != 0)
+    return 1;
   if (a.src.capacity() == 0) return 0;           // no tokens to move
   const int64_t most = a.budget < a.src.capacity() ? a.budget : a.src.capacity();
-  kv4_move_kernel<<<dim3((unsigned)((most + kRowsThreads / 8 - 1) / (kRowsThreads / 8)),
-                         (unsigned)a.src.n_kv, (unsigned)a.src.n_seqs), kRowsThreads, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? 0 : 1;
+  const int per = rows_a_warp(most * a.src.n_kv * a.src.n_seqs, 4), block = kRowsThreads / 32 * per;
+  return launch_behind(kv4_move_kernel, dim3((unsigned)((most + block - 1) / block), (unsigned)a.src.n_kv,
+                                             (unsigned)a.src.n_seqs), kRowsThreads, 0, st, a, per);
 }
 
 }  // namespace hq

@@ -18,7 +18,9 @@ struct Kv4View {
   unsigned char *pages;
   int64_t n_pages;
   int page_tokens, page_units;
+  int page_shift;           // log2(page_tokens) when a power of two, else -1
   int n_kv;
+  int kv_shift;             // log2(n_kv) likewise
   const int32_t *table;     // [n_seqs][width] page numbers
   int n_seqs, width;
   const uint32_t *signs;    // 128-bit sign mask
@@ -88,15 +90,24 @@ int launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t st);
 int launch_kv4_evict(const Kv4EvictArgs &a, cudaStream_t st);
 
 #ifdef __CUDACC__
-// The page of position `pos` of sequence `seq` (both in range), or -1 when
-// the table names none of the pool's pages.
-__device__ __forceinline__ int64_t kv4_page(const Kv4View &c, int seq, int pos) {
-  const int p = __ldg(c.table + (int64_t)seq * c.width + pos / c.page_tokens);
-  return p >= 0 && p < c.n_pages ? (int64_t)p : -1;
+// x / y of nonnegative x and positive y, by a 32-bit division where it fits or a shift (>= 0).
+__device__ __forceinline__ int64_t kv4_divide(int64_t x, int64_t y, int shift = -1) {
+  if (shift >= 0) return x >> shift;
+  return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
 }
-// The unit of head h that holds position `pos` of a page.
-__device__ __forceinline__ unsigned char *kv4_unit(const Kv4View &c, int64_t page, int h, int pos) {
-  return c.pages + ((page * c.n_kv + h) * c.page_units + pos % c.page_tokens / kUnit) * kUnitBytes;
+// The place of (sequence, position, head): 16 x its unit's number in the pool +
+// its token in the unit, or kNoPlace where there is no such position or the
+// table names none of the pool's pages.
+constexpr uint32_t kNoPlace = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t kv4_place(const Kv4View &c, int seq, int pos, int h) {
+  if (seq >= c.n_seqs || pos < 0 || pos >= c.capacity()) return kNoPlace;
+  const int j = (int)kv4_divide(pos, c.page_tokens, c.page_shift), in_page = pos - j * c.page_tokens;
+  const int page = __ldg(c.table + (int64_t)seq * c.width + j);
+  if (page < 0 || page >= c.n_pages) return kNoPlace;
+  return (uint32_t)((page * c.n_kv + h) * c.page_units + in_page / kUnit) * kUnit + (uint32_t)(in_page % kUnit);
+}
+__device__ __forceinline__ unsigned char *kv4_unit(const Kv4View &c, uint32_t place) {
+  return c.pages + (int64_t)(place / kUnit) * kUnitBytes;
 }
 // A sequence's length, held to [0, capacity]; *bad when it was outside.
 __device__ __forceinline__ int kv4_length(const Kv4View &c, const int32_t *lengths, int seq, bool *bad) {

@@ -20,17 +20,16 @@ size_t size_of(int k) { return k == HQ_T_F32 ? 4 : 2; }
 
 // The sizes of a cache; its pointers are looked at only by cache_ok.
 bool sizes_ok(const hq_kv4_cache *c) {
-  return c && c->n_pages >= 0 && c->n_pages <= INT32_MAX && c->page_tokens > 0 &&
+  return c && c->n_pages > 0 && c->n_pages <= INT32_MAX && c->page_tokens > 0 &&
          c->page_tokens % HQ_KV4_UNIT == 0 && c->n_kv_heads > 0 && c->n_kv_heads <= 65535 &&
          c->n_seqs >= 0 && c->n_seqs <= 65535 && c->table_width >= 0 &&
          (int64_t)c->table_width * c->page_tokens <= kMaxCapacity &&
-         // unit numbers of the pool fit 31 bits
-         (c->n_pages == 0 ||
-          c->n_pages <= INT32_MAX / c->n_kv_heads / (c->page_tokens / HQ_KV4_UNIT));
+         // 16 x a unit's number in the pool fits 32 bits
+         c->n_pages < (1 << 28) / c->n_kv_heads / (c->page_tokens / HQ_KV4_UNIT);
 }
 
 bool cache_ok(const hq_kv4_cache *c) {
-  return sizes_ok(c) && (c->n_pages == 0 || c->d_pages) && aligned(c->d_pages, 16) &&
+  return sizes_ok(c) && c->d_pages && aligned(c->d_pages, 16) &&
          ((int64_t)c->n_seqs * c->table_width == 0 || c->d_table) && aligned(c->d_table, 4) &&
          c->d_signs && aligned(c->d_signs, 4);
 }
@@ -41,7 +40,9 @@ Kv4View view_of(const hq_kv4_cache *c) {
   v.n_pages = c->n_pages;
   v.page_tokens = c->page_tokens;
   v.page_units = c->page_tokens / HQ_KV4_UNIT;
+  v.page_shift = pow2_shift(c->page_tokens);
   v.n_kv = c->n_kv_heads;
+  v.kv_shift = pow2_shift(c->n_kv_heads);
   v.table = c->d_table;
   v.n_seqs = c->n_seqs;
   v.width = c->table_width;

@@ -10,6 +10,7 @@
 #include "hq_device.cuh"
 #include "hq_kv4.h"
 #include "hq_kv4_io.cuh"
+#include "hq_launch.cuh"
 #include "hq_umma.cuh"
 
 namespace hq {
@@ -41,10 +42,10 @@ struct Shape {
 
 // Work of one (sequence, head, row tile) beyond its units, in units: the
 // blocks split the batch into equal pieces of units + kSegmentCost.
-constexpr int kSegmentCost = 8, kMinPiece = 24;
+constexpr int kSegmentCost = 24, kMinPiece = 40;
 // A batch whose longest sequence is this short is not split inside sequences:
 // a join would take longer than the units it spreads.
-constexpr int kWholeSpan = 48;
+constexpr int kWholeSpan = 64;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -177,10 +178,6 @@ __device__ __forceinline__ void finish_stats(const Kv4AttnArgs &a, int b, int h,
   if (a.mass_out != nullptr) a.row_lse[((int64_t)b * a.c.n_kv + h) * a.R + row] = l2;
 }
 
-__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {   // both positive
-  return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
-}
-
 // Where a block's piece of the batch begins, and the piece's length: the
 // (sequence, head, row tile) triples laid end to end, each of its units +
 // kSegmentCost, are cut into equal pieces.
@@ -220,7 +217,7 @@ struct Walk {
         b_begin = b_end;
         continue;
       }
-      const int pair = (int)divide(cur - b_begin, span1);       // head and row tile of sequence b
+      const int pair = (int)kv4_divide(cur - b_begin, span1);       // head and row tile of sequence b
       const int64_t at = b_begin + (int64_t)pair * span1;    // where the pair begins
       s->b = b;
       s->pair = pair;
@@ -254,7 +251,7 @@ __device__ Piece find_piece(const Kv4AttnArgs &a) {
       top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
     }
     const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
-    const int64_t even = divide(total + gridDim.x - 1, gridDim.x), least = top <= kWholeSpan ? top : kMinPiece;
+    const int64_t even = kv4_divide(total + gridDim.x - 1, gridDim.x), least = top <= kWholeSpan ? top : kMinPiece;
     p.size = even > least ? even : least;
     p.begin = (int64_t)blockIdx.x * p.size;
     p.end = p.begin + p.size < total ? p.begin + p.size : total;
@@ -287,7 +284,7 @@ __device__ Piece find_piece(const Kv4AttnArgs &a) {
     top = max(top, s_top[w]);
   }
   top += kSegmentCost;
-  const int64_t even = divide(total + gridDim.x - 1, gridDim.x), least = top <= kWholeSpan ? top : kMinPiece;
+  const int64_t even = kv4_divide(total + gridDim.x - 1, gridDim.x), least = top <= kWholeSpan ? top : kMinPiece;
   p.size = even > least ? even : least;
   p.begin = (int64_t)blockIdx.x * p.size;
   p.end = p.begin + p.size < total ? p.begin + p.size : total;
@@ -353,7 +350,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
   // copies: 16 bytes a lane; V's 16-byte chunks are permuted inside their
   // 128-byte rows so that the reads of a warp touch all banks
   const uint32_t cp_v = kUnitV + (lane >> 3) * 128 + (((lane & 7) ^ (2 * (lane >> 3))) * 16);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  follow_launch();
   const uint32_t sign_bits = __ldg(a.c.signs + ((tid & 7) >> 1)) >> (16 * (tid & 1));
   const Piece piece = find_piece(a);
   Walk walk{piece.begin, piece.end, piece.b_begin, piece.b};
@@ -708,7 +705,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
     if (!whole && seg.u_lo == 0) {               // begun here, ended by later blocks
       join_b = seg.b;
       join_pair = seg.pair;
-      join_count = (int)(divide(seg.at_end - 1, piece.size) - blockIdx.x);
+      join_count = (int)(kv4_divide(seg.at_end - 1, piece.size) - blockIdx.x);
     }
     if (tid < 8 * kRows) {
       float M = kNoMax, MW = kNoMax, L = 0.0f;
@@ -776,7 +773,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, i
   __shared__ __align__(16) float s_tr[4 * kTrTile];
   __shared__ __align__(16) float s_x[kJoinThreads / 32][kTile];
   __shared__ float s_l[kJoinThreads / 32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");          // launched while that kernel runs
+  follow_launch();                               // launched while that kernel runs
   const int4 job = reinterpret_cast<const int4 *>(a.joins)[blockIdx.x];
   const int rr = blockIdx.y, h = job.z / a.row_tiles, row = (job.z % a.row_tiles) * rows + rr;
   if (job.x == 0 || row >= a.R) return;
@@ -832,9 +829,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, i
 __global__ void __launch_bounds__(256) kv4_mass_kernel(Kv4AttnArgs a) {
   const int h = blockIdx.y, b = blockIdx.z;
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  follow_launch();
   bool bad;
   const int len = kv4_length(a.c, a.lengths, b, &bad);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (t >= len) return;
   const int64_t head = (int64_t)b * a.c.n_kv + h, cap = a.c.capacity();
   float s = 0.0f;
@@ -864,22 +861,6 @@ int resident_blocks() {
   return n;
 }
 
-// A launch that may begin while the one before it in the stream still runs;
-// its kernel waits for that one's end before it reads what that one wrote.
-template <class... Params, class... Args>
-int launch_behind(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t st, Args... args) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...) == cudaSuccess ? 0 : 1;
-}
-
 template <int NC, bool CAP, bool MASS>
 int launch_attn(const Kv4AttnArgs &a, cudaStream_t st) {
   int grid = resident_blocks<NC, CAP, MASS>();
@@ -890,9 +871,9 @@ int launch_attn(const Kv4AttnArgs &a, cudaStream_t st) {
   int64_t most = ((a.c.capacity() / kUnit + kSegmentCost) * pairs + kMinPiece - 1) / kMinPiece;
   if (most < pairs) most = pairs;
   if (most < grid) grid = (int)most;
-  kv4_attn_kernel<NC, CAP, MASS><<<grid, kAttnThreads, Shape<NC>::smem, st>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return 1;
-  return launch_behind(kv4_join_kernel, dim3((unsigned)grid, Shape<NC>::rows), kJoinThreads, st, a,
+  if (launch_behind(kv4_attn_kernel<NC, CAP, MASS>, dim3((unsigned)grid), kAttnThreads, Shape<NC>::smem, st, a) != 0)
+    return 1;
+  return launch_behind(kv4_join_kernel, dim3((unsigned)grid, Shape<NC>::rows), kJoinThreads, 0, st, a,
                        (int)Shape<NC>::rows);
 }
 
@@ -917,7 +898,7 @@ int launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t st) {
   if (rc != 0) return rc;
   if (a.mass_out != nullptr && a.c.capacity() > 0)
     return launch_behind(kv4_mass_kernel, dim3((unsigned)((a.c.capacity() + 255) / 256), (unsigned)a.c.n_kv,
-                                               (unsigned)a.c.n_seqs), 256, st, a);
+                                               (unsigned)a.c.n_seqs), 256, 0, st, a);
   return 0;
 }
 

@@ -8,11 +8,12 @@
 
 namespace hq {
 
-__device__ __forceinline__ void unpack16(int kind, const uint4 &w, float *x) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// 8 packed 16-bit values to fp32 (exact).
+template <int KIND>
+__device__ __forceinline__ void unpack8(const uint32_t u[4], float *x) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (kind == HQ_T_BF16) {
+    if constexpr (KIND == HQ_T_BF16) {
       x[2 * i] = __uint_as_float(u[i] << 16);
       x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
     } else {
@@ -23,38 +24,64 @@ __device__ __forceinline__ void unpack16(int kind, const uint4 &w, float *x) {
   }
 }
 
-// The lane's 16 values of a row that starts at element `at` of `base`;
-// KIND is HQ_T_BF16, HQ_T_F16 or HQ_T_F32 (every conversion is exact).
+// The lane's 16 values of a row, as they are in memory: 8 words of 16-bit or
+// 16 of 32-bit values, from element `at` of `base` on.
 template <int KIND>
-__device__ __forceinline__ void load_row16(const void *base, int64_t at, int r, bool vec, float x[16]) {
-  if constexpr (KIND == HQ_T_F32) {
-    const float *p = static_cast<const float *>(base) + at + 16 * r;
-    if (vec) {
+struct Row16 {
+  static constexpr int words = KIND == HQ_T_F32 ? 16 : 8;
+  uint32_t w[words];
+  __device__ __forceinline__ void load(const void *base, int64_t at, int r, bool vec) {
+    if constexpr (KIND == HQ_T_F32) {
+      const uint32_t *p = static_cast<const uint32_t *>(base) + at + 16 * r;
+      if (vec) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(p) + c);
-        x[4 * c] = v.x; x[4 * c + 1] = v.y; x[4 * c + 2] = v.z; x[4 * c + 3] = v.w;
+        for (int c = 0; c < 4; ++c) put4(4 * c, __ldg(reinterpret_cast<const uint4 *>(p) + c));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = __ldg(p + i);
       }
     } else {
+      const uint16_t *p = static_cast<const uint16_t *>(base) + at + 16 * r;
+      if (vec) {
+        put4(0, __ldg(reinterpret_cast<const uint4 *>(p)));
+        put4(4, __ldg(reinterpret_cast<const uint4 *>(p) + 1));
+      } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __ldg(p + i);
+        for (int i = 0; i < 8; ++i) w[i] = (uint32_t)__ldg(p + 2 * i) | ((uint32_t)__ldg(p + 2 * i + 1) << 16);
+      }
     }
-  } else {
-    const uint16_t *p = static_cast<const uint16_t *>(base) + at + 16 * r;
-    uint4 w[2];
-    if (vec) {
-      w[0] = __ldg(reinterpret_cast<const uint4 *>(p));
-      w[1] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < words; ++i) w[i] = 0u;
+  }
+  // The values in fp32, those whose bit of `flips` (bit i: value i) is set negated.
+  __device__ __forceinline__ void get(uint32_t flips, float x[16]) const {
+    if constexpr (KIND == HQ_T_F32) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(w[i] ^ ((flips << (31 - i)) & 0x80000000u));
     } else {
       uint32_t u[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = (uint32_t)__ldg(p + 2 * i) | ((uint32_t)__ldg(p + 2 * i + 1) << 16);
-      w[0] = make_uint4(u[0], u[1], u[2], u[3]);
-      w[1] = make_uint4(u[4], u[5], u[6], u[7]);
+      for (int i = 0; i < 8; ++i) {                // bits 2 i and 2 i + 1 to bits 15 and 31
+        u[i] = w[i] ^ (((flips << (15 - 2 * i)) & 0x8000u) | ((flips << (30 - 2 * i)) & 0x80000000u));
+      }
+      unpack8<KIND>(u, x);
+      unpack8<KIND>(u + 4, x + 8);
     }
-    unpack16(KIND, w[0], x);
-    unpack16(KIND, w[1], x + 8);
   }
+
+ private:
+  __device__ __forceinline__ void put4(int i, uint4 v) {
+    w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+  }
+};
+
+template <int KIND>
+__device__ __forceinline__ void load_row16(const void *base, int64_t at, int r, bool vec, float x[16]) {
+  Row16<KIND> row;
+  row.load(base, at, r, vec);
+  row.get(0u, x);
 }
 
 // fp32 -> two 16-bit values in one word, each rounded to nearest even.
