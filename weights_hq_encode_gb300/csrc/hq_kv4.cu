@@ -20,21 +20,74 @@ __device__ __forceinline__ int kv4_chunk(int which, int tok, int r) {
   return which == 0 ? tok * 64 + r * 8 : kUnitV + (tok >> 1) * 128 + r * 16 + (tok & 1) * 8;
 }
 
-// Two values' codes added up into 4-bit fields: floor(fl(fl(z inv) + 8)), the
-// floor by a sum with 2^23 rounded towards zero.  |z| inv is at most 7.5
-// (1 + 2^-8) and a few units, so the codes are 0 .. 15 as they are.
-__device__ __forceinline__ void add_codes(uint32_t &w, float z0, float z1, uint64_t inv, int at) {
+// fwht128_t8_smem without its last step back to the lanes' own dimensions: y[m]
+// is coordinate r + 8 m.  The caller orders calls on one table by __syncwarp.
+__device__ __forceinline__ void fwht128_t8_columns(float x[16], float *tile, int r, float y[16]) {
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (!(j & h)) bfly2(x[j], x[j + 8], x[j + h], x[j + h + 8]);
+  }
+  float2 *const out = reinterpret_cast<float2 *>(tile + 2 * r);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)                    // coordinates 16 r + j, 16 r + j + 8
+    out[j * (kTrRow / 2)] = make_float2(__fadd_rn(x[j], x[j + 8]), __fsub_rn(x[j], x[j + 8]));
+  __syncwarp();
+  const float4 *const in = reinterpret_cast<const float4 *>(tile + kTrRow * r);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float4 v = in[q];
+    y[4 * q] = v.x; y[4 * q + 1] = v.y; y[4 * q + 2] = v.z; y[4 * q + 3] = v.w;
+  }
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (!(j & h)) bfly2(y[2 * j], y[2 * j + 1], y[2 * (j + h)], y[2 * (j + h) + 1]);
+  }
+}
+
+// Two values' codes into field `at` of two words of 4-bit fields:
+// floor(fl(fl(z inv) + 8)), the floor by a sum with 2^23 rounded towards zero.
+// |z| inv is at most 7.5 (1 + 2^-8) and a few units, so the codes are 0 .. 15 as
+// they are; 2^23's own bits are taken out at the end.
+__device__ __forceinline__ void add_codes(uint32_t &even, uint32_t &odd, float z0, float z1, uint64_t inv, int at) {
   uint64_t t = add2(mul2(pk2(z0, z1), inv), pk2(8.0f, 8.0f));
   asm("add.rz.f32x2 %0, %1, %2;" : "=l"(t) : "l"(t), "l"(pk2(8388608.0f, 8388608.0f)));
   float a, b;
   upk2(t, a, b);
-  w += (__float_as_uint(a) << (4 * at)) + (__float_as_uint(b) << (4 * at + 4));
+  even += __float_as_uint(a) << (4 * at);
+  odd += __float_as_uint(b) << (4 * at);
+}
+
+// Codes of coordinates r + 8 m, fields i of even and odd for m = 2 i and 2 i + 1,
+// to the row's words 2 r and 2 r + 1 (coordinates 16 r .. 16 r + 15): a
+// transposition over the row's 8 lanes in four exchanges.  A lane first joins its
+// nibbles with its neighbour's (even lanes take the even m) to bytes r / 2 of
+// 8 words, then bytes go over by halves: words by distance 4, 2 and 1 lanes.
+__device__ __forceinline__ uint2 words_of_columns(uint32_t even, uint32_t odd, int r) {
+  const bool q = r & 1, b1 = r & 2, b2 = r & 4;
+  const uint32_t got = __shfl_xor_sync(0xffffffffu, q ? even : odd, 1);
+  const uint32_t lo = q ? got : even, hi = q ? odd : got;
+  const uint32_t x = (lo & 0x0F0F0F0Fu) | ((hi & 0x0F0F0F0Fu) << 4);           // items 0, 2, 4, 6
+  const uint32_t y = ((lo >> 4) & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u);           // items 1, 3, 5, 7
+  const uint32_t l = __byte_perm(x, y, 0x5410), h = __byte_perm(x, y, 0x7632);  // items 0 2 1 3, 4 6 5 7
+  const uint32_t k1 = b2 ? h : l, g1 = __shfl_xor_sync(0xffffffffu, b2 ? l : h, 4);
+  const uint32_t a = __byte_perm(k1, g1, 0x6240), c = __byte_perm(k1, g1, 0x7351);
+  const uint32_t k2 = b1 ? c : a, g2 = __shfl_xor_sync(0xffffffffu, b1 ? a : c, 2);
+  const uint32_t f = __byte_perm(k2, g2, 0x5410), g = __byte_perm(k2, g2, 0x7632);
+  const uint32_t k3 = q ? g : f, g3 = __shfl_xor_sync(0xffffffffu, q ? f : g, 1);
+  // byte k came from the lanes r / 2 ^ {0, 2, 1, 3}[k]
+  const uint32_t p = r >> 1;
+  const uint32_t order = p == 0 ? 0x3120u : p == 1 ? 0x1302u : p == 2 ? 0x2031u : 0x0213u;
+  return make_uint2(__byte_perm(q ? g3 : k3, 0u, order), __byte_perm(q ? k3 : g3, 0u, order));
 }
 
 // Codes K and V rows, 8 lanes an entry as the codec's kernels hold a tile
 // (lane r: dimensions 16 r .. 16 r + 15), so that the transform is the codec's,
-// its stages in the codec's order, and a lane's 16 codes are the 8 bytes it
-// stores.  Bound by instructions: about 220 a warp for 4 rows.
+// its stages in the codec's order.  It is not taken back to the lanes'
+// dimensions in fp32: the codes are, 8 bytes a lane instead of 64.
 template <int KIND>
 __global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(Kv4RowArgs a) {
   __shared__ __align__(16) float s_tr[(kRowsThreads / 8) * kTrTile];
@@ -62,9 +115,10 @@ __global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(Kv4RowArgs 
   const int tok = place % kUnit;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    float y[16];
-    rows[which].get(mw, y);
-    fwht128_t8(y, s_tr + tl * kTrTile, r);
+    float x[16], y[16];
+    rows[which].get(mw, x);
+    if (which == 1) __syncwarp();                // the table is free
+    fwht128_t8_columns(x, s_tr + tl * kTrTile, r, y);
     // the largest magnitude as an integer: an infinity or a NaN is above every finite value
     uint32_t top = 0;
 #pragma unroll
@@ -76,14 +130,14 @@ __global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(Kv4RowArgs 
     if (sf < 0x1p-126f) sf = 0.0f;               // no subnormal scales: the row is zero
     const float inv = sf > 0.0f ? __fdiv_rn(1.0f, __fmul_rn(sf, kRoot128)) : 0.0f;
     const uint64_t inv2 = pk2(inv, inv);
-    // 2^23's own bits, shifted to every field of a word
-    constexpr uint32_t kOnes = 0x4B000000u * 0x11111111u;
-    uint32_t w[2] = {0u - kOnes, 0u - kOnes};
+    constexpr uint32_t kOnes = 0x4B000000u * 0x11111111u;      // 2^23's bits in every field
+    uint32_t even = 0u - kOnes, odd = 0u - kOnes;
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) add_codes(w[j >> 3], y[j], y[j + 1], inv2, j & 7);
+    for (int i = 0; i < 8; ++i) add_codes(even, odd, y[2 * i], y[2 * i + 1], inv2, i);
+    uint2 w = words_of_columns(even, odd, r);
     if (place == kNoPlace) continue;
-    if (sf == 0.0f) w[0] = w[1] = 0x88888888u;
-    *reinterpret_cast<uint2 *>(unit + kv4_chunk(which, tok, r)) = make_uint2(w[0], w[1]);
+    if (sf == 0.0f) w.x = w.y = 0x88888888u;
+    *reinterpret_cast<uint2 *>(unit + kv4_chunk(which, tok, r)) = w;
     if (r == 0) {
       if (!finite) atomicOr(a.status, (uint32_t)HQ_ERR_RANGE);
       reinterpret_cast<uint16_t *>(unit + (which == 0 ? kUnitKs : kUnitVs))[tok] =
