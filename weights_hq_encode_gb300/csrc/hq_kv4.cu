@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(Kv4RowArgs 
     rows[0].zero();
     rows[1].zero();
   }
-  const uint32_t mw = __ldg(a.c.signs + (r >> 1)) >> (16 * (r & 1));
+  const uint32_t mw = (__ldg(a.c.signs + (r >> 1)) >> (16 * (r & 1))) & 0xFFFFu;
   unsigned char *const unit = kv4_unit(a.c, place);
   const int tok = place % kUnit;
 #pragma unroll
@@ -119,14 +119,25 @@ __global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(Kv4RowArgs 
     rows[which].get(mw, x);
     if (which == 1) __syncwarp();                // the table is free
     fwht128_t8_columns(x, s_tr + tl * kTrTile, r, y);
-    // the largest magnitude as an integer: an infinity or a NaN is above every finite value
-    uint32_t top = 0;
+    // the largest magnitude; the maximum passes over a NaN, so a sum of 0 x every value looks for
+    // NaNs and infinities
+    float top = 0.0f;
+    uint64_t odd_one = 0;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+    for (int j = 0; j < 16; j += 2) {
+      top = fmaxf(fmaxf(top, fabsf(y[j])), fabsf(y[j + 1]));
+      odd_one = fma2(pk2(y[j], y[j + 1]), 0ull, odd_one);
+    }
+    float n0, n1;
+    upk2(odd_one, n0, n1);
+    top = __fadd_rn(top, __fadd_rn(n0, n1));     // NaN if there was one
 #pragma unroll
-    for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const bool finite = top < 0x7F800000u;
-    float sf = finite ? __bfloat162float(__float2bfloat16_rn(__fmul_rn(__uint_as_float(top), kAbsToScale))) : 0.0f;
+    for (int d = 1; d < 8; d <<= 1) {
+      const float o = __shfl_xor_sync(0xffffffffu, top, d);
+      top = top > o || top != top ? top : o;     // NaN wins
+    }
+    const bool finite = top < INFINITY;
+    float sf = finite ? __bfloat162float(__float2bfloat16_rn(__fmul_rn(top, kAbsToScale))) : 0.0f;
     if (sf < 0x1p-126f) sf = 0.0f;               // no subnormal scales: the row is zero
     const float inv = sf > 0.0f ? __fdiv_rn(1.0f, __fmul_rn(sf, kRoot128)) : 0.0f;
     const uint64_t inv2 = pk2(inv, inv);
@@ -317,14 +328,19 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *s_w, int fl
   return v + (warp > 0 ? before : 0u);
 }
 
-// The positions that one head of one sequence keeps.  The threshold mass is
-// found digit by digit (11, 11 and 10 bits of the ordered key, most
-// significant first) from histograms in shared memory; a last pass in order
-// compacts what lies above it and the first of what equals it.
-__global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a) {
+// The positions that one head of one sequence keeps.  The competing masses'
+// keys are read once (the first `cached` into shared memory) for their least and
+// largest; the threshold is found digit by digit of (key - least), 11 bits at a
+// time from the top of that range, by histograms in shared memory; a last pass in
+// order compacts what lies above it and the first of what equals it.  Digits of the
+// range and not of the key: masses of a few binary orders spread over all 2048 bins, where
+// the key's own top bits are a handful of values and their atomics one
+// behind another (28 us for 128 heads of 29000 tokens).
+__global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a, int cached) {
+  extern __shared__ __align__(16) uint32_t s_keys[];
   __shared__ uint32_t s_hist[kSelBins];
   __shared__ uint32_t s_w[64];
-  __shared__ uint32_t s_digit, s_above;
+  __shared__ uint32_t s_digit, s_above, s_least, s_most;
   follow_launch();
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   bool bad;
@@ -339,17 +355,41 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
   for (int i = need + tid; i < keep; i += kSelThreads) kept[i] = old + i - need;
   for (int i = keep + tid; i < a.budget; i += kSelThreads) kept[i] = -1;
   if (need == 0) return;
-  uint32_t prefix = 0, want = (uint32_t)need;    // digits found; how many to keep among their equals
+  if (tid == 0) {
+    s_least = 0xFFFFFFFFu;
+    s_most = 0u;
+  }
+  __syncthreads();
+  uint32_t least = 0xFFFFFFFFu, most = 0u;
+#pragma unroll 8
+  for (int i = tid; i < old; i += kSelThreads) {
+    const uint32_t key = mass_key(__ldg(mass + i));
+    if (i < cached) s_keys[i] = key;
+    least = min(least, key);
+    most = max(most, key);
+  }
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if ((tid & 31) == 0) {
+    atomicMin(&s_least, least);
+    atomicMax(&s_most, most);
+  }
+  __syncthreads();
+  least = s_least;
+  const auto key_of = [&](int i) { return (i < cached ? s_keys[i] : mass_key(__ldg(mass + i))) - least; };
+  int shift = 32 - __clz((int)(s_most - least));  // bits of the range: those below `shift` are to be found
+  uint32_t prefix = 0, want = (uint32_t)need;     // digits found; how many to keep among their equals
   int flip = 0;
-  for (int digit = 0; digit < 3; ++digit) {
-    const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
-    const uint32_t bins = digit == 2 ? 1024u : 2048u;
-    const uint32_t above_mask = digit == 0 ? 0u : digit == 1 ? 0xFFE00000u : 0xFFFFFC00u;
+  while (shift > 0) {
+    const int bits = min(shift, 11);
+    const uint32_t found = shift == 32 ? 0u : 0xFFFFFFFFu << shift;   // bits of the digits found
+    shift -= bits;
     for (int i = tid; i < kSelBins; i += kSelThreads) s_hist[i] = 0;
     __syncthreads();
+#pragma unroll 4
     for (int i = tid; i < old; i += kSelThreads) {
-      const uint32_t key = mass_key(__ldg(mass + i));
-      if ((key & above_mask) == prefix) atomicAdd(&s_hist[(key >> shift) & (bins - 1)], 1u);
+      const uint32_t key = key_of(i);
+      if ((key & found) == prefix) atomicAdd(&s_hist[(key >> shift) & ((1u << bits) - 1)], 1u);
     }
     __syncthreads();
     // bins from the largest down, two a thread
@@ -357,7 +397,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
     uint32_t total;
     const uint32_t end = block_scan(c0 + c1, s_w, flip, &total), begin = end - c0 - c1;
     flip ^= 1;
-    if (begin < want && want <= end) {           // exactly one thread
+    if (begin < want && want <= end) {            // exactly one thread
       const bool first = want <= begin + c0;
       s_digit = first ? d0 : d0 - 1;
       s_above = first ? begin : begin + c0;
@@ -372,7 +412,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int i = base + 4 * tid + j;
-      key[j] = i < old ? mass_key(__ldg(mass + i)) : 0u;
+      key[j] = i < old ? key_of(i) : 0u;
       if (i < old) c += key[j] > prefix ? 1u : key[j] == prefix ? 0x10000u : 0u;
     }
     uint32_t total;
@@ -475,7 +515,14 @@ int launch_kv4_read(const Kv4RowArgs &a, cudaStream_t st) {
 }
 
 int launch_kv4_evict(const Kv4EvictArgs &a, cudaStream_t st) {
-  if (launch_behind(kv4_select_kernel, dim3((unsigned)a.src.n_kv, (unsigned)a.src.n_seqs), kSelThreads, 0, st, a) != 0)
+  // keys in shared memory, as many as a block may have
+  constexpr int kMostKeys = 48 * 1024;
+  const int cached = a.src.capacity() < kMostKeys ? (int)a.src.capacity() : kMostKeys;
+  if (cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4) !=
+      cudaSuccess)
+    return 1;
+  if (launch_behind(kv4_select_kernel, dim3((unsigned)a.src.n_kv, (unsigned)a.src.n_seqs), kSelThreads,
+                    (size_t)cached * 4, st, a, cached) != 0)
     return 1;
   if (a.src.capacity() == 0) return 0;           // no tokens to move
   const int64_t most = a.budget < a.src.capacity() ? a.budget : a.src.capacity();

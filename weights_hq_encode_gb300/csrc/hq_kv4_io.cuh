@@ -55,17 +55,17 @@ struct Row16 {
 #pragma unroll
     for (int i = 0; i < words; ++i) w[i] = 0u;
   }
-  // The values in fp32, those whose bit of `flips` (bit i: value i) is set negated.
+  // The values in fp32, those whose bit of `flips` (bits 0-15) is set negated.
   __device__ __forceinline__ void get(uint32_t flips, float x[16]) const {
     if constexpr (KIND == HQ_T_F32) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(w[i] ^ ((flips << (31 - i)) & 0x80000000u));
     } else {
       uint32_t u[8];
+      // bits 2 i and 2 i + 1 of flips at bits 15 and 31 of the 64-bit word shifted by 2 i
+      const uint32_t low = (flips << 15) | (flips << 30 & 0x80000000u), high = flips >> 2;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {                // bits 2 i and 2 i + 1 to bits 15 and 31
-        u[i] = w[i] ^ (((flips << (15 - 2 * i)) & 0x8000u) | ((flips << (30 - 2 * i)) & 0x80000000u));
-      }
+      for (int i = 0; i < 8; ++i) u[i] = w[i] ^ (__funnelshift_r(low, high, 2 * i) & 0x80008000u);
       unpack8<KIND>(u, x);
       unpack8<KIND>(u + 4, x + 8);
     }
