@@ -518,8 +518,9 @@ int launch_kv4_evict(const Kv4EvictArgs &a, cudaStream_t st) {
   // keys in shared memory, as many as a block may have
   constexpr int kMostKeys = 48 * 1024;
   const int cached = a.src.capacity() < kMostKeys ? (int)a.src.capacity() : kMostKeys;
-  if (cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4) !=
-      cudaSuccess)
+  if (cached > 8 * 1024 &&                       // with s_hist above what a block has unasked
+      cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4) !=
+          cudaSuccess)
     return 1;
   if (launch_behind(kv4_select_kernel, dim3((unsigned)a.src.n_kv, (unsigned)a.src.n_seqs), kSelThreads,
                     (size_t)cached * 4, st, a, cached) != 0)

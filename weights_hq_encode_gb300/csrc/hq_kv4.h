@@ -58,6 +58,7 @@ struct Kv4AttnArgs {
   float *lse;               // [n_seqs][q_len][Hq] or nullptr
   const float *mass_in;     // [n_seqs][n_kv][capacity] or nullptr
   float *mass_out;          // the same, or nullptr: no mass
+  int whole;                // set by the launch: a block a (sequence, head, row tile), no joins
   int row_tiles;            // tiles of rows a KV head has
   float *part;              // workspace: sums that several blocks share
   float *stat;              // workspace: their references and sums of weights

@@ -240,6 +240,16 @@ __device__ Piece find_piece(const Kv4AttnArgs &a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.c.n_seqs;
   Piece p;
+  if (a.whole) {                                 // block i takes the i-th (sequence, head, row tile)
+    const int pairs = a.c.n_kv * a.row_tiles;
+    p.b = blockIdx.x / pairs;
+    const int units = units_of(a, p.b);
+    p.size = units + kSegmentCost;
+    p.b_begin = 0;                               // laid out from this sequence on
+    p.begin = (int64_t)(blockIdx.x - p.b * pairs) * p.size;
+    p.end = units == 0 ? p.begin : p.begin + p.size;
+    return p;
+  }
   if (B <= 32) {                                 // every warp by itself, a sequence a lane
     const int64_t span = lane < B ? span_of(a, lane) : 0;
     int top = lane < B ? units_of(a, lane) + kSegmentCost : 0;
@@ -745,7 +755,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
     }
     __syncthreads();                             // the ring and the statistics are free
   }
-  if (tid == 0) reinterpret_cast<int4 *>(a.joins)[blockIdx.x] = make_int4(join_count, join_b, join_pair, 0);
+  if (tid == 0 && !a.whole) reinterpret_cast<int4 *>(a.joins)[blockIdx.x] = make_int4(join_count, join_b, join_pair, 0);
   // rows of sequences without tokens, and lengths out of range
   for (int sb = blockIdx.x; sb < a.c.n_seqs; sb += gridDim.x) {
     bool bad_len;
@@ -871,8 +881,12 @@ int launch_attn(const Kv4AttnArgs &a, cudaStream_t st) {
   int64_t most = ((a.c.capacity() / kUnit + kSegmentCost) * pairs + kMinPiece - 1) / kMinPiece;
   if (most < pairs) most = pairs;
   if (most < grid) grid = (int)most;
-  if (launch_behind(kv4_attn_kernel<NC, CAP, MASS>, dim3((unsigned)grid), kAttnThreads, Shape<NC>::smem, st, a) != 0)
+  Kv4AttnArgs w = a;
+  w.whole = pairs <= grid && a.c.capacity() / kUnit + kSegmentCost <= kWholeSpan;
+  if (w.whole) grid = (int)pairs;
+  if (launch_behind(kv4_attn_kernel<NC, CAP, MASS>, dim3((unsigned)grid), kAttnThreads, Shape<NC>::smem, st, w) != 0)
     return 1;
+  if (w.whole) return 0;                         // nothing to join
   return launch_behind(kv4_join_kernel, dim3((unsigned)grid, Shape<NC>::rows), kJoinThreads, 0, st, a,
                        (int)Shape<NC>::rows);
 }

@@ -277,35 +277,40 @@ _KINDS = {torch.bfloat16: HQ_T_BF16, torch.float32: HQ_T_F32, torch.float16: HQ_
 
 def _on(t, cache, name, dtype, shape=None):
     """The address of a contiguous tensor of the given dtype (and shape) on the cache's device."""
+    try:
+        if (t.dtype is dtype and t.get_device() == cache._index and t.is_contiguous() and
+                (shape is None or t.shape == shape)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {dtype} tensor")
-    if t.device != cache._device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {cache._device}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
-    return t.data_ptr()
+    if t.get_device() != cache._index:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache._pages.device}")
+    raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
 def _rows_on(t, cache, name, shape):
-    """Address and kind of a tensor of rows: any strides, the last dimension contiguous."""
+    """Address, kind and strides of a tensor of rows: any outer strides, contiguous rows."""
     if not isinstance(t, torch.Tensor) or t.dtype not in _KINDS:
         raise TypeError(f"{name} must be a bf16, fp16 or fp32 tensor")
-    if t.device != cache._device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {cache._device}")
-    if tuple(t.shape) != shape or t.stride(-1) != 1:
-        raise ValueError(f"{name} must have the shape {shape} with contiguous rows, "
-                         f"not {tuple(t.shape)} with strides {t.stride()}")
-    return t.data_ptr(), _KINDS[t.dtype]
+    if t.get_device() != cache._index:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache._pages.device}")
+    stride = t.stride()
+    if t.shape != shape or stride[-1] != 1:
+        raise ValueError(f"{name} must have the shape {tuple(shape)} with contiguous rows, "
+                         f"not {tuple(t.shape)} with strides {stride}")
+    return t.data_ptr(), _KINDS[t.dtype], stride
 
 
 def _launch(cache, call, stream, *args) -> int:
     """A library call with the cache's device current, on `stream` or that device's current one."""
-    if stream is None:
-        stream = torch.cuda.current_stream(cache._device)
-    if torch.cuda.current_device() == cache._device.index:
-        return call(*args, stream.cuda_stream)
-    with torch.cuda.device(cache._device):
-        return call(*args, stream.cuda_stream)
+    index = cache._index
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        return call(*args, raw)
+    with torch.cuda.device(index):
+        return call(*args, raw)
 
 
 def hq_kv4_page_bytes(n_kv_heads: int, page_tokens: int) -> int:
@@ -331,7 +336,7 @@ def make_kv4_cache(pages: torch.Tensor, table: torch.Tensor, page_tokens: int, n
         raise ValueError("expected whole pages, a table [n_seqs, width] and 4 words of signs")
     c = hq_kv4_cache(pages.data_ptr(), pages.numel() // page, page_tokens, n_kv_heads,
                      table.data_ptr(), table.shape[0], table.shape[1], signs.data_ptr())
-    c._pages, c._table, c._signs, c._device = pages, table, signs, pages.device
+    c._pages, c._table, c._signs, c._index = pages, table, signs, pages.get_device()
     c._ref = ctypes.byref(c)
     return c
 
@@ -342,13 +347,13 @@ def hq_kv4_append(cache: hq_kv4_cache, k: torch.Tensor, v: torch.Tensor, seq: to
     cache at sequences `seq` and positions `pos` (int32 [n_tokens])."""
     n = seq.numel()
     shape = (n, cache.n_kv_heads, HQ_TILE)
-    kp, kind = _rows_on(k, cache, "k", shape)
-    vp, vkind = _rows_on(v, cache, "v", shape)
+    kp, kind, ks = _rows_on(k, cache, "k", shape)
+    vp, vkind, vs = _rows_on(v, cache, "v", shape)
     if kind != vkind:
         raise TypeError("k and v must have one dtype")
-    return _launch(cache, _lib.hq_kv4_append, stream, cache._ref, kp, vp, kind, k.stride(0),
-                   k.stride(1), v.stride(0), v.stride(1), _on(seq, cache, "seq", torch.int32),
-                   _on(pos, cache, "pos", torch.int32, tuple(seq.shape)), n,
+    return _launch(cache, _lib.hq_kv4_append, stream, cache._ref, kp, vp, kind, ks[0], ks[1],
+                   vs[0], vs[1], _on(seq, cache, "seq", torch.int32),
+                   _on(pos, cache, "pos", torch.int32, seq.shape), n,
                    _on(status, cache, "status", torch.int32))
 
 
@@ -357,14 +362,14 @@ def hq_kv4_read(cache: hq_kv4_cache, seq: torch.Tensor, pos: torch.Tensor, k: to
     """Writes the rows of tokens (seq, pos) to k, v [n_tokens, n_kv_heads, 128]."""
     n = seq.numel()
     shape = (n, cache.n_kv_heads, HQ_TILE)
-    kp, kind = _rows_on(k, cache, "k", shape)
-    vp, vkind = _rows_on(v, cache, "v", shape)
+    kp, kind, ks = _rows_on(k, cache, "k", shape)
+    vp, vkind, vs = _rows_on(v, cache, "v", shape)
     if kind != vkind:
         raise TypeError("k and v must have one dtype")
     return _launch(cache, _lib.hq_kv4_read, stream, cache._ref,
                    _on(seq, cache, "seq", torch.int32),
-                   _on(pos, cache, "pos", torch.int32, tuple(seq.shape)), n, kp, vp, kind,
-                   k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                   _on(pos, cache, "pos", torch.int32, seq.shape), n, kp, vp, kind,
+                   ks[0], ks[1], vs[0], vs[1],
                    _on(status, cache, "status", torch.int32))
 
 
@@ -384,14 +389,14 @@ def hq_kv4_attention(cache: hq_kv4_cache, lengths: torch.Tensor, q: torch.Tensor
         raise TypeError("q must be a tensor [n_seqs, q_len, Hq, 128]")
     B, q_len, Hq, _ = q.shape
     shape = (cache.n_seqs, q_len, Hq, HQ_TILE)
-    qp, kind = _rows_on(q, cache, "q", shape)
+    qp, kind, qs = _rows_on(q, cache, "q", shape)
     if not isinstance(out, torch.Tensor) or out.dtype not in _KINDS:
         raise TypeError("out must be a bf16, fp16 or fp32 tensor")
     mass_shape = (cache.n_seqs, cache.n_kv_heads, cache.table_width * cache.page_tokens)
     return _launch(
         cache, _lib.hq_kv4_attention, stream, cache._ref,
-        _on(lengths, cache, "lengths", torch.int32, (cache.n_seqs,)), qp, kind, q.stride(0),
-        q.stride(1), q.stride(2), q_len, Hq, scale, cap, _on(out, cache, "out", out.dtype, shape),
+        _on(lengths, cache, "lengths", torch.int32, (cache.n_seqs,)), qp, kind, qs[0],
+        qs[1], qs[2], q_len, Hq, scale, cap, _on(out, cache, "out", out.dtype, shape),
         _KINDS[out.dtype],
         None if lse is None else _on(lse, cache, "lse", torch.float32, shape[:3]),
         None if mass_in is None else _on(mass_in, cache, "mass_in", torch.float32, mass_shape),
@@ -403,7 +408,7 @@ def hq_kv4_evict(src: hq_kv4_cache, lengths: torch.Tensor, mass: torch.Tensor, d
                  recent: int, kept: torch.Tensor, new_lengths: torch.Tensor,
                  new_mass: torch.Tensor, status: torch.Tensor, stream=None) -> int:
     """Moves the tokens that every KV head keeps (budget = kept.shape[2]) to dst's pages."""
-    if dst._device != src._device:
+    if dst._index != src._index:
         raise ValueError("src and dst must be on one device")
     if not isinstance(kept, torch.Tensor) or kept.dim() != 3:
         raise TypeError("kept must be an int32 tensor [n_seqs, n_kv_heads, budget]")
