@@ -406,11 +406,13 @@ def test_attention_on_streams_in_graphs_and_in_place_mass(hq):
     assert torch.equal(out, alone[0][0])
     first = mass.clone()
     graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
+    with torch.cuda.graph(graph):                # behind copies and a fill, as in a serving step
+        q.copy_(qs[1])
+        out.zero_()
         hq.hq_kv4_attention(C.c, C.d_lens, q, 0.1, 0.0, out, lse, mass, mass, ws, C.status)
     for lens in ([900, 333], [17, 0], [400, 333]):
         C.d_lens.copy_(ints(lens))
-        q.copy_(qs[1])
+        q.zero_()
         before = mass.clone()
         graph.replay()
         torch.cuda.synchronize()

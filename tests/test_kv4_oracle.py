@@ -147,7 +147,7 @@ def test_attention_refusals(hq):
         assert call_attention(hq, cache(hq, **bad)) == hq.HQ_ERR_INVALID, bad
     for bad in (dict(lengths=None), dict(q=None), dict(out=None), dict(ws=None), dict(status=None),
                 dict(q_kind=7), dict(out_kind=7), dict(q_len=0), dict(q_len=1 << 17), dict(Hq=0),
-                dict(Hq=3), dict(scale=float("nan")), dict(scale=float("inf")), dict(cap=-1.0),
+                dict(Hq=3), dict(scale=float("nan")), dict(scale=float("inf")), dict(cap=-1.0), dict(cap=1e-7),
                 dict(cap=float("inf")), dict(mass_in=FAKE), dict(ws_bytes=0), dict(ws=FAKE + 16),
                 dict(out=FAKE + 4), dict(q=FAKE + 1), dict(lse=FAKE + 2), dict(mass_out=FAKE + 1)):
         assert call_attention(hq, cache(hq), **bad) == hq.HQ_ERR_INVALID, bad

@@ -134,7 +134,7 @@ int hq_kv4_attention(const hq_kv4_cache *c, const int32_t *d_lengths, const void
                      size_t ws_bytes, uint32_t *d_status, hq_stream_t stream) {
   AttnSizes s;
   if (!cache_ok(c) || !kind_ok(q_kind) || !kind_ok(out_kind) || !d_status || !std::isfinite(scale) ||
-      !std::isfinite(cap) || cap < 0.0f || (d_mass_in && !d_mass_out) ||
+      !std::isfinite(cap) || cap < 0.0f || (cap > 0.0f && cap < 0x1p-20f) || (d_mass_in && !d_mass_out) ||
       !attn_sizes(c, q_len, Hq, d_mass_out != nullptr, &s))
     return HQ_ERR_INVALID;
   if (c->n_seqs == 0) return HQ_OK;

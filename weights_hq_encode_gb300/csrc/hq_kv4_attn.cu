@@ -22,11 +22,10 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLoScale = 2048.0f;
 constexpr float kNoMax = -3.0e38f;               // below every finite score
 
-// A stage of the ring is a tile of 32 tokens: two units.
-constexpr int kTileTokens = 2 * kUnit;
-constexpr int kStageBytes = 2 * kUnitBytes;
 constexpr int kWarps = 4;                        // warps of a block
 constexpr int kAttnThreads = 32 * kWarps;
+constexpr int kUnits = 2;                        // units of a tile, a warp's step: 32 tokens
+constexpr int kTileTokens = kUnits * kUnit, kStageBytes = kUnits * kUnitBytes;
 constexpr int kStages = 3;                       // tiles a warp has in its ring
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 
@@ -34,14 +33,21 @@ constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 template <int NC>
 struct Shape {
   static constexpr int rows = 4 * NC;            // query rows of a block
-  static constexpr int blocks = NC == 1 ? 3 : 2; // resident blocks a multiprocessor
+  // Resident blocks a multiprocessor: 12 warps of 168 registers, or 8 of 255.
+  // More warps of fewer registers keep parts of a tile in local memory: 16
+  // of 128 took 118 us instead of 110 for 16 x 32768 tokens of 8 heads and 4
+  // query rows, 12 of 168 with 8 rows 60 instead of 54 for 16 x 8192.
+  static constexpr int blocks = NC == 1 ? 3 : 2;
   static constexpr int q_bytes = 8 * NC * 32 * 8;   // query fragments: 8 K steps, 8 bytes a lane
   static constexpr int smem = kRingBytes + q_bytes + rows * kTrTile * 4;
   static_assert(kWarps * rows * kTile * 4 <= kRingBytes, "the warps' sums fit the ring");
 };
 
 // Work of one (sequence, head, row tile) beyond its units, in units: the
-// blocks split the batch into equal pieces of units + kSegmentCost.
+// blocks split the batch into equal pieces of units + kSegmentCost.  Rotating
+// its queries and adding up its sums takes a block about 5 us, in which it streams
+// 30 units (24 ragged sessions of 4093 tokens with 16 rows: 69 us with a cost of 8, 61
+// with 24).
 constexpr int kSegmentCost = 24, kMinPiece = 40;
 // A batch whose longest sequence is this short is not split inside sequences:
 // a join would take longer than the units it spreads.
@@ -87,7 +93,8 @@ __device__ __forceinline__ void mma16816(float d[4], uint32_t a0, uint32_t a1, u
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // Copies of the stream: read once, so they go first when L2 needs room, and
-// the code, tables and queries of the next launches stay there.
+// the code, tables and queries of the next launches stay there (the first
+// tile of a long batch's blocks begins after 5 us instead of 7).
 __device__ __forceinline__ uint64_t stream_policy() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -343,7 +350,13 @@ __device__ Piece find_piece(const Kv4AttnArgs &a) {
 // split of 4 rows fills one instruction.  The codes are unpacked in registers,
 // straight into operand fragments; that is why these are not tcgen05
 // products, whose operands would first have to be stored to shared memory as
-// fp16, four times the bytes that were read.
+// fp16, four times the bytes that were read: 1 KB of 16-bit K and V a token
+// against the 128 bytes a cycle that shared memory takes, 16 cycles for reading and
+// writing a token beside the 5 to 6 in which memory delivers it.
+//
+// 16 sequences x 32768 tokens x 8 heads, 4 query rows a head: 113 us, 4.9 TB/s,
+// 72% of the copy rate; the copies alone take 98 us, the rest is what instruction
+// issue (about 300 a warp for 16 tokens) does not hide.
 template <int NC, bool CAP, bool MASS>
 __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kernel(Kv4AttnArgs a) {
   constexpr int kRows = Shape<NC>::rows;
@@ -389,8 +402,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
       else if (a.kind == HQ_T_F16) load_q16<HQ_T_F16>(a, qa, r, x);
       else load_q16<HQ_T_BF16>(a, qa, r, x);
     }
-    const int mine = ((seg.u_hi - seg.u_lo + 1) / 2 - warp + kWarps - 1) / kWarps;
-    int unit[2] = {-1, -1};                      // unit numbers in the pool of 32 of this warp's tiles
+    const int mine = ((seg.u_hi - seg.u_lo + kUnits - 1) / kUnits - warp + kWarps - 1) / kWarps;
+    int unit[kUnits];                            // unit numbers in the pool of 32 of this warp's tiles
     int issued = 0;                              // tiles asked for
     uint32_t put = 0;                            // byte offset of the next one's stage
     const auto issue = [&]() -> uint32_t {       // the next tile into its stage; one group, maybe empty
@@ -399,8 +412,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
         if ((issued & 31) == 0) {                // the next 32 tiles' pages, a tile a lane
           bool bad = false;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int u = seg.u_lo + 2 * (warp + kWarps * (issued + lane)) + k, pj = u / a.c.page_units;
+          for (int k = 0; k < kUnits; ++k) {
+            const int u = seg.u_lo + kUnits * (warp + kWarps * (issued + lane)) + k, pj = u / a.c.page_units;
             unit[k] = -1;
             if (u < seg.u_hi) {
               const int page = __ldg(a.c.table + (int64_t)seg.b * a.c.width + pj);
@@ -411,17 +424,19 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
           }
           if (bad) atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
         }
-        const int ua = __shfl_sync(0xffffffffu, unit[0], issued & 31);
-        const int ub = __shfl_sync(0xffffffffu, unit[1], issued & 31);
         const unsigned char *base = a.c.pages + lane * 16;
-        const uint32_t k = ring_a + put + lane * 16, v = ring_a + put + cp_v;
-        cp_async_codes(ua, k, v, base + (int64_t)ua * kUnitBytes, policy);
-        cp_async_codes(ub, k + kUnitBytes, v + kUnitBytes, base + (int64_t)ub * kUnitBytes, policy);
-        const int us = lane < 4 ? ua : ub;       // scales: four lanes a unit
-        if (lane < 8 && us >= 0)
-          cp_async16(ring_a + put + kUnitKs + lane * 16 + (lane < 4 ? 0 : kUnitBytes - 64),
-                     base + (int64_t)us * kUnitBytes + kUnitKs - (lane < 4 ? 0 : 64), policy);
-        got = (ua >= 0 ? 1u : 0u) | (ub >= 0 ? 2u : 0u);
+        int us = -1;                             // scales: four lanes a unit
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+          const int uk = __shfl_sync(0xffffffffu, unit[k], issued & 31);
+          const uint32_t dst = ring_a + put + k * kUnitBytes;
+          cp_async_codes(uk, dst + lane * 16, dst + cp_v, base + (int64_t)uk * kUnitBytes, policy);
+          if ((lane >> 2) == k) us = uk;
+          got |= uk >= 0 ? 1u << k : 0u;
+        }
+        if (us >= 0)
+          cp_async16(ring_a + put + kUnitKs + lane * 16 + (lane >> 2) * (kUnitBytes - 64),
+                     base + (int64_t)us * kUnitBytes + kUnitKs - (lane >> 2) * 64, policy);
         ++issued;
         put += kStageBytes;
         if (put == kStages * kStageBytes) put = 0;
@@ -429,9 +444,9 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
       asm volatile("cp.async.commit_group;" ::: "memory");
       return got;
     };
-    uint32_t have = 0;                           // two bits a tile in the ring, the oldest lowest
+    uint32_t have = 0;                           // kUnits bits a tile in the ring, the oldest lowest
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) have |= issue() << (2 * i);
+    for (int i = 0; i < kStages - 1; ++i) have |= issue() << (kUnits * i);
     // ---- the query rows: rotated, scaled by a power of two, split, as mma fragments
     if (tid < 8 * kRows) {
 #pragma unroll
@@ -472,16 +487,14 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
       }
     }
     __syncthreads();
-    uint2 qb[8][NC];
+    // query fragments: in registers with 4 rows, else read beside every use
+    uint2 qr[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) qr[k] = s_q[k * NC * 32 + lane];
+    const auto query = [&](int k, int g) { return NC == 1 ? qr[k] : s_q[(k * NC + g) * 32 + lane]; };
     uint64_t zmul[NC];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-#pragma unroll
-      for (int g = 0; g < NC; ++g) qb[k][g] = s_q[(k * NC + g) * 32 + lane];
-#pragma unroll
-    for (int g = 0; g < NC; ++g) {
-      zmul[g] = pk2(s_mul[4 * g + e0], s_mul[4 * g + e0 + 1]);
-    }
+    for (int g = 0; g < NC; ++g) zmul[g] = pk2(s_mul[4 * g + e0], s_mul[4 * g + e0 + 1]);
     const int seen_all = len - a.q_len + row0 / a.G + 1;    // the least of any row here
     const float cap_l2 = CAP ? __fmul_rn(a.cap, kLog2e) : 0.0f;
 
@@ -503,20 +516,20 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
     }
     // ---- the tiles
     uint32_t get = 0;                            // byte offset of the next tile's stage
-    int t0 = (seg.u_lo + 2 * warp) * kUnit;
+    int t0 = (seg.u_lo + kUnits * warp) * kUnit;
     for (int i = 0; i < mine; ++i, t0 += kWarps * kTileTokens) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();                              // tile i has come, and tile i - 1 is used up
-      have |= issue() << (2 * (kStages - 1));
+      have |= issue() << (kUnits * (kStages - 1));
       const unsigned char *const U = ring + get;
-      const uint32_t got = have & 3u;
-      have >>= 2;
+      const uint32_t got = have & ((1u << kUnits) - 1);
+      have >>= kUnits;
       get += kStageBytes;
       if (get == kStages * kStageBytes) get = 0;
       // scores: lane (n8, c4) gets tokens n8 and n8 + 8 of a unit, columns 2 c4, 2 c4 + 1
-      float z[2][NC][2][2], sv[2][2];            // [unit][group][token][row], V's scales
+      float z[kUnits][NC][2][2], sv[kUnits][2];  // [unit][group][token][row], V's scales
 #pragma unroll
-      for (int un = 0; un < 2; ++un) {
+      for (int un = 0; un < kUnits; ++un) {
         const unsigned char *const V = U + un * kUnitBytes;
         float s[NC][4];
         const uint4 k0 = read16(V + lane * 16), k1 = read16(V + lane * 16 + 512);
@@ -528,11 +541,10 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
           code_pairs(w1[j], factor, p1);
 #pragma unroll
           for (int g = 0; g < NC; ++g) {
-            if (j == 0)
-              mma16816_first(s[g], p0[0], p1[0], p0[1], p1[1], qb[0][g].x, qb[0][g].y);
-            else
-              mma16816(s[g], p0[0], p1[0], p0[1], p1[1], qb[2 * j][g].x, qb[2 * j][g].y);
-            mma16816(s[g], p0[2], p1[2], p0[3], p1[3], qb[2 * j + 1][g].x, qb[2 * j + 1][g].y);
+            const uint2 q0 = query(2 * j, g), q1 = query(2 * j + 1, g);
+            if (j == 0) mma16816_first(s[g], p0[0], p1[0], p0[1], p1[1], q0.x, q0.y);
+            else mma16816(s[g], p0[0], p1[0], p0[1], p1[1], q0.x, q0.y);
+            mma16816(s[g], p0[2], p1[2], p0[3], p1[3], q1.x, q1.y);
           }
         }
         const float sk[2] = {read_bf16(V + kUnitKs + 2 * n8), read_bf16(V + kUnitKs + 2 * n8 + 16)};
@@ -559,9 +571,10 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
             }
           }
       }
-      if (t0 + kTileTokens > seen_all || got != 3u) {       // warp-uniform: not every row sees every token
+      // warp-uniform: not every row sees every token
+      if (t0 + kTileTokens > seen_all || got != (1u << kUnits) - 1) {
 #pragma unroll
-        for (int un = 0; un < 2; ++un)
+        for (int un = 0; un < kUnits; ++un)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int at = t0 + kUnit * un + 8 * t + n8;
@@ -583,7 +596,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
             if (zr >= a.R) continue;
             float *zrow = a.z + (((int64_t)seg.b * a.c.n_kv + h) * a.R + zr) * a.c.capacity() + t0 + n8;
 #pragma unroll
-            for (int un = 0; un < 2; ++un)
+            for (int un = 0; un < kUnits; ++un)
               if (t0 + kUnit * un < seg.u_hi * kUnit) {
                 zrow[kUnit * un] = z[un][g][0][e];
                 zrow[kUnit * un + 8] = z[un][g][1][e];
@@ -592,25 +605,33 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
       }
       // The references m (a whole number) and f move only when a score is more than 4 above m, or a
       // weight 2^(z - m) s f could pass 2^15: f holds the row's largest weight so far near 2^7.
-      float zt = kNoMax, ft = 0.0f;
+      float zt = kNoMax, ft = 0.0f, st = 0.0f;
+#pragma unroll
+      for (int un = 0; un < kUnits; ++un) st = fmaxf(fmaxf(st, sv[un][0]), sv[un][1]);
 #pragma unroll
       for (int g = 0; g < NC; ++g)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float top = fmaxf(fmaxf(z[0][g][0][e], z[0][g][1][e]), fmaxf(z[1][g][0][e], z[1][g][1][e]));
+          float top = kNoMax;
+#pragma unroll
+          for (int un = 0; un < kUnits; ++un) top = fmaxf(fmaxf(top, z[un][g][0][e]), z[un][g][1][e]);
           zt = fmaxf(zt, __fsub_rn(top, m[g][e]));
           ft = fmaxf(ft, f[g][e]);
         }
-      const float st = fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[1][0], sv[1][1]));
       if (__any_sync(0xffffffffu, zt > 4.0f || __fmul_rn(st, ft) > 2048.0f)) {
-        const float ls[2][2] = {{lg2(sv[0][0]), lg2(sv[0][1])}, {lg2(sv[1][0]), lg2(sv[1][1])}};
+        float ls[kUnits][2];
+#pragma unroll
+        for (int un = 0; un < kUnits; ++un) {
+          ls[un][0] = lg2(sv[un][0]);
+          ls[un][1] = lg2(sv[un][1]);
+        }
 #pragma unroll
         for (int g = 0; g < NC; ++g) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float mt = kNoMax, ut = kNoMax;
 #pragma unroll
-            for (int un = 0; un < 2; ++un)
+            for (int un = 0; un < kUnits; ++un)
 #pragma unroll
               for (int t = 0; t < 2; ++t) {
                 mt = fmaxf(mt, z[un][g][t][e]);
@@ -640,9 +661,9 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
           }
         }
       }
-      uint32_t pb[2][NC][2];
+      uint32_t pb[kUnits][NC][2];
 #pragma unroll
-      for (int un = 0; un < 2; ++un)
+      for (int un = 0; un < kUnits; ++un)
 #pragma unroll
         for (int g = 0; g < NC; ++g)
 #pragma unroll
@@ -657,26 +678,30 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
             pb[un][g][t] = transpose8(low ? lo : hi);
           }
       // lane (n8, c4) holds the 16 dimensions of chunk n8 of token pairs c4 and 4 + c4
-      const uint4 v00 = read16(U + ld_v), v01 = read16(U + ld_v + 512);
-      const uint4 v10 = read16(U + kUnitBytes + ld_v), v11 = read16(U + kUnitBytes + ld_v + 512);
+      uint4 v[kUnits][2];
+#pragma unroll
+      for (int un = 0; un < kUnits; ++un) {
+        v[un][0] = read16(U + un * kUnitBytes + ld_v);
+        v[un][1] = read16(U + un * kUnitBytes + ld_v + 512);
+      }
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          uint32_t p00[4], p01[4], p10[4], p11[4];
           const uint32_t pick = hf ? 0x7632u : 0x5410u;
-          code_pairs(__byte_perm(w ? v00.y : v00.x, w ? v00.w : v00.z, pick), factor, p00);
-          code_pairs(__byte_perm(w ? v01.y : v01.x, w ? v01.w : v01.z, pick), factor, p01);
-          code_pairs(__byte_perm(w ? v10.y : v10.x, w ? v10.w : v10.z, pick), factor, p10);
-          code_pairs(__byte_perm(w ? v11.y : v11.x, w ? v11.w : v11.z, pick), factor, p11);
 #pragma unroll
-          for (int g = 0; g < NC; ++g)
+          for (int un = 0; un < kUnits; ++un) {
+            const uint4 va = v[un][0], vb = v[un][1];
+            uint32_t p0[4], p1[4];
+            code_pairs(__byte_perm(w ? va.y : va.x, w ? va.w : va.z, pick), factor, p0);
+            code_pairs(__byte_perm(w ? vb.y : vb.x, w ? vb.w : vb.z, pick), factor, p1);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float *sum = acc[g][4 * w + 2 * hf + j];
-              mma16816(sum, p00[2 * j], p00[2 * j + 1], p01[2 * j], p01[2 * j + 1], pb[0][g][0], pb[0][g][1]);
-              mma16816(sum, p10[2 * j], p10[2 * j + 1], p11[2 * j], p11[2 * j + 1], pb[1][g][0], pb[1][g][1]);
-            }
+            for (int g = 0; g < NC; ++g)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                mma16816(acc[g][4 * w + 2 * hf + j], p0[2 * j], p0[2 * j + 1], p1[2 * j], p1[2 * j + 1],
+                         pb[un][g][0], pb[un][g][1]);
+          }
         }
       }
     }
