@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
   const int n8 = lane >> 2, c4 = lane & 3;       // fragment row group, and place in it
   const bool low = c4 >= 2;                      // this lane's columns are low parts
   const int e0 = 2 * (c4 & 1);                   // its rows of a column group: e0, e0 + 1
+  const int tok = n8 + (low ? 8 : 0);            // its token of a unit
   const uint32_t ld_v = kUnitV + c4 * 128 + ((n8 ^ (2 * c4)) * 16);
   const uint64_t policy = stream_policy();
   uint32_t factor;                               // 2^15 twice, in a register that is not filled again
@@ -492,9 +493,13 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
 #pragma unroll
     for (int k = 0; k < 8; ++k) qr[k] = s_q[k * NC * 32 + lane];
     const auto query = [&](int k, int g) { return NC == 1 ? qr[k] : s_q[(k * NC + g) * 32 + lane]; };
-    uint64_t zmul[NC];
+    uint64_t m_own[NC], m_other[NC];             // multipliers of this lane's and its partner's part
 #pragma unroll
-    for (int g = 0; g < NC; ++g) zmul[g] = pk2(s_mul[4 * g + e0], s_mul[4 * g + e0 + 1]);
+    for (int g = 0; g < NC; ++g) {
+      const uint64_t mul = pk2(s_mul[4 * g + e0], s_mul[4 * g + e0 + 1]);
+      m_own[g] = mul2(mul, pk2(k_own, k_own));
+      m_other[g] = mul2(mul, pk2(k_other, k_other));
+    }
     const int seen_all = len - a.q_len + row0 / a.G + 1;    // the least of any row here
     const float cap_l2 = CAP ? __fmul_rn(a.cap, kLog2e) : 0.0f;
 
@@ -526,8 +531,10 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
       have >>= kUnits;
       get += kStageBytes;
       if (get == kStages * kStageBytes) get = 0;
-      // scores: lane (n8, c4) gets tokens n8 and n8 + 8 of a unit, columns 2 c4, 2 c4 + 1
-      float z[kUnits][NC][2][2], sv[kUnits][2];  // [unit][group][token][row], V's scales
+      // Scores: lane (n8, c4) gets tokens n8 and n8 + 8 of a unit, columns 2 c4, 2 c4 + 1.  Lanes
+      // c4 and c4 ^ 2 hold the high and the low parts of the same rows: the first goes on with
+      // token n8, the second with token n8 + 8, each with the other's part of its token's scores.
+      float z[kUnits][NC][2], sv[kUnits];        // [unit][group][row], V's scales
 #pragma unroll
       for (int un = 0; un < kUnits; ++un) {
         const unsigned char *const V = U + un * kUnitBytes;
@@ -547,98 +554,79 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
             mma16816(s[g], p0[2], p1[2], p0[3], p1[3], q1.x, q1.y);
           }
         }
-        const float sk[2] = {read_bf16(V + kUnitKs + 2 * n8), read_bf16(V + kUnitKs + 2 * n8 + 16)};
-        sv[un][0] = read_bf16(V + kUnitVs + 2 * n8);
-        sv[un][1] = read_bf16(V + kUnitVs + 2 * n8 + 16);
+        const float sk = read_bf16(V + kUnitKs + 2 * tok);
+        sv[un] = read_bf16(V + kUnitVs + 2 * tok);
 #pragma unroll
-        for (int g = 0; g < NC; ++g)
+        for (int g = 0; g < NC; ++g) {
+          const float o0 = __shfl_xor_sync(0xffffffffu, low ? s[g][0] : s[g][2], 2);
+          const float o1 = __shfl_xor_sync(0xffffffffu, low ? s[g][1] : s[g][3], 2);
+          const uint64_t own = low ? pk2(s[g][2], s[g][3]) : pk2(s[g][0], s[g][1]);
+          upk2(mul2(fma2(pk2(o0, o1), m_other[g], mul2(own, m_own[g])), pk2(sk, sk)), z[un][g][0], z[un][g][1]);
+          if (CAP) {                             // cap tanh(y) = cap (1 - 2 / (1 + e^2|y|)), y's sign
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float o0 = __shfl_xor_sync(0xffffffffu, s[g][2 * t], 2);
-            const float o1 = __shfl_xor_sync(0xffffffffu, s[g][2 * t + 1], 2);
-            // powers of two: both lanes of a (high, low) pair get the same sum, bit for bit, as their
-            // two parts of one weight have to add up
-            const uint64_t d = fma2(pk2(o0, o1), pk2(k_other, k_other),
-                                    mul2(pk2(s[g][2 * t], s[g][2 * t + 1]), pk2(k_own, k_own)));
-            upk2(mul2(mul2(d, pk2(sk[t], sk[t])), zmul[g]), z[un][g][t][0], z[un][g][t][1]);
-            if (CAP) {                           // cap tanh(y) = cap (1 - 2 / (1 + e^2|y|)), y's sign
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float y = z[un][g][t][e], ey = ex2(__fmul_rn(fabsf(y), 2.0f * kLog2e));
-                z[un][g][t][e] = copysignf(
-                    __fmul_rn(cap_l2, __fsub_rn(1.0f, __fdividef(2.0f, __fadd_rn(ey, 1.0f)))), y);
-              }
+            for (int e = 0; e < 2; ++e) {
+              const float y = z[un][g][e], ey = ex2(__fmul_rn(fabsf(y), 2.0f * kLog2e));
+              z[un][g][e] = copysignf(
+                  __fmul_rn(cap_l2, __fsub_rn(1.0f, __fdividef(2.0f, __fadd_rn(ey, 1.0f)))), y);
             }
           }
+        }
       }
       // warp-uniform: not every row sees every token
       if (t0 + kTileTokens > seen_all || got != (1u << kUnits) - 1) {
 #pragma unroll
-        for (int un = 0; un < kUnits; ++un)
+        for (int un = 0; un < kUnits; ++un) {
+          const int at = t0 + kUnit * un + tok;
+          const bool none = !((got >> un) & 1u) || at >= len;
+          if (none) sv[un] = 0.0f;               // what lies there is no scale
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int at = t0 + kUnit * un + 8 * t + n8;
-            const bool none = !((got >> un) & 1u) || at >= len;
-            if (none) sv[un][t] = 0.0f;          // what lies there is no scale
+          for (int g = 0; g < NC; ++g)
 #pragma unroll
-            for (int g = 0; g < NC; ++g)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (none || at >= s_seen[4 * g + e0 + e]) z[un][g][t][e] = -INFINITY;
-          }
+            for (int e = 0; e < 2; ++e)
+              if (none || at >= s_seen[4 * g + e0 + e]) z[un][g][e] = -INFINITY;
+        }
       }
-      if (MASS && !low) {
+      if (MASS) {
 #pragma unroll
         for (int g = 0; g < NC; ++g)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int zr = row0 + 4 * g + e0 + e;
             if (zr >= a.R) continue;
-            float *zrow = a.z + (((int64_t)seg.b * a.c.n_kv + h) * a.R + zr) * a.c.capacity() + t0 + n8;
+            float *zrow = a.z + (((int64_t)seg.b * a.c.n_kv + h) * a.R + zr) * a.c.capacity() + t0 + tok;
 #pragma unroll
             for (int un = 0; un < kUnits; ++un)
-              if (t0 + kUnit * un < seg.u_hi * kUnit) {
-                zrow[kUnit * un] = z[un][g][0][e];
-                zrow[kUnit * un + 8] = z[un][g][1][e];
-              }
+              if (t0 + kUnit * un < seg.u_hi * kUnit) zrow[kUnit * un] = z[un][g][e];
           }
       }
       // The references m (a whole number) and f move only when a score is more than 4 above m, or a
       // weight 2^(z - m) s f could pass 2^15: f holds the row's largest weight so far near 2^7.
       float zt = kNoMax, ft = 0.0f, st = 0.0f;
 #pragma unroll
-      for (int un = 0; un < kUnits; ++un) st = fmaxf(fmaxf(st, sv[un][0]), sv[un][1]);
+      for (int un = 0; un < kUnits; ++un) st = fmaxf(st, sv[un]);
 #pragma unroll
       for (int g = 0; g < NC; ++g)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float top = kNoMax;
 #pragma unroll
-          for (int un = 0; un < kUnits; ++un) top = fmaxf(fmaxf(top, z[un][g][0][e]), z[un][g][1][e]);
+          for (int un = 0; un < kUnits; ++un) top = fmaxf(top, z[un][g][e]);
           zt = fmaxf(zt, __fsub_rn(top, m[g][e]));
           ft = fmaxf(ft, f[g][e]);
         }
       if (__any_sync(0xffffffffu, zt > 4.0f || __fmul_rn(st, ft) > 2048.0f)) {
-        float ls[kUnits][2];
-#pragma unroll
-        for (int un = 0; un < kUnits; ++un) {
-          ls[un][0] = lg2(sv[un][0]);
-          ls[un][1] = lg2(sv[un][1]);
-        }
 #pragma unroll
         for (int g = 0; g < NC; ++g) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float mt = kNoMax, ut = kNoMax;
 #pragma unroll
-            for (int un = 0; un < kUnits; ++un)
+            for (int un = 0; un < kUnits; ++un) {
+              mt = fmaxf(mt, z[un][g][e]);
+              ut = fmaxf(ut, __fadd_rn(z[un][g][e], lg2(sv[un])));
+            }
 #pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                mt = fmaxf(mt, z[un][g][t][e]);
-                ut = fmaxf(ut, __fadd_rn(z[un][g][t][e], ls[un][t]));
-              }
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
+            for (int d = 2; d < 32; d <<= 1) {
               mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, d));
               ut = fmaxf(ut, __shfl_xor_sync(0xffffffffu, ut, d));
             }
@@ -648,9 +636,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
             const float u2 = fmaxf(__fadd_rn(__fsub_rn(m[g][e], lf), 7.0f), ceilf(ut));
             const float l2 = fminf(fmaxf(__fadd_rn(__fsub_rn(m2, u2), 7.0f), -120.0f), 120.0f);
             const float f2 = __uint_as_float((uint32_t)((int)l2 + 127) << 23);
-            const float down = ex2(__fsub_rn(m[g][e], m2));
             const float by = ex2(__fadd_rn(__fsub_rn(m[g][e], m2), __fsub_rn(l2, lf)));
-            l[g][e] = __fmul_rn(l[g][e], down);
+            l[g][e] = __fmul_rn(l[g][e], ex2(__fsub_rn(m[g][e], m2)));
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               acc[g][k][e] = __fmul_rn(acc[g][k][e], by);
@@ -661,22 +648,23 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
           }
         }
       }
+      // weights: this lane's token's parts, the partner's from it
       uint32_t pb[kUnits][NC][2];
 #pragma unroll
       for (int un = 0; un < kUnits; ++un)
 #pragma unroll
-        for (int g = 0; g < NC; ++g)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            float p0, p1, w0, w1;
-            upk2(sub2(pk2(z[un][g][t][0], z[un][g][t][1]), pk2(m[g][0], m[g][1])), p0, p1);
-            const uint64_t p = pk2(ex2(p0), ex2(p1));
-            upk2(add2(pk2(l[g][0], l[g][1]), p), l[g][0], l[g][1]);
-            upk2(mul2(mul2(p, pk2(sv[un][t], sv[un][t])), pk2(f[g][0], f[g][1])), w0, w1);
-            uint32_t hi, lo;
-            split2(w0, w1, hi, lo);
-            pb[un][g][t] = transpose8(low ? lo : hi);
-          }
+        for (int g = 0; g < NC; ++g) {
+          float p0, p1, w0, w1;
+          upk2(sub2(pk2(z[un][g][0], z[un][g][1]), pk2(m[g][0], m[g][1])), p0, p1);
+          const uint64_t p = pk2(ex2(p0), ex2(p1));
+          upk2(add2(pk2(l[g][0], l[g][1]), p), l[g][0], l[g][1]);
+          upk2(mul2(mul2(p, pk2(sv[un], sv[un])), pk2(f[g][0], f[g][1])), w0, w1);
+          uint32_t hi, lo;
+          split2(w0, w1, hi, lo);
+          const uint32_t from = __shfl_xor_sync(0xffffffffu, low ? hi : lo, 2);
+          pb[un][g][0] = transpose8(low ? from : hi);
+          pb[un][g][1] = transpose8(low ? lo : from);
+        }
       // lane (n8, c4) holds the 16 dimensions of chunk n8 of token pairs c4 and 4 + c4
       uint4 v[kUnits][2];
 #pragma unroll
@@ -713,7 +701,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[g][e] = __fadd_rn(l[g][e], __shfl_xor_sync(0xffffffffu, l[g][e], d));
+        for (int d = 2; d < 32; d <<= 1) l[g][e] = __fadd_rn(l[g][e], __shfl_xor_sync(0xffffffffu, l[g][e], d));
         // dimensions 16 n8 .. + 15 of row e: both lanes of a (high, low) pair form the sums, the
         // high one stores row e0, the low one row e0 + 1
         float *dst = s_acc + (warp * kRows + 4 * g + e0 + e) * kTile + 16 * n8;
