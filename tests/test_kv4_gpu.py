@@ -572,6 +572,45 @@ def test_a_serving_loop(hq):
     assert int(C.status) == 0 and max(C.lens) <= budget + 10
 
 
+def test_a_chain_without_waits(hq):
+    """Torch kernels that write the next call's inputs, appends, attentions and reads behind one
+    another in a stream, each launched while the one before it runs: the same bits as with a
+    wait after every call."""
+    def run(wait):
+        rng = np.random.default_rng(41)
+        B, nh, page, width = 4, 2, 16, 40
+        C = Cache(hq, rng, [600, 33, 15, 1], nh, page, width=width)
+        g = torch.Generator(device="cuda")
+        g.manual_seed(7)
+        ws = torch.zeros(hq.hq_kv4_attention_workspace_bytes(C.c, 1, 8, True), dtype=torch.uint8,
+                         device="cuda")
+        mass = torch.zeros((B, nh, width * page), device="cuda")
+        k, v = (torch.empty((B, nh, 128), device="cuda") for _ in range(2))
+        q, out = torch.empty((B, 1, 8, 128), device="cuda"), torch.empty((B, 1, 8, 128), device="cuda")
+        seq, rows_k, rows_v = ints(range(B)), torch.empty_like(k), torch.empty_like(k)
+        seen = []
+        for _ in range(25):
+            for t in (k, v, q):
+                t.normal_(generator=g)
+            hq.hq_kv4_append(C.c, k, v, seq, C.d_lens, C.status)
+            if wait:
+                torch.cuda.synchronize()
+            hq.hq_kv4_read(C.c, seq, C.d_lens, rows_k, rows_v, C.status)
+            C.d_lens += 1
+            if wait:
+                torch.cuda.synchronize()
+            hq.hq_kv4_attention(C.c, C.d_lens, q, 0.1, 0.0, out, None, mass, mass, ws, C.status)
+            if wait:
+                torch.cuda.synchronize()
+            seen += [out.clone(), rows_k.clone(), rows_v.clone()]
+        torch.cuda.synchronize()
+        assert int(C.status) == 0
+        return seen + [mass, C.d_pages]
+
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
+
+
 def test_binding_checks(hq):
     rng = np.random.default_rng(50)
     C = Cache(hq, rng, [20, 30], 2, 16)

@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(Kv4RowArgs 
   if (i < a.n_tokens) {                          // every lane stays for the transform
     rows[0].load(a.rows.k, i * a.rows.k_token + h * a.rows.k_head, r, a.rows.vec != 0);
     rows[1].load(a.rows.v, i * a.rows.v_token + h * a.rows.v_head, r, a.rows.vec != 0);
-    const int seq = __ldg(a.seq + i), pos = __ldg(a.pos + i);
+    const int seq = a.seq[i], pos = a.pos[i];
     if (seq >= 0) {
       place = kv4_place(a.c, seq, pos, h);
       if (place == kNoPlace && r == 0) atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(Kv4RowArgs 
     rows[0].zero();
     rows[1].zero();
   }
-  const uint32_t mw = (__ldg(a.c.signs + (r >> 1)) >> (16 * (r & 1))) & 0xFFFFu;
+  const uint32_t mw = (a.c.signs[r >> 1] >> (16 * (r & 1))) & 0xFFFFu;
   unsigned char *const unit = kv4_unit(a.c, place);
   const int tok = place % kUnit;
 #pragma unroll
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(Kv4RowArgs a, in
   if (lane < per_warp && first + lane < entries) {
     const int64_t i = kv4_divide(first + lane, a.c.n_kv, a.c.kv_shift);
     const int h = (int)(first + lane - i * a.c.n_kv);
-    const int seq = __ldg(a.seq + i), pos = __ldg(a.pos + i);
+    const int seq = a.seq[i], pos = a.pos[i];
     writes = seq >= 0;                           // no padding token
     if (writes) {
       place = kv4_place(a.c, seq, pos, h);
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(Kv4RowArgs a, in
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int dj = d + (j & 1) + 64 * (j >> 1);
-    flip[j] = ((__ldg(a.c.signs + (dj >> 5)) >> (dj & 31)) & 1u) << 31;
+    flip[j] = ((a.c.signs[dj >> 5] >> (dj & 31)) & 1u) << 31;
   }
   const bool same = a.rows.k_token == a.rows.v_token && a.rows.k_head == a.rows.v_head;
   const uint32_t k_off = 16 * c4, v_off = kUnitV + 32 * c4;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a,
   uint32_t least = 0xFFFFFFFFu, most = 0u;
 #pragma unroll 8
   for (int i = tid; i < old; i += kSelThreads) {
-    const uint32_t key = mass_key(__ldg(mass + i));
+    const uint32_t key = mass_key(mass[i]);
     if (i < cached) s_keys[i] = key;
     least = min(least, key);
     most = max(most, key);
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a,
   }
   __syncthreads();
   least = s_least;
-  const auto key_of = [&](int i) { return (i < cached ? s_keys[i] : mass_key(__ldg(mass + i))) - least; };
+  const auto key_of = [&](int i) { return (i < cached ? s_keys[i] : mass_key(mass[i])) - least; };
   int shift = 32 - __clz((int)(s_most - least));  // bits of the range: those below `shift` are to be found
   uint32_t prefix = 0, want = (uint32_t)need;     // digits found; how many to keep among their equals
   int flip = 0;
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_move_kernel(Kv4EvictArgs a, 
     const int t = a.kept[head * a.budget + i];
     from = kv4_place(a.src, b, t, h);
     to = kv4_place(a.dst, b, i, h);
-    a.new_mass[head * a.dst.capacity() + i] = __ldg(a.mass + head * a.src.capacity() + t);
+    a.new_mass[head * a.dst.capacity() + i] = a.mass[head * a.src.capacity() + t];
     if (from == kNoPlace || to == kNoPlace) {
       atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
       from = to = kNoPlace;

@@ -103,7 +103,7 @@ constexpr uint32_t kNoPlace = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t kv4_place(const Kv4View &c, int seq, int pos, int h) {
   if (seq >= c.n_seqs || pos < 0 || pos >= c.capacity()) return kNoPlace;
   const int j = (int)kv4_divide(pos, c.page_tokens, c.page_shift), in_page = pos - j * c.page_tokens;
-  const int page = __ldg(c.table + (int64_t)seq * c.width + j);
+  const int page = c.table[(int64_t)seq * c.width + j];
   if (page < 0 || page >= c.n_pages) return kNoPlace;
   return (uint32_t)((page * c.n_kv + h) * c.page_units + in_page / kUnit) * kUnit + (uint32_t)(in_page % kUnit);
 }
@@ -112,7 +112,7 @@ __device__ __forceinline__ unsigned char *kv4_unit(const Kv4View &c, uint32_t pl
 }
 // A sequence's length, held to [0, capacity]; *bad when it was outside.
 __device__ __forceinline__ int kv4_length(const Kv4View &c, const int32_t *lengths, int seq, bool *bad) {
-  const int n = __ldg(lengths + seq), cap = c.width * c.page_tokens;
+  const int n = lengths[seq], cap = c.width * c.page_tokens;
   *bad = n < 0 || n > cap;
   return n < 0 ? 0 : n > cap ? cap : n;
 }

@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
   // 128-byte rows so that the reads of a warp touch all banks
   const uint32_t cp_v = kUnitV + (lane >> 3) * 128 + (((lane & 7) ^ (2 * (lane >> 3))) * 16);
   follow_launch();
-  const uint32_t sign_bits = __ldg(a.c.signs + ((tid & 7) >> 1)) >> (16 * (tid & 1));
+  const uint32_t sign_bits = a.c.signs[(tid & 7) >> 1] >> (16 * (tid & 1));
   const Piece piece = find_piece(a);
   Walk walk{piece.begin, piece.end, piece.b_begin, piece.b};
   Segment seg;
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
             const int u = seg.u_lo + kUnits * (warp + kWarps * (issued + lane)) + k, pj = u / a.c.page_units;
             unit[k] = -1;
             if (u < seg.u_hi) {
-              const int page = __ldg(a.c.table + (int64_t)seg.b * a.c.width + pj);
+              const int page = a.c.table[(int64_t)seg.b * a.c.width + pj];
               if (page >= 0 && page < a.c.n_pages)
                 unit[k] = (page * a.c.n_kv + h) * a.c.page_units + u - pj * a.c.page_units;
               else bad = true;
@@ -720,7 +720,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
         }
         if (n8 == 0 && !low)
           s_stat[warp][4 * g + e0 + e] =
-              RowStat{m[g][e], l[g][e], __fsub_rn(m[g][e], (float)((int)(__float_as_uint(f[g][e]) >> 23) - 127)), 0.0f};
+              RowStat{m[g][e], l[g][e],
+                      __fsub_rn(m[g][e], (float)((int)(__float_as_uint(f[g][e]) >> 23) - 127)), 0.0f};
       }
     }
     __syncthreads();
@@ -768,7 +769,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
     }
     __syncthreads();                             // the ring and the statistics are free
   }
-  if (tid == 0 && !a.whole) reinterpret_cast<int4 *>(a.joins)[blockIdx.x] = make_int4(join_count, join_b, join_pair, 0);
+  if (tid == 0 && !a.whole)
+    reinterpret_cast<int4 *>(a.joins)[blockIdx.x] = make_int4(join_count, join_b, join_pair, 0);
   // rows of sequences without tokens, and lengths out of range
   for (int sb = blockIdx.x; sb < a.c.n_seqs; sb += gridDim.x) {
     bool bad_len;
@@ -843,26 +845,38 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, i
   }
   normalize(y, M, MW, L);
   const int j = row / a.G, hq = h * a.G + row % a.G;
-  const uint32_t sign_bits = __ldg(a.c.signs + (r >> 1)) >> (16 * (r & 1));
+  const uint32_t sign_bits = a.c.signs[r >> 1] >> (16 * (r & 1));
   finish_row(a, y, s_tr + (lane >> 3) * kTrTile, r, sign_bits, lane < 8, ((int64_t)job.y * a.q_len + j) * a.Hq + hq);
   if (lane == 0) finish_stats(a, job.y, h, row, M, L);
 }
 
-// mass_out = mass_in + sum over the head's rows of 2^(z - log2 of the row's sum).
-__global__ void __launch_bounds__(256) kv4_mass_kernel(Kv4AttnArgs a) {
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// mass_out = mass_in + sum over the head's rows of 2^(z - log2 of the row's
+// sum), rows in order, four tokens a thread.
+constexpr int kMassThreads = 256;
+__global__ void __launch_bounds__(kMassThreads) kv4_mass_kernel(Kv4AttnArgs a) {
   follow_launch();
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int64_t t = ((int64_t)blockIdx.x * kMassThreads + threadIdx.x) * 4;
   bool bad;
   const int len = kv4_length(a.c, a.lengths, b, &bad);
   if (t >= len) return;
-  const int64_t head = (int64_t)b * a.c.n_kv + h, cap = a.c.capacity();
-  float s = 0.0f;
+  const int64_t head = (int64_t)b * a.c.n_kv + h, cap = a.c.capacity();   // a multiple of 16
+  const float *z = a.z + head * a.R * cap + t, *lse = a.row_lse + head * a.R;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
   for (int row = 0; row < a.R; ++row) {
-    const float z = a.z[(head * a.R + row) * cap + t];
-    if (z > -INFINITY || z != z) s = __fadd_rn(s, ex2(__fsub_rn(z, a.row_lse[head * a.R + row])));
+    const float4 v = *reinterpret_cast<const float4 *>(z + row * cap);
+    const float l = lse[row], x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (x[k] > -INFINITY || x[k] != x[k]) s[k] = __fadd_rn(s[k], ex2(__fsub_rn(x[k], l)));
   }
-  a.mass_out[head * cap + t] = a.mass_in != nullptr ? __fadd_rn(a.mass_in[head * cap + t], s) : s;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (t + k >= len) break;
+    const int64_t at = head * cap + t + k;
+    a.mass_out[at] = a.mass_in != nullptr ? __fadd_rn(a.mass_in[at], s[k]) : s[k];
+  }
 }
 
 // Resident blocks of the attention kernel on the current device (asked once
@@ -924,8 +938,9 @@ int launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t st) {
   const int rc = row_groups(a.R) == 1 ? launch_rows<1>(a, st) : launch_rows<2>(a, st);
   if (rc != 0) return rc;
   if (a.mass_out != nullptr && a.c.capacity() > 0)
-    return launch_behind(kv4_mass_kernel, dim3((unsigned)((a.c.capacity() + 255) / 256), (unsigned)a.c.n_kv,
-                                               (unsigned)a.c.n_seqs), 256, 0, st, a);
+    return launch_behind(kv4_mass_kernel,
+                         dim3((unsigned)((a.c.capacity() + 4 * kMassThreads - 1) / (4 * kMassThreads)),
+                              (unsigned)a.c.n_kv, (unsigned)a.c.n_seqs), kMassThreads, 0, st, a);
   return 0;
 }
 

@@ -35,19 +35,19 @@ struct Row16 {
       const uint32_t *p = static_cast<const uint32_t *>(base) + at + 16 * r;
       if (vec) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) put4(4 * c, __ldg(reinterpret_cast<const uint4 *>(p) + c));
+        for (int c = 0; c < 4; ++c) put4(4 * c, reinterpret_cast<const uint4 *>(p)[c]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = __ldg(p + i);
+        for (int i = 0; i < 16; ++i) w[i] = p[i];
       }
     } else {
       const uint16_t *p = static_cast<const uint16_t *>(base) + at + 16 * r;
       if (vec) {
-        put4(0, __ldg(reinterpret_cast<const uint4 *>(p)));
-        put4(4, __ldg(reinterpret_cast<const uint4 *>(p) + 1));
+        put4(0, reinterpret_cast<const uint4 *>(p)[0]);
+        put4(4, reinterpret_cast<const uint4 *>(p)[1]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = (uint32_t)__ldg(p + 2 * i) | ((uint32_t)__ldg(p + 2 * i + 1) << 16);
+        for (int i = 0; i < 8; ++i) w[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
       }
     }
   }

@@ -8,6 +8,9 @@ namespace hq {
 // waits until all that came before it in the stream has ended and can be
 // seen, and lets the launch after it begin likewise.  No thread may leave
 // before it, as the next kernel relies on this one's end for all before it.
+// Behind it ordinary loads see what came before; loads through the read-only
+// path (__ldg) are not for such kernels, whose lifetime begins before their
+// inputs are written.
 __device__ __forceinline__ void follow_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -27,7 +30,9 @@ int launch_behind(void (*kernel)(Params...), dim3 grid, int threads, size_t smem
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...) == cudaSuccess ? 0 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...) == cudaSuccess) return 0;
+  cudaGetLastError();                            // reported here, not to the next caller
+  return 1;
 }
 
 }  // namespace hq
