@@ -49,7 +49,7 @@ def quantize(x: np.ndarray, mask):
         s = np.where(s < F32(2.0 ** -126), F32(0), s)
         inv = np.where(s > 0, F32(1) / (s * F32(11.313708498984761)), F32(0)).astype(F32)
         zz = np.where(s[..., None] > 0, z, F32(0))
-        t = np.floor(zz * inv[..., None] + F32(8))
+        t = np.floor(zz.astype(np.float64) * inv[..., None].astype(np.float64)) + 8   # exact products
     return np.clip(t, 0, 15).astype(np.uint8), s.astype(F32), bad
 
 

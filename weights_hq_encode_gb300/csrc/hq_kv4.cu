@@ -48,13 +48,13 @@ __device__ __forceinline__ void fwht128_t8_columns(float x[16], float *tile, int
   }
 }
 
-// Two values' codes into field `at` of two words of 4-bit fields:
-// floor(fl(fl(z inv) + 8)), the floor by a sum with 2^23 rounded towards zero.
-// |z| inv is at most 7.5 (1 + 2^-8) and a few units, so the codes are 0 .. 15 as
-// they are; 2^23's own bits are taken out at the end.
+// Two values' codes into field `at` of two words of 4-bit fields: floor(z inv + 8)
+// exactly, by one fused multiply-add to 2^23 + 8 rounded towards zero.  |z| inv is
+// at most 7.5 (1 + 2^-8) and a few units, so the codes are 0 .. 15 as they are;
+// 2^23's own bits are taken out at the end.
 __device__ __forceinline__ void add_codes(uint32_t &even, uint32_t &odd, float z0, float z1, uint64_t inv, int at) {
-  uint64_t t = add2(mul2(pk2(z0, z1), inv), pk2(8.0f, 8.0f));
-  asm("add.rz.f32x2 %0, %1, %2;" : "=l"(t) : "l"(t), "l"(pk2(8388608.0f, 8388608.0f)));
+  uint64_t t;
+  asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(pk2(z0, z1)), "l"(inv), "l"(pk2(8388616.0f, 8388616.0f)));
   float a, b;
   upk2(t, a, b);
   even += __float_as_uint(a) << (4 * at);
@@ -163,24 +163,25 @@ __device__ __forceinline__ uint32_t signs_f16(int i, int j, int k) {
   return (0x3C00u | ((uint32_t)(__popc(i & j) & 1) << 15)) | (0x3C000000u | ((uint32_t)(__popc(i & k) & 1) << 31));
 }
 
-// Writes a row's 4 values of this lane, dimensions d, d + 1 and d + 64, d + 65.
-template <int KIND>
-__device__ __forceinline__ void store4(void *base, int64_t at, bool vec, const float v[4], const uint32_t flip[4]) {
+// Writes a row's 4 values of this lane, dimensions d, d + 1 and d + 64, d + 65; p: dimension d.
+// VEC: the row starts on a 16-byte boundary.
+template <int KIND, bool VEC>
+__device__ __forceinline__ void store4(char *to, const float v[4], const uint32_t flip[4]) {
   if constexpr (KIND == HQ_T_F32) {
-    float x[4], *p = static_cast<float *>(base) + at;
+    float x[4], *p = reinterpret_cast<float *>(to);
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(__float_as_uint(v[j]) ^ flip[j]);
-    if (vec) {
+    if constexpr (VEC) {
       *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
       *reinterpret_cast<float2 *>(p + 64) = make_float2(x[2], x[3]);
     } else {
       p[0] = x[0]; p[1] = x[1]; p[64] = x[2]; p[65] = x[3];
     }
   } else {
-    uint16_t *p = static_cast<uint16_t *>(base) + at;
+    uint16_t *p = reinterpret_cast<uint16_t *>(to);
     const uint32_t lo = round_pair<KIND>(v[0], v[1]) ^ (flip[0] >> 16 | flip[1]);
     const uint32_t hi = round_pair<KIND>(v[2], v[3]) ^ (flip[2] >> 16 | flip[3]);
-    if (vec) {
+    if constexpr (VEC) {
       *reinterpret_cast<uint32_t *>(p) = lo;
       *reinterpret_cast<uint32_t *>(p + 64) = hi;
     } else {
@@ -199,7 +200,7 @@ __device__ __forceinline__ void store4(void *base, int64_t at, bool vec, const f
 // by its 330 instructions for 4 rows (68 us for 262144 entries to bf16, 25 of
 // them the memory's).
 constexpr int kReadBatch = 4;                    // entries of a warp at a time
-template <int KIND>
+template <int KIND, bool VEC>
 __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(Kv4RowArgs a, int per_warp) {
   follow_launch();
   const int lane = threadIdx.x & 31, n8 = lane >> 2, c4 = lane & 3;
@@ -209,7 +210,8 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(Kv4RowArgs a, in
   // an entry a lane: its place, its scales and where its rows go
   uint32_t place = 0;
   bool writes = false;
-  int64_t k_at = 0, v_at = 0;
+  constexpr int kSize = KIND == HQ_T_F32 ? 4 : 2;
+  int64_t k_to = 0, v_to = 0;                    // addresses
   float ks = 0.0f, vs = 0.0f;
   if (lane < per_warp && first + lane < entries) {
     const int64_t i = kv4_divide(first + lane, a.c.n_kv, a.c.kv_shift);
@@ -218,8 +220,8 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(Kv4RowArgs a, in
     writes = seq >= 0;                           // no padding token
     if (writes) {
       place = kv4_place(a.c, seq, pos, h);
-      k_at = i * a.rows.k_token + h * a.rows.k_head;
-      v_at = i * a.rows.v_token + h * a.rows.v_head;
+      k_to = reinterpret_cast<int64_t>(a.rows.k) + (i * a.rows.k_token + h * a.rows.k_head) * kSize;
+      v_to = reinterpret_cast<int64_t>(a.rows.v) + (i * a.rows.v_token + h * a.rows.v_head) * kSize;
       if (place == kNoPlace) {
         atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
         place = 0;                               // the pool's first row, times a scale of 0
@@ -247,7 +249,9 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(Kv4RowArgs a, in
     const int dj = d + (j & 1) + 64 * (j >> 1);
     flip[j] = ((a.c.signs[dj >> 5] >> (dj & 31)) & 1u) << 31;
   }
+  // V's rows lie where K's do, `apart` bytes further on, when the strides are the same
   const bool same = a.rows.k_token == a.rows.v_token && a.rows.k_head == a.rows.v_head;
+  const int64_t apart = reinterpret_cast<int64_t>(a.rows.v) - reinterpret_cast<int64_t>(a.rows.k);
   const uint32_t k_off = 16 * c4, v_off = kUnitV + 32 * c4;
 #pragma unroll 1
   for (int e0 = 0; e0 < 32 && (live >> e0) != 0; e0 += kReadBatch) {
@@ -266,8 +270,8 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(Kv4RowArgs a, in
 #pragma unroll
     for (int e = 0; e < kReadBatch; ++e) {
       if (!((live >> (e0 + e)) & 1u)) continue;  // warp-uniform
-      const int64_t to_k = __shfl_sync(0xffffffffu, k_at, e0 + e) + d;
-      const int64_t to_v = same ? to_k : __shfl_sync(0xffffffffu, v_at, e0 + e) + d;
+      const int64_t to_k = __shfl_sync(0xffffffffu, k_to, e0 + e) + d * kSize;
+      const int64_t to_v = same ? to_k + apart : __shfl_sync(0xffffffffu, v_to, e0 + e) + d * kSize;
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         const uint4 w = which == 0 ? k[e] : make_uint4(lo[e].x, lo[e].y, hi[e].x, hi[e].y);
@@ -287,8 +291,7 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(Kv4RowArgs a, in
             : "r"(t0), "r"(t1), "r"(g0), "f"(0.0f));
         upk2(mul2(pk2(x[0], x[1]), pk2(s, s)), x[0], x[1]);
         upk2(mul2(pk2(x[2], x[3]), pk2(s, s)), x[2], x[3]);
-        store4<KIND>(const_cast<void *>(which == 0 ? a.rows.k : a.rows.v), which == 0 ? to_k : to_v,
-                     a.rows.vec != 0, x, flip);
+        store4<KIND, VEC>(reinterpret_cast<char *>(which == 0 ? to_k : to_v), x, flip);
       }
     }
   }
@@ -493,24 +496,30 @@ int launch_kv4_append(const Kv4RowArgs &a, cudaStream_t st) {
   }
 }
 
-// Rows a warp takes, a power of two from `least` to 32: as many as leave work
-// for 16 warps a multiprocessor (few rows a warp for short calls, whose time is
-// that of one warp's chain of loads; many for long ones, whose look-ups are
-// then one a lane).
-static int rows_a_warp(int64_t rows, int least) {
-  int per = 32;
-  while (per > least && rows < (int64_t)per * 16 * 152) per /= 2;
-  return per;
+// Rows a warp takes, a multiple of `step` (or 1) up to 32: as many as fill whole
+// waves of the 4 blocks that a multiprocessor holds.  Short calls get few, as
+// their time is that of one warp's chain of loads; long ones many, whose look-ups
+// are then one a lane (262144 rows: 39 us with 32 a warp in 1.7 waves).
+static int rows_a_warp(int64_t rows, int step) {
+  constexpr int64_t kWave = 152 * 4 * (kRowsThreads / 32);
+  const int64_t waves = (rows + 32 * kWave - 1) / (32 * kWave);
+  const int64_t per = (rows + waves * kWave - 1) / (waves * kWave);
+  return per <= 1 && step == 1 ? 1 : (int)((per + 3) / 4 * 4);
 }
 
 int launch_kv4_read(const Kv4RowArgs &a, cudaStream_t st) {
   const int64_t entries = a.n_tokens * a.c.n_kv;
   const int per = rows_a_warp(entries, 1), block = kRowsThreads / 32 * per;
   const dim3 grid((unsigned)((entries + block - 1) / block));
+  const bool vec = a.rows.vec != 0;
+  const auto go = [&](auto with, auto without) {
+    return vec ? launch_behind(with, grid, kRowsThreads, 0, st, a, per)
+               : launch_behind(without, grid, kRowsThreads, 0, st, a, per);
+  };
   switch (a.rows.kind) {
-    case HQ_T_F32: return launch_behind(kv4_read_kernel<HQ_T_F32>, grid, kRowsThreads, 0, st, a, per);
-    case HQ_T_F16: return launch_behind(kv4_read_kernel<HQ_T_F16>, grid, kRowsThreads, 0, st, a, per);
-    default: return launch_behind(kv4_read_kernel<HQ_T_BF16>, grid, kRowsThreads, 0, st, a, per);
+    case HQ_T_F32: return go(kv4_read_kernel<HQ_T_F32, true>, kv4_read_kernel<HQ_T_F32, false>);
+    case HQ_T_F16: return go(kv4_read_kernel<HQ_T_F16, true>, kv4_read_kernel<HQ_T_F16, false>);
+    default: return go(kv4_read_kernel<HQ_T_BF16, true>, kv4_read_kernel<HQ_T_BF16, false>);
   }
 }
 
