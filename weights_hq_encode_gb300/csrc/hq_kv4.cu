@@ -332,13 +332,14 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *s_w, int fl
 }
 
 // The positions that one head of one sequence keeps.  The competing masses'
-// keys are read once (the first `cached` into shared memory) for their least and
-// largest; the threshold is found digit by digit of (key - least), 11 bits at a
-// time from the top of that range, by histograms in shared memory; a last pass in
-// order compacts what lies above it and the first of what equals it.  Digits of the
-// range and not of the key: masses of a few binary orders spread over all 2048 bins, where
-// the key's own top bits are a handful of values and their atomics one
-// behind another (28 us for 128 heads of 29000 tokens).
+// keys are read once (the first `cached` into shared memory, four at a time from
+// there on) for their least and largest; the threshold is found digit by digit
+// of (key - least), 11 bits at a time from the top of that range, by
+// histograms in shared memory; a last pass in order compacts what lies above it
+// and the first of what equals it.  Digits of the range and not of the key:
+// masses of a few binary orders spread over all 2048 bins, where the key's own
+// top bits are a handful of values and their atomics one behind another.
+// cached: a multiple of 4.
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a, int cached) {
   extern __shared__ __align__(16) uint32_t s_keys[];
   __shared__ uint32_t s_hist[kSelBins];
@@ -363,6 +364,8 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a,
     s_most = 0u;
   }
   __syncthreads();
+  const int near = min(old, cached);             // keys in shared memory; a few behind them fill up a four
+  uint4 *const s_keys4 = reinterpret_cast<uint4 *>(s_keys);
   uint32_t least = 0xFFFFFFFFu, most = 0u;
 #pragma unroll 8
   for (int i = tid; i < old; i += kSelThreads) {
@@ -379,7 +382,8 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a,
   }
   __syncthreads();
   least = s_least;
-  const auto key_of = [&](int i) { return (i < cached ? s_keys[i] : mass_key(mass[i])) - least; };
+  // fillers are least keys behind all others: equals go to the lower position, so none is kept
+  if (tid < 3 && near + tid < ((near + 3) & ~3)) s_keys[near + tid] = least;
   int shift = 32 - __clz((int)(s_most - least));  // bits of the range: those below `shift` are to be found
   uint32_t prefix = 0, want = (uint32_t)need;     // digits found; how many to keep among their equals
   int flip = 0;
@@ -387,13 +391,22 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a,
     const int bits = min(shift, 11);
     const uint32_t found = shift == 32 ? 0u : 0xFFFFFFFFu << shift;   // bits of the digits found
     shift -= bits;
+    const uint32_t mask = (1u << bits) - 1;
     for (int i = tid; i < kSelBins; i += kSelThreads) s_hist[i] = 0;
     __syncthreads();
-#pragma unroll 4
-    for (int i = tid; i < old; i += kSelThreads) {
-      const uint32_t key = key_of(i);
-      if ((key & found) == prefix) atomicAdd(&s_hist[(key >> shift) & ((1u << bits) - 1)], 1u);
+    const auto count = [&](uint32_t key) {
+      key -= least;
+      if ((key & found) == prefix) atomicAdd(&s_hist[(key >> shift) & mask], 1u);
+    };
+#pragma unroll 2
+    for (int i = tid; 4 * i < near; i += kSelThreads) {
+      const uint4 k = s_keys4[i];
+      count(k.x);
+      count(k.y);
+      count(k.z);
+      count(k.w);
     }
+    for (int i = cached + tid; i < old; i += kSelThreads) count(mass_key(mass[i]));
     __syncthreads();
     // bins from the largest down, two a thread
     const uint32_t d0 = kSelBins - 1 - 2 * tid, c0 = s_hist[d0], c1 = s_hist[d0 - 1];
@@ -409,29 +422,40 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a,
     prefix |= s_digit << shift;
     want -= s_above;
   }
+  __syncthreads();                                // the fillers, when no digit was to be found
+  // 8 keys a thread in a step: those above the threshold so far in the low half of a word, its
+  // equals in the high half
+  const uint32_t level = prefix + least;
   uint32_t gt_before = 0, eq_before = 0;
-  for (int base = 0; base < old; base += 4 * kSelThreads) {
-    uint32_t key[4], c = 0;
+  for (int base = 0; base < old; base += 8 * kSelThreads) {
+    const int at = base + 8 * tid;
+    uint32_t key[8], c = 0;
+    if (at + 8 <= cached) {                       // what lies behind `near` is not looked at
+      const uint4 x = s_keys4[at / 4], y = s_keys4[at / 4 + 1];
+      key[0] = x.x; key[1] = x.y; key[2] = x.z; key[3] = x.w;
+      key[4] = y.x; key[5] = y.y; key[6] = y.z; key[7] = y.w;
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = base + 4 * tid + j;
-      key[j] = i < old ? key_of(i) : 0u;
-      if (i < old) c += key[j] > prefix ? 1u : key[j] == prefix ? 0x10000u : 0u;
+      for (int j = 0; j < 8; ++j) key[j] = at + j < old ? mass_key(mass[at + j]) : 0u;
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (at + j < old) c += key[j] > level ? 1u : key[j] == level ? 0x10000u : 0u;
     uint32_t total;
     const uint32_t incl = block_scan(c, s_w, flip, &total), excl = incl - c;
     flip ^= 1;
-    uint32_t gt = gt_before + (excl & 0xFFFFu), eq = eq_before + (excl >> 16);
+    if (c != 0) {
+      uint32_t gt = gt_before + (excl & 0xFFFFu), eq = eq_before + (excl >> 16);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = base + 4 * tid + j;
-      if (i >= old) break;
-      if (key[j] > prefix) {
-        kept[gt + min(eq, want)] = i;
-        ++gt;
-      } else if (key[j] == prefix) {
-        if (eq < want) kept[gt + eq] = i;
-        ++eq;
+      for (int j = 0; j < 8; ++j) {
+        if (at + j >= old) break;
+        if (key[j] > level) {
+          kept[gt + min(eq, want)] = at + j;
+          ++gt;
+        } else if (key[j] == level) {
+          if (eq < want) kept[gt + eq] = at + j;
+          ++eq;
+        }
       }
     }
     gt_before += total & 0xFFFFu;
