@@ -96,11 +96,13 @@ __global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(Kv4RowArgs 
   const int64_t entry = (int64_t)blockIdx.x * (kRowsThreads / 8) + tl;
   const int64_t i = kv4_divide(entry, a.c.n_kv, a.c.kv_shift);
   const int h = (int)(entry - i * a.c.n_kv);
+  // K and V rows one after the other, or, in short calls, in blocks of their own (gridDim.y 2)
+  const auto takes = [](int which) { return gridDim.y == 1 || (int)blockIdx.y == which; };
   Row16<KIND> rows[2];
   uint32_t place = kNoPlace;
   if (i < a.n_tokens) {                          // every lane stays for the transform
-    rows[0].load(a.rows.k, i * a.rows.k_token + h * a.rows.k_head, r, a.rows.vec != 0);
-    rows[1].load(a.rows.v, i * a.rows.v_token + h * a.rows.v_head, r, a.rows.vec != 0);
+    if (takes(0)) rows[0].load(a.rows.k, i * a.rows.k_token + h * a.rows.k_head, r, a.rows.vec != 0);
+    if (takes(1)) rows[1].load(a.rows.v, i * a.rows.v_token + h * a.rows.v_head, r, a.rows.vec != 0);
     const int seq = a.seq[i], pos = a.pos[i];
     if (seq >= 0) {
       place = kv4_place(a.c, seq, pos, h);
@@ -115,6 +117,7 @@ __global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(Kv4RowArgs 
   const int tok = place % kUnit;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
+    if (!takes(which)) continue;
     float x[16], y[16];
     rows[which].get(mw, x);
     if (which == 1) __syncwarp();                // the table is free
@@ -367,8 +370,20 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a,
   const int near = min(old, cached);             // keys in shared memory; a few behind them fill up a four
   uint4 *const s_keys4 = reinterpret_cast<uint4 *>(s_keys);
   uint32_t least = 0xFFFFFFFFu, most = 0u;
+  int from = 0;                                  // where the loads one by one begin
+  if ((reinterpret_cast<uintptr_t>(mass) & 15) == 0) {
+    from = near & ~3;
 #pragma unroll 8
-  for (int i = tid; i < old; i += kSelThreads) {
+    for (int i = tid; 4 * i < from; i += kSelThreads) {
+      const float4 m = reinterpret_cast<const float4 *>(mass)[i];
+      const uint4 k = make_uint4(mass_key(m.x), mass_key(m.y), mass_key(m.z), mass_key(m.w));
+      s_keys4[i] = k;
+      least = min(least, min(min(k.x, k.y), min(k.z, k.w)));
+      most = max(most, max(max(k.x, k.y), max(k.z, k.w)));
+    }
+  }
+#pragma unroll 8
+  for (int i = from + tid; i < old; i += kSelThreads) {
     const uint32_t key = mass_key(mass[i]);
     if (i < cached) s_keys[i] = key;
     least = min(least, key);
@@ -512,7 +527,8 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_move_kernel(Kv4EvictArgs a, 
 
 // ---------------------------------------------------------------- launches
 int launch_kv4_append(const Kv4RowArgs &a, cudaStream_t st) {
-  const dim3 grid((unsigned)((a.n_tokens * a.c.n_kv + kRowsThreads / 8 - 1) / (kRowsThreads / 8)));
+  const unsigned blocks = (unsigned)((a.n_tokens * a.c.n_kv + kRowsThreads / 8 - 1) / (kRowsThreads / 8));
+  const dim3 grid(blocks, blocks <= 152 * 5 / 2 ? 2 : 1);      // twice the blocks while they fit at once
   switch (a.rows.kind) {
     case HQ_T_F32: return launch_behind(kv4_append_kernel<HQ_T_F32>, grid, kRowsThreads, 0, st, a);
     case HQ_T_F16: return launch_behind(kv4_append_kernel<HQ_T_F16>, grid, kRowsThreads, 0, st, a);
