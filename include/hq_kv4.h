@@ -91,7 +91,8 @@ int hq_kv4_append(const hq_kv4_cache *c, const void *d_k, const void *d_v, int k
 
 /* Gives rows of the cache back as the values they stand for,
  * D H (c - 7.5) s / sqrt(128) rounded to `kind`.  Arguments as for
- * hq_kv4_append, d_k and d_v being written; padding tokens' rows are left as
+ * hq_kv4_append, d_k and d_v being written (no two rows overlap; a token may be
+ * read more than once); padding tokens' rows are left as
  * they were, rows that HQ_ERR_PAGE names become zeros.  With the head stride
  * of [n_kv_heads][tokens][128] the rows are a slab for hq_encode. */
 int hq_kv4_read(const hq_kv4_cache *c, const int32_t *d_seq, const int32_t *d_pos,
@@ -142,13 +143,14 @@ int hq_kv4_attention(const hq_kv4_cache *c, const int32_t *d_lengths, const void
  *   d_mass         [n_seqs][n_kv_heads][src capacity] fp32
  *   dst            n_seqs, n_kv_heads and signs of src; capacity >= min(budget,
  *                  src capacity)
- *   budget         >= 1; recent: 0 .. budget
+ *   budget         1 .. 2^30; recent: 0 .. budget
  *   d_kept         [n_seqs][n_kv_heads][budget] int32: the positions kept,
  *                  then -1
  *   d_new_lengths  [n_seqs] int32: min(length, budget)
  *   d_new_mass     [n_seqs][n_kv_heads][dst capacity] fp32: the kept tokens'
  *                  mass; entries from the new length on are left as they were
- * d_kept, d_new_lengths and d_new_mass overlap no input.  d_status is OR-ed
+ * d_kept, d_new_lengths and d_new_mass overlap no input (new lengths or masses
+ * in the place of the old ones are refused).  d_status is OR-ed
  * with HQ_ERR_PAGE. */
 int hq_kv4_evict(const hq_kv4_cache *src, const int32_t *d_lengths, const float *d_mass,
                  const hq_kv4_cache *dst, int budget, int recent, int32_t *d_kept,

@@ -161,8 +161,8 @@ def test_attention_refusals(hq):
 
 
 def call_evict(hq, src, dst, **kw):
-    a = dict(lengths=FAKE, mass=FAKE, budget=64, recent=8, kept=FAKE, new_lengths=FAKE,
-             new_mass=FAKE, status=FAKE)
+    a = dict(lengths=FAKE, mass=FAKE, budget=64, recent=8, kept=FAKE + 4096,
+             new_lengths=FAKE + 8192, new_mass=FAKE + 12288, status=FAKE)
     a.update(kw)
     return hq.lib().hq_kv4_evict(ctypes.byref(src), a["lengths"], a["mass"], ctypes.byref(dst),
                                  a["budget"], a["recent"], a["kept"], a["new_lengths"],
@@ -176,7 +176,9 @@ def test_evict_refusals(hq):
         assert call_evict(hq, cache(hq), cache(hq, **{**other, **bad})) == hq.HQ_ERR_INVALID, bad
     for bad in (dict(lengths=None), dict(mass=None), dict(kept=None), dict(new_lengths=None),
                 dict(new_mass=None), dict(status=None), dict(budget=0), dict(budget=-1),
-                dict(recent=-1), dict(recent=65), dict(mass=FAKE + 2), dict(kept=FAKE + 1)):
+                dict(recent=-1), dict(recent=65), dict(mass=FAKE + 2), dict(kept=FAKE + 1),
+                dict(budget=(1 << 30) + 1), dict(budget=0x7FFFFFFF), dict(new_lengths=FAKE),
+                dict(new_mass=FAKE)):                     # in place of an input
         assert call_evict(hq, cache(hq), cache(hq, **other), **bad) == hq.HQ_ERR_INVALID, bad
     for dst in (dict(n_seqs=2), dict(n_kv_heads=1), dict(table_width=1)):
         assert call_evict(hq, cache(hq), cache(hq, **{**other, **dst})) == hq.HQ_ERR_INVALID, dst
@@ -207,6 +209,11 @@ def test_binding_refuses_what_does_not_fit(hq):
     with pytest.raises(ValueError):
         hq.make_kv4_cache(torch.zeros(2112, dtype=torch.uint8), torch.zeros((1, 1), dtype=torch.int32),
                           24, 1, torch.zeros(4, dtype=torch.int32))
+    with pytest.raises(ValueError):                      # 16 once cut to 32 bits
+        hq.make_kv4_cache(torch.zeros(2112, dtype=torch.uint8), torch.zeros((1, 1), dtype=torch.int32),
+                          (1 << 32) + 16, 1, torch.zeros(4, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        hq.hq_kv4_page_bytes(1 << 32 | 1, 16)
     with pytest.raises(TypeError):
         hq.make_kv4_cache(torch.zeros(2112), torch.zeros((1, 1), dtype=torch.int32), 16, 1,
                           torch.zeros(4, dtype=torch.int32))

@@ -181,14 +181,16 @@ int hq_kv4_evict(const hq_kv4_cache *src, const int32_t *d_lengths, const float 
                  const hq_kv4_cache *dst, int budget, int recent, int32_t *d_kept,
                  int32_t *d_new_lengths, float *d_new_mass, uint32_t *d_status,
                  hq_stream_t stream) {
-  if (!cache_ok(src) || !cache_ok(dst) || !d_status || budget < 1 || recent < 0 || recent > budget ||
+  if (!cache_ok(src) || !cache_ok(dst) || !d_status || budget < 1 ||
+      budget > kMaxCapacity || recent < 0 || recent > budget ||
       src->n_seqs != dst->n_seqs || src->n_kv_heads != dst->n_kv_heads)
     return HQ_ERR_INVALID;
   if (src->n_seqs == 0) return HQ_OK;
   const int64_t cap = (int64_t)src->table_width * src->page_tokens;
   const int64_t dcap = (int64_t)dst->table_width * dst->page_tokens;
   if (dcap < (budget < cap ? budget : cap) || !d_lengths || !d_kept || !d_new_lengths ||
-      (cap > 0 && (!d_mass || !d_new_mass || src->d_table == dst->d_table)))
+      (cap > 0 && (!d_mass || !d_new_mass || src->d_table == dst->d_table || d_new_mass == d_mass)) ||
+      d_new_lengths == d_lengths)
     return HQ_ERR_INVALID;
   if (!aligned(d_mass, 4) || !aligned(d_new_mass, 4) || !aligned(d_kept, 4) ||
       !aligned(d_lengths, 4) || !aligned(d_new_lengths, 4))

@@ -313,7 +313,15 @@ def _launch(cache, call, stream, *args) -> int:
         return call(*args, raw)
 
 
+def _fits_int(**values) -> None:
+    """ctypes would cut larger values to 32 bits."""
+    for name, v in values.items():
+        if not -2**31 <= v < 2**31:
+            raise ValueError(f"{name} must fit 32 bits, not {v}")
+
+
 def hq_kv4_page_bytes(n_kv_heads: int, page_tokens: int) -> int:
+    _fits_int(n_kv_heads=n_kv_heads, page_tokens=page_tokens)
     return int(_lib.hq_kv4_page_bytes(n_kv_heads, page_tokens))
 
 
@@ -334,6 +342,7 @@ def make_kv4_cache(pages: torch.Tensor, table: torch.Tensor, page_tokens: int, n
             raise ValueError("pages, table and signs must be on one CUDA device")
     if pages.numel() % page or table.dim() != 2 or signs.numel() != 4:
         raise ValueError("expected whole pages, a table [n_seqs, width] and 4 words of signs")
+    _fits_int(n_seqs=table.shape[0], table_width=table.shape[1])
     c = hq_kv4_cache(pages.data_ptr(), pages.numel() // page, page_tokens, n_kv_heads,
                      table.data_ptr(), table.shape[0], table.shape[1], signs.data_ptr())
     c._pages, c._table, c._signs, c._index = pages, table, signs, pages.get_device()
@@ -375,6 +384,7 @@ def hq_kv4_read(cache: hq_kv4_cache, seq: torch.Tensor, pos: torch.Tensor, k: to
 
 def hq_kv4_attention_workspace_bytes(cache: hq_kv4_cache, q_len: int, Hq: int,
                                      want_mass: bool = False) -> int:
+    _fits_int(q_len=q_len, Hq=Hq)
     return int(_lib.hq_kv4_attention_workspace_bytes(cache._ref, q_len, Hq, int(want_mass)))
 
 
@@ -413,6 +423,7 @@ def hq_kv4_evict(src: hq_kv4_cache, lengths: torch.Tensor, mass: torch.Tensor, d
     if not isinstance(kept, torch.Tensor) or kept.dim() != 3:
         raise TypeError("kept must be an int32 tensor [n_seqs, n_kv_heads, budget]")
     B, nh, budget = src.n_seqs, src.n_kv_heads, kept.shape[2]
+    _fits_int(budget=budget, recent=recent)
     return _launch(
         src, _lib.hq_kv4_evict, stream, src._ref,
         _on(lengths, src, "lengths", torch.int32, (B,)),
