@@ -14,8 +14,10 @@ addends to the largest and cut what falls below, 2 u of the largest for each:
 |c_t| = max(norm of a row's codes, 7.5 sqrt(128)), so 8 x 34 u of that, 18 u for
 the start and the pairing of dimensions, and 4 u for the products with the
 scales: |dz| <= 30 u zeta + 294 u zeta_c, zeta = |scale| |q| max |Khat_t|,
-zeta_c = |scale| |q| max s_t |c_t|, plus 8 u cap for the capped form (cap is
-multiplied by a value in [-1, 1] that is off by a few u).  exp2 is off
+zeta_c = |scale| |q| max s_t |c_t|, plus 8 u min(cap, 4 zeta) for the capped form:
+tanh(y) is off by at most 8 u (e^2|y| by 4 u and 2 |y| u, of which less than half
+arrives, a quotient by 4 u, a sum and a difference by u each), and below |y| = 1/4,
+where a series takes over, by 6 u for its rest and u for each of 4 roundings of y.  exp2 is off
 by 4 u, so the softmax's weights are off by 2 |dz| + 12 u and their sum by u
 for each of at most T / 16 + 20 additions on a thread and across threads.  The value
 side splits the weights into two fp16 parts (4 u) and adds centred codes: an
@@ -215,7 +217,8 @@ def check(C, q, scale, cap, got, kind="f32", mass=None, lens=None, plain=False):
                       q.double().cpu().numpy(), MASK, scale, cap, m)
     out, lse, mass_out = (None if t is None else t.double().cpu().numpy() for t in got)
     steps = max(lens) / 16 if len(lens) else 0
-    score = 30 * U * ref["zeta"] + 294 * U * ref["zeta_codes"] + 8 * U * cap
+    min_cap = np.minimum(cap, 4 * ref["zeta"])
+    score = 30 * U * ref["zeta"] + 294 * U * ref["zeta_codes"] + 8 * U * min_cap
     tol = ((2 * score + (34 * steps + 100) * U) * np.linalg.norm(ref["size"], axis=-1) +
            600 * U * np.sqrt(128.0) * ref["scales"])
     rounding = HALF_STEP[kind] * np.linalg.norm(ref["out"], axis=-1) * 1.01
@@ -283,6 +286,16 @@ def test_attention_against_reference(hq, case):
     again = attend(hq, C, q, 128 ** -0.5, cap, DT[do], m, lse=False)
     assert torch.equal(got[0], again[0])         # the order of the sums is fixed
     assert got[2] is None or torch.equal(got[2], again[2])
+
+
+@pytest.mark.parametrize("cap", [2.0 ** 10, 2.0 ** 20, 2.0 ** 100])
+def test_attention_caps_far_above_the_scores(hq, cap):
+    """Scores that the cap hardly bends keep their own precision, not the cap's."""
+    rng = np.random.default_rng(19)
+    C = Cache(hq, rng, [300, 33], 2, 32)
+    for G in (4, 6):
+        q = queries(rng, 2, 1, 2 * G, "f32")
+        check(C, q, 0.1, cap, attend(hq, C, q, 0.1, cap, torch.float32), plain=True)
 
 
 def test_attention_many_ragged_sequences(hq):

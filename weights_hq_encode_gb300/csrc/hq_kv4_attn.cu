@@ -85,6 +85,25 @@ __device__ __forceinline__ void code_pairs(uint32_t x, uint32_t factor, uint32_t
   p[2] = centred(y & 0x000F000Fu, factor, 0xA380A380u);
   p[3] = centred(y, factor, 0xB3F8B3F8u);
 }
+// cap tanh(y) of two values: y's sign and 1 - 2 / (1 + e^2|y|) from 1/4 on; below, where
+// that is off by 2^-23 beside a small value, y - y^3 / 3 + 2 y^5 / 15 - 17 y^7 / 315, whose rest
+// is less than 3.4e-7 of it.
+__device__ __forceinline__ uint64_t cap_tanh(uint64_t yy, float cap) {
+  const uint64_t y2 = mul2(yy, yy);
+  uint64_t t = fma2(y2, pk2(-17.0f / 315.0f, -17.0f / 315.0f), pk2(2.0f / 15.0f, 2.0f / 15.0f));
+  t = fma2(y2, t, pk2(-1.0f / 3.0f, -1.0f / 3.0f));
+  t = fma2(mul2(yy, y2), t, yy);
+  float y[2], p[2];
+  upk2(yy, y[0], y[1]);
+  upk2(t, p[0], p[1]);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float ey = ex2(__fmul_rn(fabsf(y[e]), 2.0f * kLog2e));
+    const float far = copysignf(__fsub_rn(1.0f, __fdividef(2.0f, __fadd_rn(ey, 1.0f))), y[e]);
+    p[e] = __fmul_rn(cap, fabsf(y[e]) < 0.25f ? p[e] : far);
+  }
+  return pk2(p[0], p[1]);
+}
 __device__ __forceinline__ void mma16816(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -561,15 +580,9 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
           const float o0 = __shfl_xor_sync(0xffffffffu, low ? s[g][0] : s[g][2], 2);
           const float o1 = __shfl_xor_sync(0xffffffffu, low ? s[g][1] : s[g][3], 2);
           const uint64_t own = low ? pk2(s[g][2], s[g][3]) : pk2(s[g][0], s[g][1]);
-          upk2(mul2(fma2(pk2(o0, o1), m_other[g], mul2(own, m_own[g])), pk2(sk, sk)), z[un][g][0], z[un][g][1]);
-          if (CAP) {                             // cap tanh(y) = cap (1 - 2 / (1 + e^2|y|)), y's sign
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float y = z[un][g][e], ey = ex2(__fmul_rn(fabsf(y), 2.0f * kLog2e));
-              z[un][g][e] = copysignf(
-                  __fmul_rn(cap_l2, __fsub_rn(1.0f, __fdividef(2.0f, __fadd_rn(ey, 1.0f)))), y);
-            }
-          }
+          const uint64_t zz = mul2(fma2(pk2(o0, o1), m_other[g], mul2(own, m_own[g])), pk2(sk, sk));
+          upk2(zz, z[un][g][0], z[un][g][1]);
+          if (CAP) upk2(cap_tanh(zz, cap_l2), z[un][g][0], z[un][g][1]);
         }
       }
       // warp-uniform: not every row sees every token
