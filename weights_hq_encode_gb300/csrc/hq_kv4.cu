@@ -87,7 +87,9 @@ __device__ __forceinline__ uint2 words_of_columns(uint32_t even, uint32_t odd, i
 // Codes K and V rows, 8 lanes an entry as the codec's kernels hold a tile
 // (lane r: dimensions 16 r .. 16 r + 15), so that the transform is the codec's,
 // its stages in the codec's order.  It is not taken back to the lanes'
-// dimensions in fp32: the codes are, 8 bytes a lane instead of 64.
+// dimensions in fp32: the codes are, 8 bytes a lane instead of 64.  Bound by
+// instruction issue (71% of the cycles): 289000 entries in bf16 take 58 us where
+// their 186 MB want 27.
 template <int KIND>
 __global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(Kv4RowArgs a) {
   __shared__ __align__(16) float s_tr[(kRowsThreads / 8) * kTrTile];
@@ -199,9 +201,9 @@ __device__ __forceinline__ void store4(char *to, const float v[4], const uint32_
 // exact (+-1 times half-integers, sums below 2^10 in fp16 and fp32), so the
 // one rounding is that of the product with the scale; and a lane ends with
 // dimensions 8 n8 + 2 c4 and the next, and the same + 64: whole 128-byte
-// stores.  The codec's transform in registers and shared memory instead was bound
-// by its 330 instructions for 4 rows (68 us for 262144 entries to bf16, 25 of
-// them the memory's).
+// stores.  262144 entries to bf16: 37.5 us, 25 of them the memory's, bound by the
+// issue of 81 instructions an entry (56% of the cycles).  The codec's transform
+// in registers and shared memory instead takes 330 for 4 rows, 68 us.
 constexpr int kReadBatch = 4;                    // entries of a warp at a time
 template <int KIND, bool VEC>
 __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(Kv4RowArgs a, int per_warp) {
@@ -342,7 +344,8 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *s_w, int fl
 // and the first of what equals it.  Digits of the range and not of the key:
 // masses of a few binary orders spread over all 2048 bins, where the key's own
 // top bits are a handful of values and their atomics one behind another.
-// cached: a multiple of 4.
+// cached: a multiple of 4.  16 x 32768 tokens of 8 heads: 128 blocks, one a
+// multiprocessor, 21 us for 15 MB of masses, bound by the passes over a block's keys.
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a, int cached) {
   extern __shared__ __align__(16) uint32_t s_keys[];
   __shared__ uint32_t s_hist[kSelBins];
@@ -480,7 +483,9 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a,
 
 // Rows and masses of the kept positions, up to 32 a warp: a lane looks one up,
 // moves its scales and its mass; then 8 lanes a row move the codes, all rows'
-// loads before the first store.
+// loads before the first store.  16 x 4096 of 32768 tokens, 8 heads: 40 us for 69 MB
+// each way, 179 MB read: a kept V row's pieces lie in the 128 bytes of its token
+// pair, and the memory delivers 64 at a time.
 __global__ void __launch_bounds__(kRowsThreads) kv4_move_kernel(Kv4EvictArgs a, int per_warp) {
   follow_launch();
   const int lane = threadIdx.x & 31, r = lane & 7, h = blockIdx.y, b = blockIdx.z;

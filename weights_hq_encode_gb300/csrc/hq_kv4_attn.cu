@@ -373,9 +373,13 @@ __device__ Piece find_piece(const Kv4AttnArgs &a) {
 // against the 128 bytes a cycle that shared memory takes, 16 cycles for reading and
 // writing a token beside the 5 to 6 in which memory delivers it.
 //
-// 16 sequences x 32768 tokens x 8 heads, 4 query rows a head: 113 us, 4.9 TB/s,
-// 72% of the copy rate; the copies alone take 98 us, the rest is what instruction
-// issue (about 300 a warp for 16 tokens) does not hide.
+// 16 sequences x 32768 tokens x 8 heads, 4 query rows a head: 110 us, 5.0 TB/s,
+// 74% of the copy rate; the copies alone take 98 us, the rest is what instruction
+// issue (about 293 a warp for 16 tokens, 54% of the cycles) does not hide.  One
+// sequence of 131072 tokens: 37 us, of which 15 do not depend on its length (the
+// first tile's way 5, the end and the join 6).  With 16 query rows a head the
+// codes are unpacked for every 8 of them: 24 x 2200 tokens 56 us, bound by
+// the latency of 8 warps a multiprocessor (issue 49%, tensor cores 35%).
 template <int NC, bool CAP, bool MASS>
 __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kernel(Kv4AttnArgs a) {
   constexpr int kRows = Shape<NC>::rows;
