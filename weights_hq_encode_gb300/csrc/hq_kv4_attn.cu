@@ -29,18 +29,13 @@ constexpr int kTileTokens = kUnits * kUnit, kStageBytes = kUnits * kUnitBytes;
 constexpr int kStages = 3;                       // tiles a warp has in its ring
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 
-// NC column groups of 8: the high and the low parts of 4 query rows each
-template <int NC>
+// Blocks of 4, 8 or 16 query rows
+template <int ROWS>
 struct Shape {
-  static constexpr int rows = 4 * NC;            // query rows of a block
-  // Resident blocks a multiprocessor: 12 warps of 168 registers, or 8 of 255.
-  // More warps of fewer registers keep parts of a tile in local memory: 16
-  // of 128 took 118 us instead of 110 for 16 x 32768 tokens of 8 heads and 4
-  // query rows, 12 of 168 with 8 rows 60 instead of 54 for 16 x 8192.
-  static constexpr int blocks = NC == 1 ? 3 : 2;
-  static constexpr int q_bytes = 8 * NC * 32 * 8;   // query fragments: 8 K steps, 8 bytes a lane
-  static constexpr int smem = kRingBytes + q_bytes + rows * kTrTile * 4;
-  static_assert(kWarps * rows * kTile * 4 <= kRingBytes, "the warps' sums fit the ring");
+  static constexpr int q_bytes = 2 * ROWS * kTile * 2;      // query fragments, high and low parts
+  static constexpr int smem = kRingBytes + q_bytes + ROWS * kTrTile * 4;
+  static constexpr int blocks = ROWS == 4 ? 3 : 2;          // resident blocks a multiprocessor
+  static_assert(kWarps * ROWS * kTile * 4 <= kRingBytes, "the warps' sums fit the ring");
 };
 
 // Work of one (sequence, head, row tile) beyond its units, in units: the
@@ -160,6 +155,15 @@ __device__ __forceinline__ void split2(float lo, float hi, uint32_t &h, uint32_t
   const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
   float r0, r1;                                  // exact: 2^11 x - 2^11 h
   upk2(fma2(pk2(f.x, f.y), pk2(-kLoScale, -kLoScale), mul2(pk2(lo, hi), pk2(kLoScale, kLoScale))), r0, r1);
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(rest) : "f"(r1), "f"(r0));
+}
+
+// The same with the rests as they are: they miss a value by 2^-22 of it, and by 2^-25.
+__device__ __forceinline__ void split2_plain(float lo, float hi, uint32_t &h, uint32_t &rest) {
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+  float r0, r1;
+  upk2(sub2(pk2(lo, hi), pk2(f.x, f.y)), r0, r1);          // exact
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(rest) : "f"(r1), "f"(r0));
 }
 
@@ -380,16 +384,19 @@ __device__ Piece find_piece(const Kv4AttnArgs &a) {
 // first tile's way 5, the end and the join 6).  With 16 query rows a head the
 // codes are unpacked for every 8 of them: 24 x 2200 tokens 56 us, bound by
 // the latency of 8 warps a multiprocessor (issue 49%, tensor cores 35%).
-template <int NC, bool CAP, bool MASS>
-__global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kernel(Kv4AttnArgs a) {
-  constexpr int kRows = Shape<NC>::rows;
+template <int kRows, bool CAP, bool MASS>
+__global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_kernel(Kv4AttnArgs a) {
+  constexpr bool kWide = kRows > 4;              // high and low parts in products of their own
+  constexpr int kGroups = kWide ? kRows / 8 : 1; // of 8 columns
+  constexpr int kHalves = kWide ? 2 : 1;         // tokens of a unit that a lane goes on with
+  constexpr int kApart = kWide ? 4 : 2;          // lanes this far and further apart share rows
   extern __shared__ __align__(128) unsigned char s_mem[];
   __shared__ RowStat s_stat[kWarps][kRows];
   __shared__ float s_mul[kRows];                 // multiplier of the scores
   __shared__ int s_seen[kRows];                  // tokens seen
   uint2 *const s_q = reinterpret_cast<uint2 *>(s_mem + kRingBytes);
   float *const s_acc = reinterpret_cast<float *>(s_mem);   // in the ring's place
-  float *const s_tr = reinterpret_cast<float *>(s_mem + kRingBytes + Shape<NC>::q_bytes);
+  float *const s_tr = reinterpret_cast<float *>(s_mem + kRingBytes + Shape<kRows>::q_bytes);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   unsigned char *const ring = s_mem + warp * kStages * kStageBytes;
   const uint32_t ring_a = smem_addr(ring);
@@ -402,9 +409,9 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
   Walk walk{piece.begin, piece.end, piece.b_begin, piece.b};
   Segment seg;
   const int n8 = lane >> 2, c4 = lane & 3;       // fragment row group, and place in it
-  const bool low = c4 >= 2;                      // this lane's columns are low parts
-  const int e0 = 2 * (c4 & 1);                   // its rows of a column group: e0, e0 + 1
-  const int tok = n8 + (low ? 8 : 0);            // its token of a unit
+  const bool low = !kWide && c4 >= 2;            // this lane's columns are low parts
+  const int e0 = kWide ? 2 * c4 : 2 * (c4 & 1);  // its rows of a group: e0, e0 + 1
+  const int tok = n8 + (low ? 8 : 0);            // its token of a unit (8 or 16 rows: and the one 8 further on)
   const uint32_t ld_v = kUnitV + c4 * 128 + ((n8 ^ (2 * c4)) * 16);
   const uint64_t policy = stream_policy();
   uint32_t factor;                               // 2^15 twice, in a register that is not filled again
@@ -492,7 +499,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
         x[i] = __fmaf_rn(__fmul_rn(x[i], sc), 16.0f, -x[i + 1]);
       }
       // lane r holds words 2 (r & 1), 2 (r & 1) + 1 of the 32 dimensions of place r / 2; row rr is
-      // columns rr % 4 (high parts) and rr % 4 + 4 (low parts) of group rr / 4
+      // column rr % 8 of group rr / 8, high and low parts side by side, or, with 4 rows, columns rr
+      // (high) and rr + 4 (low)
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
 #pragma unroll
@@ -500,9 +508,14 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
           uint2 hi, lo;
           split2(x[8 * w + 2 * i], x[8 * w + 2 * i + 4], hi.x, lo.x);
           split2(x[8 * w + 2 * i + 1], x[8 * w + 2 * i + 5], hi.y, lo.y);
-          uint2 *dst = s_q + ((2 * (2 * (r & 1) + w) + i) * NC + (rr >> 2)) * 32 + (rr & 3) * 4 + (r >> 1);
-          dst[0] = hi;
-          dst[16] = lo;
+          const int k = 2 * (2 * (r & 1) + w) + i;
+          if constexpr (kWide) {
+            reinterpret_cast<uint4 *>(s_q)[(k * kRows + rr) * 4 + (r >> 1)] = make_uint4(hi.x, hi.y, lo.x, lo.y);
+          } else {
+            uint2 *dst = s_q + k * 32 + rr * 4 + (r >> 1);
+            dst[0] = hi;
+            dst[16] = lo;
+          }
         }
       }
       if (r == 0) {
@@ -513,13 +526,14 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
     __syncthreads();
     // query fragments: in registers with 4 rows, else read beside every use
     uint2 qr[8];
+    if (!kWide) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) qr[k] = s_q[k * NC * 32 + lane];
-    const auto query = [&](int k, int g) { return NC == 1 ? qr[k] : s_q[(k * NC + g) * 32 + lane]; };
-    uint64_t m_own[NC], m_other[NC];             // multipliers of this lane's and its partner's part
+      for (int k = 0; k < 8; ++k) qr[k] = s_q[k * 32 + lane];
+    }
+    uint64_t m_own[kGroups], m_other[kGroups];   // multipliers of this lane's and the other part
 #pragma unroll
-    for (int g = 0; g < NC; ++g) {
-      const uint64_t mul = pk2(s_mul[4 * g + e0], s_mul[4 * g + e0 + 1]);
+    for (int g = 0; g < kGroups; ++g) {
+      const uint64_t mul = pk2(s_mul[8 * g + e0], s_mul[8 * g + e0 + 1]);
       m_own[g] = mul2(mul, pk2(k_own, k_own));
       m_other[g] = mul2(mul, pk2(k_other, k_other));
     }
@@ -528,9 +542,9 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
 
     // sums: l of 2^(z - m), acc of w (c - 7.5) 2^-9, w = 2^(z - m) s f, f a power of two a row;
     // acc of odd dimensions with 16 times theirs and the even one's before them
-    float acc[NC][8][4], l[NC][2], m[NC][2], f[NC][2];
+    float acc[kGroups][8][4], l[kGroups][2], m[kGroups][2], f[kGroups][2];
 #pragma unroll
-    for (int g = 0; g < NC; ++g) {
+    for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -554,14 +568,15 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
       have >>= kUnits;
       get += kStageBytes;
       if (get == kStages * kStageBytes) get = 0;
-      // Scores: lane (n8, c4) gets tokens n8 and n8 + 8 of a unit, columns 2 c4, 2 c4 + 1.  Lanes
-      // c4 and c4 ^ 2 hold the high and the low parts of the same rows: the first goes on with
-      // token n8, the second with token n8 + 8, each with the other's part of its token's scores.
-      float z[kUnits][NC][2], sv[kUnits];        // [unit][group][row], V's scales
+      // Scores: lane (n8, c4) gets tokens n8 and n8 + 8 of a unit, columns 2 c4, 2 c4 + 1.  With 8
+      // or 16 rows these are the rows' high parts, the low parts come in a second result.  With 4 rows
+      // lanes c4 and c4 ^ 2 hold the high and the low parts of the same rows: the first goes on with token
+      // n8, the second with token n8 + 8, each with the other's part of its token's scores.
+      float z[kUnits][kGroups][kHalves][2], sv[kUnits][kHalves];   // [unit][group][token][row], V's scales
 #pragma unroll
       for (int un = 0; un < kUnits; ++un) {
         const unsigned char *const V = U + un * kUnitBytes;
-        float s[NC][4];
+        float s[kGroups][kHalves][4];            // [group][high, low]
         const uint4 k0 = read16(V + lane * 16), k1 = read16(V + lane * 16 + 512);
         const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
@@ -570,80 +585,116 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
           code_pairs(w0[j], factor, p0);
           code_pairs(w1[j], factor, p1);
 #pragma unroll
-          for (int g = 0; g < NC; ++g) {
-            const uint2 q0 = query(2 * j, g), q1 = query(2 * j + 1, g);
-            if (j == 0) mma16816_first(s[g], p0[0], p1[0], p0[1], p1[1], q0.x, q0.y);
-            else mma16816(s[g], p0[0], p1[0], p0[1], p1[1], q0.x, q0.y);
-            mma16816(s[g], p0[2], p1[2], p0[3], p1[3], q1.x, q1.y);
+          for (int g = 0; g < kGroups; ++g) {
+            uint4 q0, q1;                        // high and low parts
+            if constexpr (kWide) {
+              q0 = reinterpret_cast<const uint4 *>(s_q)[(2 * j * kGroups + g) * 32 + lane];
+              q1 = reinterpret_cast<const uint4 *>(s_q)[((2 * j + 1) * kGroups + g) * 32 + lane];
+            } else {
+              q0 = make_uint4(qr[2 * j].x, qr[2 * j].y, 0u, 0u);
+              q1 = make_uint4(qr[2 * j + 1].x, qr[2 * j + 1].y, 0u, 0u);
+            }
+#pragma unroll
+            for (int t = 0; t < kHalves; ++t) {
+              const uint32_t b0 = t == 0 ? q0.x : q0.z, b1 = t == 0 ? q0.y : q0.w;
+              if (j == 0) mma16816_first(s[g][t], p0[0], p1[0], p0[1], p1[1], b0, b1);
+              else mma16816(s[g][t], p0[0], p1[0], p0[1], p1[1], b0, b1);
+            }
+#pragma unroll
+            for (int t = 0; t < kHalves; ++t)
+              mma16816(s[g][t], p0[2], p1[2], p0[3], p1[3], t == 0 ? q1.x : q1.z, t == 0 ? q1.y : q1.w);
           }
         }
-        const float sk = read_bf16(V + kUnitKs + 2 * tok);
-        sv[un] = read_bf16(V + kUnitVs + 2 * tok);
 #pragma unroll
-        for (int g = 0; g < NC; ++g) {
-          const float o0 = __shfl_xor_sync(0xffffffffu, low ? s[g][0] : s[g][2], 2);
-          const float o1 = __shfl_xor_sync(0xffffffffu, low ? s[g][1] : s[g][3], 2);
-          const uint64_t own = low ? pk2(s[g][2], s[g][3]) : pk2(s[g][0], s[g][1]);
-          const uint64_t zz = mul2(fma2(pk2(o0, o1), m_other[g], mul2(own, m_own[g])), pk2(sk, sk));
-          upk2(zz, z[un][g][0], z[un][g][1]);
-          if (CAP) upk2(cap_tanh(zz, cap_l2), z[un][g][0], z[un][g][1]);
+        for (int t = 0; t < kHalves; ++t) {
+          const float sk = read_bf16(V + kUnitKs + 2 * (tok + 8 * t));
+          sv[un][t] = read_bf16(V + kUnitVs + 2 * (tok + 8 * t));
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            uint64_t own, other;
+            if constexpr (kWide) {
+              own = pk2(s[g][0][2 * t], s[g][0][2 * t + 1]);
+              other = pk2(s[g][kHalves - 1][2 * t], s[g][kHalves - 1][2 * t + 1]);
+            } else {
+              const float *const x4 = s[g][0];
+              const float o0 = __shfl_xor_sync(0xffffffffu, low ? x4[0] : x4[2], 2);
+              const float o1 = __shfl_xor_sync(0xffffffffu, low ? x4[1] : x4[3], 2);
+              own = low ? pk2(x4[2], x4[3]) : pk2(x4[0], x4[1]);
+              other = pk2(o0, o1);
+            }
+            float *const zz = z[un][g][t];
+            uint64_t y = mul2(fma2(other, m_other[g], mul2(own, m_own[g])), pk2(sk, sk));
+            if (CAP) y = cap_tanh(y, cap_l2);
+            upk2(y, zz[0], zz[1]);
+          }
         }
       }
       // warp-uniform: not every row sees every token
       if (t0 + kTileTokens > seen_all || got != (1u << kUnits) - 1) {
 #pragma unroll
-        for (int un = 0; un < kUnits; ++un) {
-          const int at = t0 + kUnit * un + tok;
-          const bool none = !((got >> un) & 1u) || at >= len;
-          if (none) sv[un] = 0.0f;               // what lies there is no scale
+        for (int un = 0; un < kUnits; ++un)
 #pragma unroll
-          for (int g = 0; g < NC; ++g)
+          for (int t = 0; t < kHalves; ++t) {
+            const int at = t0 + kUnit * un + tok + 8 * t;
+            const bool none = !((got >> un) & 1u) || at >= len;
+            if (none) sv[un][t] = 0.0f;          // what lies there is no scale
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (none || at >= s_seen[4 * g + e0 + e]) z[un][g][e] = -INFINITY;
-        }
+            for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (none || at >= s_seen[8 * g + e0 + e]) z[un][g][t][e] = -INFINITY;
+          }
       }
       if (MASS) {
 #pragma unroll
-        for (int g = 0; g < NC; ++g)
+        for (int g = 0; g < kGroups; ++g)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int zr = row0 + 4 * g + e0 + e;
+            const int zr = row0 + 8 * g + e0 + e;
             if (zr >= a.R) continue;
             float *zrow = a.z + (((int64_t)seg.b * a.c.n_kv + h) * a.R + zr) * a.c.capacity() + t0 + tok;
 #pragma unroll
             for (int un = 0; un < kUnits; ++un)
-              if (t0 + kUnit * un < seg.u_hi * kUnit) zrow[kUnit * un] = z[un][g][e];
+              if (t0 + kUnit * un < seg.u_hi * kUnit) {
+#pragma unroll
+                for (int t = 0; t < kHalves; ++t) zrow[kUnit * un + 8 * t] = z[un][g][t][e];
+              }
           }
       }
       // The references m (a whole number) and f move only when a score is more than 4 above m, or a
       // weight 2^(z - m) s f could pass 2^15: f holds the row's largest weight so far near 2^7.
       float zt = kNoMax, ft = 0.0f, st = 0.0f;
 #pragma unroll
-      for (int un = 0; un < kUnits; ++un) st = fmaxf(st, sv[un]);
+      for (int un = 0; un < kUnits; ++un)
 #pragma unroll
-      for (int g = 0; g < NC; ++g)
+        for (int t = 0; t < kHalves; ++t) st = fmaxf(st, sv[un][t]);
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float top = kNoMax;
 #pragma unroll
-          for (int un = 0; un < kUnits; ++un) top = fmaxf(top, z[un][g][e]);
+          for (int un = 0; un < kUnits; ++un)
+#pragma unroll
+            for (int t = 0; t < kHalves; ++t) top = fmaxf(top, z[un][g][t][e]);
           zt = fmaxf(zt, __fsub_rn(top, m[g][e]));
           ft = fmaxf(ft, f[g][e]);
         }
       if (__any_sync(0xffffffffu, zt > 4.0f || __fmul_rn(st, ft) > 2048.0f)) {
 #pragma unroll
-        for (int g = 0; g < NC; ++g) {
+        for (int g = 0; g < kGroups; ++g)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float mt = kNoMax, ut = kNoMax;
 #pragma unroll
-            for (int un = 0; un < kUnits; ++un) {
-              mt = fmaxf(mt, z[un][g][e]);
-              ut = fmaxf(ut, __fadd_rn(z[un][g][e], lg2(sv[un])));
-            }
+            for (int un = 0; un < kUnits; ++un)
 #pragma unroll
-            for (int d = 2; d < 32; d <<= 1) {
+              for (int t = 0; t < kHalves; ++t) {
+                mt = fmaxf(mt, z[un][g][t][e]);
+                ut = fmaxf(ut, __fadd_rn(z[un][g][t][e], lg2(sv[un][t])));
+              }
+#pragma unroll
+            for (int d = kApart; d < 32; d <<= 1) {
               mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, d));
               ut = fmaxf(ut, __shfl_xor_sync(0xffffffffu, ut, d));
             }
@@ -663,25 +714,34 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
             m[g][e] = m2;
             f[g][e] = f2;
           }
-        }
       }
-      // weights: this lane's token's parts, the partner's from it
-      uint32_t pb[kUnits][NC][2];
+      // Weights.  With 8 or 16 rows the low parts are the rests themselves and go into the same sums as
+      // the high ones; with 4 rows they are 2^11 times the rests, in columns of their own, and a lane has
+      // its token's parts and takes the other token's from its partner.
+      uint32_t pb[kUnits][kGroups][kHalves][2];  // [unit][group][high, low][token n8, n8 + 8]
 #pragma unroll
       for (int un = 0; un < kUnits; ++un)
 #pragma unroll
-        for (int g = 0; g < NC; ++g) {
-          float p0, p1, w0, w1;
-          upk2(sub2(pk2(z[un][g][0], z[un][g][1]), pk2(m[g][0], m[g][1])), p0, p1);
-          const uint64_t p = pk2(ex2(p0), ex2(p1));
-          upk2(add2(pk2(l[g][0], l[g][1]), p), l[g][0], l[g][1]);
-          upk2(mul2(mul2(p, pk2(sv[un], sv[un])), pk2(f[g][0], f[g][1])), w0, w1);
-          uint32_t hi, lo;
-          split2(w0, w1, hi, lo);
-          const uint32_t from = __shfl_xor_sync(0xffffffffu, low ? hi : lo, 2);
-          pb[un][g][0] = transpose8(low ? from : hi);
-          pb[un][g][1] = transpose8(low ? lo : from);
-        }
+        for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+          for (int t = 0; t < kHalves; ++t) {
+            float p0, p1, w0, w1;
+            upk2(sub2(pk2(z[un][g][t][0], z[un][g][t][1]), pk2(m[g][0], m[g][1])), p0, p1);
+            const uint64_t p = pk2(ex2(p0), ex2(p1));
+            upk2(add2(pk2(l[g][0], l[g][1]), p), l[g][0], l[g][1]);
+            upk2(mul2(mul2(p, pk2(sv[un][t], sv[un][t])), pk2(f[g][0], f[g][1])), w0, w1);
+            uint32_t hi, lo;
+            if constexpr (kWide) {
+              split2_plain(w0, w1, hi, lo);
+              pb[un][g][0][t] = transpose8(hi);
+              pb[un][g][kHalves - 1][t] = transpose8(lo);
+            } else {
+              split2(w0, w1, hi, lo);
+              const uint32_t from = __shfl_xor_sync(0xffffffffu, low ? hi : lo, 2);
+              pb[un][g][0][0] = transpose8(low ? from : hi);
+              pb[un][g][0][1] = transpose8(low ? lo : from);
+            }
+          }
       // lane (n8, c4) holds the 16 dimensions of chunk n8 of token pairs c4 and 4 + c4
       uint4 v[kUnits][2];
 #pragma unroll
@@ -701,11 +761,13 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
             code_pairs(__byte_perm(w ? va.y : va.x, w ? va.w : va.z, pick), factor, p0);
             code_pairs(__byte_perm(w ? vb.y : vb.x, w ? vb.w : vb.z, pick), factor, p1);
 #pragma unroll
-            for (int g = 0; g < NC; ++g)
+            for (int t = kHalves - 1; t >= 0; --t)
 #pragma unroll
-              for (int j = 0; j < 2; ++j)
-                mma16816(acc[g][4 * w + 2 * hf + j], p0[2 * j], p0[2 * j + 1], p1[2 * j], p1[2 * j + 1],
-                         pb[un][g][0], pb[un][g][1]);
+              for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  mma16816(acc[g][4 * w + 2 * hf + j], p0[2 * j], p0[2 * j + 1], p1[2 * j], p1[2 * j + 1],
+                           pb[un][g][t][0], pb[un][g][t][1]);
           }
         }
       }
@@ -714,14 +776,14 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
     __syncthreads();                             // every warp's ring is free
     // ---- the block's sums: l over a row's lanes, then the warps
 #pragma unroll
-    for (int g = 0; g < NC; ++g) {
+    for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int d = 2; d < 32; d <<= 1) l[g][e] = __fadd_rn(l[g][e], __shfl_xor_sync(0xffffffffu, l[g][e], d));
-        // dimensions 16 n8 .. + 15 of row e: both lanes of a (high, low) pair form the sums, the
-        // high one stores row e0, the low one row e0 + 1
-        float *dst = s_acc + (warp * kRows + 4 * g + e0 + e) * kTile + 16 * n8;
+        for (int d = kApart; d < 32; d <<= 1) l[g][e] = __fadd_rn(l[g][e], __shfl_xor_sync(0xffffffffu, l[g][e], d));
+        // dimensions 16 n8 .. + 15 of row e; with 4 rows both lanes of a (high, low) pair form the
+        // sums, the high one stores row e0, the low one row e0 + 1
+        float *dst = s_acc + (warp * kRows + 8 * g + e0 + e) * kTile + 16 * n8;
         const float f_own = low ? 0.25f : 512.0f, f_other = low ? 512.0f : 0.25f;
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
@@ -729,14 +791,14 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NC>::blocks) kv4_attn_kern
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
             const float own = acc[g][k + (d >> 1)][2 * (d & 1) + e];
-            const float other = __shfl_xor_sync(0xffffffffu, own, 2);
-            v[d] = __fmaf_rn(other, f_other, __fmul_rn(own, f_own));
+            v[d] = __fmul_rn(own, f_own);
+            if (!kWide) v[d] = __fmaf_rn(__shfl_xor_sync(0xffffffffu, own, 2), f_other, v[d]);
             if (d & 1) v[d] = __fmul_rn(__fsub_rn(v[d], v[d - 1]), 0.0625f);
           }
-          if (low == (e == 1)) *reinterpret_cast<float4 *>(dst + 2 * k) = make_float4(v[0], v[1], v[2], v[3]);
+          if (kWide || low == (e == 1)) *reinterpret_cast<float4 *>(dst + 2 * k) = make_float4(v[0], v[1], v[2], v[3]);
         }
         if (n8 == 0 && !low)
-          s_stat[warp][4 * g + e0 + e] =
+          s_stat[warp][8 * g + e0 + e] =
               RowStat{m[g][e], l[g][e],
                       __fsub_rn(m[g][e], (float)((int)(__float_as_uint(f[g][e]) >> 23) - 127)), 0.0f};
       }
@@ -898,26 +960,26 @@ __global__ void __launch_bounds__(kMassThreads) kv4_mass_kernel(Kv4AttnArgs a) {
 
 // Resident blocks of the attention kernel on the current device (asked once
 // per instance and device).
-template <int NC, bool CAP, bool MASS>
+template <int ROWS, bool CAP, bool MASS>
 int resident_blocks() {
   static int cache[64] = {};
   int dev = 0, sms = 0, per_sm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (cudaFuncSetAttribute(kv4_attn_kernel<NC, CAP, MASS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Shape<NC>::smem) != cudaSuccess)
+  if (cudaFuncSetAttribute(kv4_attn_kernel<ROWS, CAP, MASS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Shape<ROWS>::smem) != cudaSuccess)
     return 0;
-  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kv4_attn_kernel<NC, CAP, MASS>, kAttnThreads,
-                                                Shape<NC>::smem);
+  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kv4_attn_kernel<ROWS, CAP, MASS>, kAttnThreads,
+                                                Shape<ROWS>::smem);
   const int n = sms * per_sm;
   if (dev >= 0 && dev < 64) cache[dev] = n;
   return n;
 }
 
-template <int NC, bool CAP, bool MASS>
+template <int ROWS, bool CAP, bool MASS>
 int launch_attn(const Kv4AttnArgs &a, cudaStream_t st) {
-  int grid = resident_blocks<NC, CAP, MASS>();
+  int grid = resident_blocks<ROWS, CAP, MASS>();
   if (grid <= 0) return 1;
   if (grid > kKv4MaxBlocks) grid = kKv4MaxBlocks;
   // no more blocks than pieces of the longest batch the table allows
@@ -928,31 +990,31 @@ int launch_attn(const Kv4AttnArgs &a, cudaStream_t st) {
   Kv4AttnArgs w = a;
   w.whole = pairs <= grid && a.c.capacity() / kUnit + kSegmentCost <= kWholeSpan;
   if (w.whole) grid = (int)pairs;
-  if (launch_behind(kv4_attn_kernel<NC, CAP, MASS>, dim3((unsigned)grid), kAttnThreads, Shape<NC>::smem, st, w) != 0)
+  if (launch_behind(kv4_attn_kernel<ROWS, CAP, MASS>, dim3((unsigned)grid), kAttnThreads, Shape<ROWS>::smem, st, w) != 0)
     return 1;
   if (w.whole) return 0;                         // nothing to join
-  return launch_behind(kv4_join_kernel, dim3((unsigned)grid, Shape<NC>::rows), kJoinThreads, 0, st, a,
-                       (int)Shape<NC>::rows);
+  return launch_behind(kv4_join_kernel, dim3((unsigned)grid, ROWS), kJoinThreads, 0, st, a, ROWS);
 }
 
-template <int NC>
+template <int ROWS>
 int launch_rows(const Kv4AttnArgs &a, cudaStream_t st) {
   const bool mass = a.mass_out != nullptr;
-  if (a.cap > 0.0f) return mass ? launch_attn<NC, true, true>(a, st) : launch_attn<NC, true, false>(a, st);
-  return mass ? launch_attn<NC, false, true>(a, st) : launch_attn<NC, false, false>(a, st);
+  if (a.cap > 0.0f) return mass ? launch_attn<ROWS, true, true>(a, st) : launch_attn<ROWS, true, false>(a, st);
+  return mass ? launch_attn<ROWS, false, true>(a, st) : launch_attn<ROWS, false, false>(a, st);
 }
 
-int row_groups(int R) { return R <= 4 ? 1 : 2; }
+int rows_a_block(int R) { return R <= 4 ? 4 : R <= 8 ? 8 : 16; }
 
 }  // namespace
 
-int kv4_row_tiles(int R) { return (R + 4 * row_groups(R) - 1) / (4 * row_groups(R)); }
-size_t kv4_part_bytes(int R) { return (size_t)2 * kKv4MaxBlocks * 4 * row_groups(R) * kTile * sizeof(float); }
-size_t kv4_stat_bytes(int R) { return (size_t)2 * kKv4MaxBlocks * 4 * row_groups(R) * sizeof(float4); }
+int kv4_row_tiles(int R) { return (R + rows_a_block(R) - 1) / rows_a_block(R); }
+size_t kv4_part_bytes(int R) { return (size_t)2 * kKv4MaxBlocks * rows_a_block(R) * kTile * sizeof(float); }
+size_t kv4_stat_bytes(int R) { return (size_t)2 * kKv4MaxBlocks * rows_a_block(R) * sizeof(float4); }
 size_t kv4_join_bytes() { return (size_t)kKv4MaxBlocks * sizeof(int4); }
 
 int launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t st) {
-  const int rc = row_groups(a.R) == 1 ? launch_rows<1>(a, st) : launch_rows<2>(a, st);
+  const int rows = rows_a_block(a.R);
+  const int rc = rows == 4 ? launch_rows<4>(a, st) : rows == 8 ? launch_rows<8>(a, st) : launch_rows<16>(a, st);
   if (rc != 0) return rc;
   if (a.mass_out != nullptr && a.c.capacity() > 0)
     return launch_behind(kv4_mass_kernel,
