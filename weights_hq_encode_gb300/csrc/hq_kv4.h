@@ -59,10 +59,11 @@ struct Kv4AttnArgs {
   const float *mass_in;     // [n_seqs][n_kv][capacity] or nullptr
   float *mass_out;          // the same, or nullptr: no mass
   int whole;                // set by the launch: a block a (sequence, head, row tile), no joins
+  int by_pair;              // likewise: joins are kept a (sequence, head, row tile), not a block
   int row_tiles;            // tiles of rows a KV head has
   float *part;              // workspace: sums that several blocks share
   float *stat;              // workspace: their references and sums of weights
-  int *joins;               // workspace: what each block leaves to be joined
+  int *joins;               // workspace: what is left to be joined
   float *z;                 // workspace [n_seqs][n_kv][R][capacity] when mass is wanted
   float *row_lse;           // workspace [n_seqs][n_kv][R]: log2 of the row's sum, with its maximum
   uint32_t *status;

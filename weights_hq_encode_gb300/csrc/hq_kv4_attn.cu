@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
   uint32_t factor;                               // 2^15 twice, in a register that is not filled again
   asm volatile("mov.b32 %0, 0x78007800;" : "=r"(factor));
   const float k_own = low ? 0x1p-6f : 0x1p5f, k_other = low ? 0x1p5f : 0x1p-6f;
-  int join_b = 0, join_count = 0, join_pair = 0;
+  int4 *const joins = reinterpret_cast<int4 *>(a.joins);
+  if (tid == 0 && !a.whole && !a.by_pair) joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   while (walk.next(a, &seg)) {
     const int h = seg.pair / a.row_tiles, row0 = (seg.pair % a.row_tiles) * kRows;
     bool bad_len;
@@ -805,11 +806,9 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
     }
     __syncthreads();
     const bool whole = seg.u_lo == 0 && seg.u_hi == seg.nu;
-    if (!whole && seg.u_lo == 0) {               // begun here, ended by later blocks
-      join_b = seg.b;
-      join_pair = seg.pair;
-      join_count = (int)(kv4_divide(seg.at_end - 1, piece.size) - blockIdx.x);
-    }
+    if (tid == 0 && seg.u_lo == 0 && !a.whole && (a.by_pair || !whole))      // begun here; ended by later blocks
+      joins[a.by_pair ? seg.b * a.c.n_kv * a.row_tiles + seg.pair : blockIdx.x] =
+          make_int4((int)(kv4_divide(seg.at_end - 1, piece.size) - blockIdx.x), blockIdx.x, seg.b, seg.pair);
     if (tid < 8 * kRows) {
       float M = kNoMax, MW = kNoMax, L = 0.0f;
 #pragma unroll
@@ -848,14 +847,15 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
     }
     __syncthreads();                             // the ring and the statistics are free
   }
-  if (tid == 0 && !a.whole)
-    reinterpret_cast<int4 *>(a.joins)[blockIdx.x] = make_int4(join_count, join_b, join_pair, 0);
   // rows of sequences without tokens, and lengths out of range
   for (int sb = blockIdx.x; sb < a.c.n_seqs; sb += gridDim.x) {
     bool bad_len;
     const int len = kv4_length(a.c, a.lengths, sb, &bad_len);
     if (bad_len && tid == 0) atomicOr(a.status, (uint32_t)HQ_ERR_PAGE);
     if (len > 0) continue;
+    if (a.by_pair && !a.whole)
+      for (int i = tid; i < a.c.n_kv * a.row_tiles; i += kAttnThreads)
+        joins[sb * a.c.n_kv * a.row_tiles + i] = make_int4(0, 0, 0, 0);
     const int64_t first = (int64_t)sb * a.q_len * a.Hq;
     for (int64_t i = tid >> 3; i < (int64_t)a.q_len * a.Hq; i += kAttnThreads / 8) {
       float zero[16];
@@ -868,65 +868,95 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
   }
 }
 
-// The sums of a (sequence, head, row tile) that several blocks share: block
-// (i, row) joins that row of what block i of the attention kernel began.  Each
-// of the warps adds every eighth block's sums, in order, a lane four
-// dimensions; the eight are added in order.
-constexpr int kJoinThreads = 256;
-__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, int rows) {
-  __shared__ __align__(16) float s_tr[4 * kTrTile];
-  __shared__ __align__(16) float s_x[kJoinThreads / 32][kTile];
-  __shared__ float s_l[kJoinThreads / 32];
+// The sums of a (sequence, head, row tile) that several blocks share, joined
+// by WARPS warps a row: each adds every WARPS-th block's sums, in order, a lane four
+// dimensions, and the warps' are added in order.  A chain of latencies: what to
+// join, the sums, asked for before the largest references are known, the
+// transform.  8 warps a row where the batch gives a row more than 8 blocks, else one
+// (24 ragged sessions of 4093 tokens, 16 rows a head, 2 or 3 blocks a row: 42 us
+// in all; 49 with 8 warps for every block of the attention and row).
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinAhead = 4;
+template <int WARPS>
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, int rows, int items) {
+  __shared__ __align__(16) float s_tr[kJoinWarps / WARPS][4 * kTrTile];
+  __shared__ __align__(16) float s_x[kJoinWarps][kTile];
+  __shared__ float s_l[kJoinWarps];
   follow_launch();                               // launched while that kernel runs
-  const int4 job = reinterpret_cast<const int4 *>(a.joins)[blockIdx.x];
-  const int rr = blockIdx.y, h = job.z / a.row_tiles, row = (job.z % a.row_tiles) * rows + rr;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WARPS;
+  const int item = blockIdx.x * (kJoinWarps / WARPS) + warp / WARPS;
+  if (item >= items) return;                     // whole blocks with 8 warps, else by themselves
+  const int4 job = reinterpret_cast<const int4 *>(a.joins)[item / rows];
+  const int rr = item % rows, h = job.w / a.row_tiles, row = (job.w % a.row_tiles) * rows + rr;
   if (job.x == 0 || row >= a.R) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float4 *stat = reinterpret_cast<const float4 *>(a.stat);
-  const auto slot_of = [&](int i) { return 2 * ((int64_t)blockIdx.x + i) + (i == 0 ? 1 : 0); };
+  const auto slot_of = [&](int i) { return (2 * ((int64_t)job.y + i) + (i == 0 ? 1 : 0)) * rows + rr; };
+  float4 s[kJoinAhead], v[kJoinAhead];
+#pragma unroll
+  for (int k = 0; k < kJoinAhead; ++k) {
+    const int i = part + WARPS * k;
+    if (i <= job.x) {
+      s[k] = stat[slot_of(i)];
+      v[k] = reinterpret_cast<const float4 *>(a.part + slot_of(i) * kTile)[lane];
+    }
+  }
   float M = kNoMax, MW = kNoMax, L = 0.0f;
   for (int i = lane; i <= job.x; i += 32) {
-    const float4 s = stat[slot_of(i) * rows + rr];
-    M = fmaxf(M, s.x);
-    MW = fmaxf(MW, s.z);
+    const float4 st = stat[slot_of(i)];
+    M = fmaxf(M, st.x);
+    MW = fmaxf(MW, st.z);
   }
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) {
     M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
     MW = fmaxf(MW, __shfl_xor_sync(0xffffffffu, MW, d));
   }
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = warp; i <= job.x; i += kJoinThreads / 32) {
-    const float4 s = stat[slot_of(i) * rows + rr];
-    const float4 v = reinterpret_cast<const float4 *>(a.part + (slot_of(i) * rows + rr) * kTile)[lane];
-    L = __fmaf_rn(s.y, ex2(__fsub_rn(s.x, M)), L);
-    const float f = ex2(__fsub_rn(s.z, MW));
-    x.x = __fmaf_rn(v.x, f, x.x);
-    x.y = __fmaf_rn(v.y, f, x.y);
-    x.z = __fmaf_rn(v.z, f, x.z);
-    x.w = __fmaf_rn(v.w, f, x.w);
-  }
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const auto add = [&](const float4 &st, const float4 &sums) {
+    L = __fmaf_rn(st.y, ex2(__fsub_rn(st.x, M)), L);
+    const float f = ex2(__fsub_rn(st.z, MW));
+    x.x = __fmaf_rn(sums.x, f, x.x);
+    x.y = __fmaf_rn(sums.y, f, x.y);
+    x.z = __fmaf_rn(sums.z, f, x.z);
+    x.w = __fmaf_rn(sums.w, f, x.w);
+  };
+#pragma unroll
+  for (int k = 0; k < kJoinAhead; ++k)
+    if (part + WARPS * k <= job.x) add(s[k], v[k]);
+#pragma unroll 4
+  for (int i = part + WARPS * kJoinAhead; i <= job.x; i += WARPS)
+    add(stat[slot_of(i)], reinterpret_cast<const float4 *>(a.part + slot_of(i) * kTile)[lane]);
   reinterpret_cast<float4 *>(s_x[warp])[lane] = x;
-  if (lane == 0) s_l[warp] = L;
-  __syncthreads();
-  if (warp != 0) return;
+  if (WARPS == 1) {
+    __syncwarp();
+  } else {
+    if (lane == 0) s_l[warp] = L;
+    __syncthreads();
+    float y = 0.0f;
+    if (threadIdx.x < kTile) {
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) y = __fadd_rn(y, s_x[w][threadIdx.x]);
+    }
+    __syncthreads();
+    if (threadIdx.x < kTile) s_x[0][threadIdx.x] = y;
+    __syncthreads();
+    if (warp != 0) return;
+    L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) L = __fadd_rn(L, s_l[w]);
+  }
   const int r = lane & 7;
   float y[16];
-  L = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) y[i] = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) {
-    L = __fadd_rn(L, s_l[w]);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = __fadd_rn(y[i], s_x[w][16 * r + i]);
+  for (int c = 0; c < 4; ++c) {
+    const float4 q = reinterpret_cast<const float4 *>(s_x[warp] + 16 * r)[c];
+    y[4 * c] = q.x; y[4 * c + 1] = q.y; y[4 * c + 2] = q.z; y[4 * c + 3] = q.w;
   }
   normalize(y, M, MW, L);
   const int j = row / a.G, hq = h * a.G + row % a.G;
   const uint32_t sign_bits = a.c.signs[r >> 1] >> (16 * (r & 1));
-  finish_row(a, y, s_tr + (lane >> 3) * kTrTile, r, sign_bits, lane < 8, ((int64_t)job.y * a.q_len + j) * a.Hq + hq);
-  if (lane == 0) finish_stats(a, job.y, h, row, M, L);
+  finish_row(a, y, s_tr[warp / WARPS] + (lane >> 3) * kTrTile, r, sign_bits, lane < 8,
+             ((int64_t)job.z * a.q_len + j) * a.Hq + hq);
+  if (lane == 0) finish_stats(a, job.z, h, row, M, L);
 }
 
 // mass_out = mass_in + sum over the head's rows of 2^(z - log2 of the row's
@@ -990,10 +1020,15 @@ int launch_attn(const Kv4AttnArgs &a, cudaStream_t st) {
   Kv4AttnArgs w = a;
   w.whole = pairs <= grid && a.c.capacity() / kUnit + kSegmentCost <= kWholeSpan;
   if (w.whole) grid = (int)pairs;
+  w.by_pair = pairs <= grid;
   if (launch_behind(kv4_attn_kernel<ROWS, CAP, MASS>, dim3((unsigned)grid), kAttnThreads, Shape<ROWS>::smem, st, w) != 0)
     return 1;
   if (w.whole) return 0;                         // nothing to join
-  return launch_behind(kv4_join_kernel, dim3((unsigned)grid, ROWS), kJoinThreads, 0, st, a, ROWS);
+  const int items = (w.by_pair ? (int)pairs : grid) * ROWS;
+  if (8 * pairs < grid)
+    return launch_behind(kv4_join_kernel<8>, dim3((unsigned)items), kJoinThreads, 0, st, a, ROWS, items);
+  return launch_behind(kv4_join_kernel<1>, dim3((unsigned)((items + kJoinWarps - 1) / kJoinWarps)), kJoinThreads, 0,
+                       st, a, ROWS, items);
 }
 
 template <int ROWS>
