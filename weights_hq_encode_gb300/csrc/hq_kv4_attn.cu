@@ -872,9 +872,10 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
 // by WARPS warps a row: each adds every WARPS-th block's sums, in order, a lane four
 // dimensions, and the warps' are added in order.  A chain of latencies: what to
 // join, the sums, asked for before the largest references are known, the
-// transform.  8 warps a row where the batch gives a row more than 8 blocks, else one
-// (24 ragged sessions of 4093 tokens, 16 rows a head, 2 or 3 blocks a row: 42 us
-// in all; 49 with 8 warps for every block of the attention and row).
+// transform.  8 warps a row while all rows' blocks fit at once, else one: 128 x 4
+// rows with 8 warps 42.9 us in all (attention of 16 ragged sessions of 8192
+// tokens, with mass), with one 44.9; 128 x 16 rows (16 x 4096 tokens) with one
+// 40.3, with 8 44.9.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinAhead = 4;
 template <int WARPS>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, int rows, int items) {
@@ -1025,7 +1026,7 @@ int launch_attn(const Kv4AttnArgs &a, cudaStream_t st) {
     return 1;
   if (w.whole) return 0;                         // nothing to join
   const int items = (w.by_pair ? (int)pairs : grid) * ROWS;
-  if (8 * pairs < grid)
+  if (items <= 4 * 152)
     return launch_behind(kv4_join_kernel<8>, dim3((unsigned)items), kJoinThreads, 0, st, a, ROWS, items);
   return launch_behind(kv4_join_kernel<1>, dim3((unsigned)((items + kJoinWarps - 1) / kJoinWarps)), kJoinThreads, 0,
                        st, a, ROWS, items);
