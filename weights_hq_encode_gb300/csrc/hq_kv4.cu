@@ -124,23 +124,13 @@ __global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(Kv4RowArgs 
     rows[which].get(mw, x);
     if (which == 1) __syncwarp();                // the table is free
     fwht128_t8_columns(x, s_tr + tl * kTrTile, r, y);
-    // the largest magnitude; the maximum passes over a NaN, so a sum of 0 x every value looks for
-    // NaNs and infinities
-    float top = 0.0f;
-    uint64_t odd_one = 0;
+    float top = 0.0f;                            // the largest magnitude, NaN if there is one
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-      top = fmaxf(fmaxf(top, fabsf(y[j])), fabsf(y[j + 1]));
-      odd_one = fma2(pk2(y[j], y[j + 1]), 0ull, odd_one);
-    }
-    float n0, n1;
-    upk2(odd_one, n0, n1);
-    top = __fadd_rn(top, __fadd_rn(n0, n1));     // NaN if there was one
+    for (int j = 0; j < 16; j += 2)
+      asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(y[j]), "f"(y[j + 1]));
 #pragma unroll
-    for (int d = 1; d < 8; d <<= 1) {
-      const float o = __shfl_xor_sync(0xffffffffu, top, d);
-      top = top > o || top != top ? top : o;     // NaN wins
-    }
+    for (int d = 1; d < 8; d <<= 1)
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(__shfl_xor_sync(0xffffffffu, top, d)));
     const bool finite = top < INFINITY;
     float sf = finite ? __bfloat162float(__float2bfloat16_rn(__fmul_rn(top, kAbsToScale))) : 0.0f;
     if (sf < 0x1p-126f) sf = 0.0f;               // no subnormal scales: the row is zero
