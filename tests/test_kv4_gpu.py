@@ -26,7 +26,14 @@ is a sixteenth of the difference of the two.  A step adds 16 products and the
 sum so far, 34 u of the largest; over the at most T / 16 steps of a warp that
 is 34 u sum_t p_t s_t x 7.5 for every dimension if each step's largest addend is
 a product of its own tokens, and 34 u T / 16 of the row's sum if it is the sum so
-far, at most A = sum_t p_t |y_t| (V in the transformed domain).  With 60 u for the
+far, at most A = sum_t p_t |y_t| (V in the transformed domain).  With more than 4
+rows a head the low parts are steps of their own into the same sum, with products
+2^-11 of the others: a warp has n <= 2 ceil(T / 128) units, so 2 n - 1 <= T / 32 + 3 steps
+that meet a sum, no more than the T / 16 counted from T = 96 on.  Below, 3 steps
+are 102 u: with the 31 u that the 100 below leave, at most 35 u |A| more than
+counted (T = 17; up to 16 tokens it is one step), and as |A| <= 7.5 sqrt(128)
+sum p s, 263 u sqrt(128) sum p s of the 345 u that the 600 below leave beside the 255
+of the products.  With 60 u for the
 joining of the parts and the transform back (9 u), in the norm of an output row:
   |d out| <= (2 |dz| + (34 T / 16 + 100) u) |A| + 600 u sqrt(128) sum_t p_t s_t
 plus half a step of the output's type, element by element.

@@ -34,7 +34,10 @@ template <int ROWS>
 struct Shape {
   static constexpr int q_bytes = 2 * ROWS * kTile * 2;      // query fragments, high and low parts
   static constexpr int smem = kRingBytes + q_bytes + ROWS * kTrTile * 4;
-  static constexpr int blocks = ROWS == 4 ? 3 : 2;          // resident blocks a multiprocessor
+  // Resident blocks a multiprocessor: 12 warps of 168 registers, or 8 of up to 255.  More warps of
+  // fewer registers keep parts of a tile in local memory: 16 of 128 took 118 us instead of 110 for 16 x
+  // 32768 tokens of 8 heads and 4 rows; 12 of 168 with 8 rows 46.6 instead of 45.5 for 16 x 8192.
+  static constexpr int blocks = ROWS == 4 ? 3 : 2;
   static_assert(kWarps * ROWS * kTile * 4 <= kRingBytes, "the warps' sums fit the ring");
 };
 
@@ -158,7 +161,8 @@ __device__ __forceinline__ void split2(float lo, float hi, uint32_t &h, uint32_t
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(rest) : "f"(r1), "f"(r0));
 }
 
-// The same with the rests as they are: they miss a value by 2^-22 of it, and by 2^-25.
+// The same with the rests as they are: the parts miss a value by 2^-22 of it and 2^-25, 2^-32
+// of the largest weight.
 __device__ __forceinline__ void split2_plain(float lo, float hi, uint32_t &h, uint32_t &rest) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
   const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
@@ -368,22 +372,26 @@ __device__ Piece find_piece(const Kv4AttnArgs &a) {
 // here, the others leave their sums for kv4_join_kernel.
 //
 // The products run on mma.sync m16n8k16, tokens (scores) and dimensions
-// (values) as the 16 rows and query rows as the 8 columns: columns 0 .. 3 the
-// high parts of 4 rows, columns 4 .. 7 their low parts, so that the fp32-level
-// split of 4 rows fills one instruction.  The codes are unpacked in registers,
+// (values) as the 16 rows and query rows as the 8 columns: with up to 4 rows
+// columns 0 .. 3 are their high parts, columns 4 .. 7 their low parts, so that the
+// fp32-level split of 4 rows fills one instruction; with more, 8 rows' high parts
+// and 8 rows' low parts are products of their own, whose values share one sum (half
+// the registers of sums of their own).  16 rows a block unpack the codes once (24
+// ragged sessions of 4093 tokens, 16 rows a head, capped: 49 us; 56 with 8 a
+// block and parts in columns).  The codes are unpacked in registers,
 // straight into operand fragments; that is why these are not tcgen05
 // products, whose operands would first have to be stored to shared memory as
 // fp16, four times the bytes that were read: 1 KB of 16-bit K and V a token
 // against the 128 bytes a cycle that shared memory takes, 16 cycles for reading and
 // writing a token beside the 5 to 6 in which memory delivers it.
 //
-// 16 sequences x 32768 tokens x 8 heads, 4 query rows a head: 110 us, 5.0 TB/s,
-// 74% of the copy rate; the copies alone take 98 us, the rest is what instruction
+// 16 sequences x 32768 tokens x 8 heads, 4 query rows a head: 108 us, 5.1 TB/s,
+// 75% of the copy rate; the copies alone take 98 us, the rest is what instruction
 // issue (about 293 a warp for 16 tokens, 54% of the cycles) does not hide.  One
 // sequence of 131072 tokens: 37 us, of which 15 do not depend on its length (the
-// first tile's way 5, the end and the join 6).  With 16 query rows a head the
-// codes are unpacked for every 8 of them: 24 x 2200 tokens 56 us, bound by
-// the latency of 8 warps a multiprocessor (issue 49%, tensor cores 35%).
+// first tile's way 4, the end and the join 6).  With 16 query rows a head, 24
+// ragged sessions of 4093 tokens take 42 us (join included), bound by the latency of
+// 8 warps a multiprocessor (issue 42%, tensor cores 51%).
 template <int kRows, bool CAP, bool MASS>
 __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_kernel(Kv4AttnArgs a) {
   constexpr bool kWide = kRows > 4;              // high and low parts in products of their own
