@@ -3,6 +3,8 @@
 // head is 132 bytes in the cache and 2 x 128 values outside it.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "hq_device.cuh"
 #include "hq_kv4.h"
 #include "hq_kv4_io.cuh"
@@ -330,17 +332,19 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *s_w, int fl
 // keys are read once (the first `cached` into shared memory, four at a time from
 // there on) for their least and largest; the threshold is found digit by digit
 // of (key - least), 11 bits at a time from the top of that range, by
-// histograms in shared memory; a last pass in order compacts what lies above it
+// histograms in shared memory, until all that share the digits are kept (one
+// pass for a few hundred masses, two for 30000, where three are the most); a last
+// pass in order compacts what lies above it
 // and the first of what equals it.  Digits of the range and not of the key:
 // masses of a few binary orders spread over all 2048 bins, where the key's own
 // top bits are a handful of values and their atomics one behind another.
 // cached: a multiple of 4.  16 x 32768 tokens of 8 heads: 128 blocks, one a
-// multiprocessor, 21 us for 15 MB of masses, bound by the passes over a block's keys.
+// multiprocessor, 19 us for 15 MB of masses (their loads 5, 7 in passes of 11 bits, 6 to compact).
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a, int cached) {
   extern __shared__ __align__(16) uint32_t s_keys[];
   __shared__ uint32_t s_hist[kSelBins];
   __shared__ uint32_t s_w[64];
-  __shared__ uint32_t s_digit, s_above, s_least, s_most;
+  __shared__ uint32_t s_digit, s_above, s_there, s_least, s_most;
   follow_launch();
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   bool bad;
@@ -366,13 +370,19 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a,
   int from = 0;                                  // where the loads one by one begin
   if ((reinterpret_cast<uintptr_t>(mass) & 15) == 0) {
     from = near & ~3;
-#pragma unroll 8
-    for (int i = tid; 4 * i < from; i += kSelThreads) {
-      const float4 m = reinterpret_cast<const float4 *>(mass)[i];
-      const uint4 k = make_uint4(mass_key(m.x), mass_key(m.y), mass_key(m.z), mass_key(m.w));
-      s_keys4[i] = k;
-      least = min(least, min(min(k.x, k.y), min(k.z, k.w)));
-      most = max(most, max(max(k.x, k.y), max(k.z, k.w)));
+    for (int i0 = tid; 4 * i0 < from; i0 += 8 * kSelThreads) {   // 8 loads, then what they bring
+      float4 m[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (4 * (i0 + u * kSelThreads) < from) m[u] = reinterpret_cast<const float4 *>(mass)[i0 + u * kSelThreads];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (4 * (i0 + u * kSelThreads) >= from) break;
+        const uint4 k = make_uint4(mass_key(m[u].x), mass_key(m[u].y), mass_key(m[u].z), mass_key(m[u].w));
+        s_keys4[i0 + u * kSelThreads] = k;
+        least = min(least, min(min(k.x, k.y), min(k.z, k.w)));
+        most = max(most, max(max(k.x, k.y), max(k.z, k.w)));
+      }
     }
   }
 #pragma unroll 8
@@ -425,29 +435,38 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a,
       const bool first = want <= begin + c0;
       s_digit = first ? d0 : d0 - 1;
       s_above = first ? begin : begin + c0;
+      s_there = first ? c0 : c1;
     }
     __syncthreads();
     prefix |= s_digit << shift;
     want -= s_above;
+    if (want == s_there && prefix + least != 0) { // all of them are kept: what is above the key before theirs
+      --prefix;
+      want = 0;
+      break;
+    }
   }
   __syncthreads();                                // the fillers, when no digit was to be found
-  // 8 keys a thread in a step: those above the threshold so far in the low half of a word, its
-  // equals in the high half
+  // The keys in order, 8 a thread in a step, or one where that is a step: those above the threshold
+  // so far in the low half of a word, its equals in the high half.
   const uint32_t level = prefix + least;
   uint32_t gt_before = 0, eq_before = 0;
-  for (int base = 0; base < old; base += 8 * kSelThreads) {
-    const int at = base + 8 * tid;
-    uint32_t key[8], c = 0;
-    if (at + 8 <= cached) {                       // what lies behind `near` is not looked at
-      const uint4 x = s_keys4[at / 4], y = s_keys4[at / 4 + 1];
-      key[0] = x.x; key[1] = x.y; key[2] = x.z; key[3] = x.w;
-      key[4] = y.x; key[5] = y.y; key[6] = y.z; key[7] = y.w;
+  const auto compact = [&](auto keys, int base) {
+    constexpr int kKeys = decltype(keys)::value;
+    const int at = base + kKeys * tid;
+    uint32_t key[kKeys < 4 ? 4 : kKeys], c = 0;
+    if (kKeys == 8 && at + 8 <= cached) {         // what lies behind `near` is not looked at
+#pragma unroll
+      for (int j = 0; j < kKeys; j += 4) {
+        const uint4 x = s_keys4[(at + j) / 4];
+        key[j] = x.x; key[j + 1] = x.y; key[j + 2] = x.z; key[j + 3] = x.w;
+      }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) key[j] = at + j < old ? mass_key(mass[at + j]) : 0u;
+      for (int j = 0; j < kKeys; ++j) key[j] = at + j < near ? s_keys[at + j] : at + j < old ? mass_key(mass[at + j]) : 0u;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < kKeys; ++j)
       if (at + j < old) c += key[j] > level ? 1u : key[j] == level ? 0x10000u : 0u;
     uint32_t total;
     const uint32_t incl = block_scan(c, s_w, flip, &total), excl = incl - c;
@@ -455,7 +474,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a,
     if (c != 0) {
       uint32_t gt = gt_before + (excl & 0xFFFFu), eq = eq_before + (excl >> 16);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < kKeys; ++j) {
         if (at + j >= old) break;
         if (key[j] > level) {
           kept[gt + min(eq, want)] = at + j;
@@ -468,7 +487,10 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a,
     }
     gt_before += total & 0xFFFFu;
     eq_before += total >> 16;
-  }
+  };
+  if (old <= kSelThreads) compact(std::integral_constant<int, 1>{}, 0);
+  else
+    for (int base = 0; base < old; base += 8 * kSelThreads) compact(std::integral_constant<int, 8>{}, base);
 }
 
 // Rows and masses of the kept positions, up to 32 a warp: a lane looks one up,
