@@ -314,6 +314,20 @@ def test_attention_many_ragged_sequences(hq):
     check(C, q, 0.1, 0.0, attend(hq, C, q, 0.1, 0.0, torch.float32), plain=True)
 
 
+@pytest.mark.parametrize("case", range(4))
+def test_attention_rows_that_many_blocks_share(hq, case):
+    """Joins by one and by eight warps, of more blocks than are read ahead, listed by (sequence,
+    head) and by block, beside sequences without tokens."""
+    rng = np.random.default_rng(40 + case)
+    lens, nh, G = (([2900] * 6 + [0] + [2900] * 6, 3, 16), ([22000, 0], 1, 4), ([0, 7000], 1, 16),
+                   ([int(x) for x in rng.integers(0, 200, 160)] + [4000], 2, 8))[case]
+    C = Cache(hq, rng, lens, nh, 16 * (1 + case))
+    q = queries(rng, len(lens), 1, nh * G, "bf16")
+    got = attend(hq, C, q, 0.1, 0.0, torch.float32)
+    check(C, q, 0.1, 0.0, got, plain=True)
+    assert torch.equal(got[0], attend(hq, C, q, 0.1, 0.0, torch.float32)[0])
+
+
 def test_attention_sharp_flat_and_uneven(hq):
     """Scores far apart (zeta about 10^3), all equal, negative scale, and V scales of very
     different size, the largest on a token of no weight."""
