@@ -544,6 +544,24 @@ def test_evict_against_reference(hq, lens, nh, page, budget, recent, new_page):
                     assert s0[h, t % page] == s1[h, i % P]
 
 
+@pytest.mark.parametrize("n,budget,recent", [(5, 3, 0), (1030, 700, 6), (1031, 700, 6), (8300, 100, 99),
+                                             (50000, 3, 1), (50000, 49990, 7)])
+def test_evict_positions_of_distinct_and_equal_masses(hq, n, budget, recent):
+    """Sequences on both sides of every limit of the selection (1024 and 8192 tokens that compete,
+    49152 keys in shared memory), masses all distinct, in steps and negative, on 16-byte boundaries and off."""
+    rng = np.random.default_rng(n)
+    C = Cache(hq, rng, [n], 1, 16, empty=True)
+    draws = rng.random(C.width * 16)
+    for mass in (draws, np.floor(draws * 50) / 50, -draws, np.exp(-40 * draws)):
+        for off in (0, 1):
+            buf = torch.zeros(mass.size + off, device="cuda")
+            d = buf[off:].view(1, 1, -1)
+            d.copy_(torch.from_numpy(mass))
+            kept = evict(hq, C, d, budget, recent)[3]
+            want = R.keep(mass.astype(np.float32), n, budget, recent)
+            assert np.array_equal(kept[0, 0].cpu().numpy(), want)
+
+
 def test_evict_equal_masses_and_bad_pages(hq):
     """All masses equal: the lowest positions win; rows whose page is outside the pool are left
     out and reported."""
