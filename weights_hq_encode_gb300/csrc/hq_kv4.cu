@@ -90,7 +90,7 @@ __device__ __forceinline__ uint2 words_of_columns(uint32_t even, uint32_t odd, i
 // (lane r: dimensions 16 r .. 16 r + 15), so that the transform is the codec's,
 // its stages in the codec's order.  It is not taken back to the lanes'
 // dimensions in fp32: the codes are, 8 bytes a lane instead of 64.  Bound by
-// instruction issue (71% of the cycles): 289000 entries in bf16 take 56 us where
+// instruction issue (72% of the cycles): 289000 entries in bf16 take 56 us where
 // their 186 MB want 27.
 template <int KIND>
 __global__ void __launch_bounds__(kRowsThreads, 5) kv4_append_kernel(Kv4RowArgs a) {
