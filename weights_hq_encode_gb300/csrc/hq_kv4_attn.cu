@@ -880,12 +880,14 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
 // by WARPS warps a row: each adds every WARPS-th block's sums, in order, a lane four
 // dimensions, and the warps' are added in order.  A chain of latencies: what to
 // join, the sums, asked for before the largest references are known, the
-// transform.  8 warps a row while all rows' blocks fit at once, else one: 128 x 4
-// rows with 8 warps 42.9 us in all (attention of 16 ragged sessions of 8192
-// tokens, with mass), with one 44.9; 128 x 16 rows (16 x 4096 tokens) with one
-// 40.3, with 8 44.9.
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinAhead = 4;
-template <int WARPS>
+// transform.  8 warps a row, and more of its sums asked for at once, while all
+// rows' blocks fit at once, else one warp: 8 x 4 rows (one sequence of 131072 tokens,
+// 57 blocks a row) with 8 sums ahead 34.5 us in all, with 4 36.9, with 32 warps
+// 35.5; 128 x 4 rows with 4 ahead 42.7 (attention of 16 ragged sessions of 8192 tokens,
+// with mass), with 8 (registers for half the blocks) 44.7, with one warp 44.9;
+// 128 x 16 rows (16 x 4096 tokens) with one 40.3, with 8 44.9.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+template <int WARPS, int AHEAD>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, int rows, int items) {
   __shared__ __align__(16) float s_tr[kJoinWarps / WARPS][4 * kTrTile];
   __shared__ __align__(16) float s_x[kJoinWarps][kTile];
@@ -893,15 +895,15 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, i
   follow_launch();                               // launched while that kernel runs
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WARPS;
   const int item = blockIdx.x * (kJoinWarps / WARPS) + warp / WARPS;
-  if (item >= items) return;                     // whole blocks with 8 warps, else by themselves
+  if (item >= items) return;                     // whole blocks, or warps by themselves
   const int4 job = reinterpret_cast<const int4 *>(a.joins)[item / rows];
   const int rr = item % rows, h = job.w / a.row_tiles, row = (job.w % a.row_tiles) * rows + rr;
   if (job.x == 0 || row >= a.R) return;
   const float4 *stat = reinterpret_cast<const float4 *>(a.stat);
   const auto slot_of = [&](int i) { return (2 * ((int64_t)job.y + i) + (i == 0 ? 1 : 0)) * rows + rr; };
-  float4 s[kJoinAhead], v[kJoinAhead];
+  float4 s[AHEAD], v[AHEAD];
 #pragma unroll
-  for (int k = 0; k < kJoinAhead; ++k) {
+  for (int k = 0; k < AHEAD; ++k) {
     const int i = part + WARPS * k;
     if (i <= job.x) {
       s[k] = stat[slot_of(i)];
@@ -929,10 +931,10 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, i
     x.w = __fmaf_rn(sums.w, f, x.w);
   };
 #pragma unroll
-  for (int k = 0; k < kJoinAhead; ++k)
+  for (int k = 0; k < AHEAD; ++k)
     if (part + WARPS * k <= job.x) add(s[k], v[k]);
 #pragma unroll 4
-  for (int i = part + WARPS * kJoinAhead; i <= job.x; i += WARPS)
+  for (int i = part + WARPS * AHEAD; i <= job.x; i += WARPS)
     add(stat[slot_of(i)], reinterpret_cast<const float4 *>(a.part + slot_of(i) * kTile)[lane]);
   reinterpret_cast<float4 *>(s_x[warp])[lane] = x;
   if (WARPS == 1) {
@@ -1034,10 +1036,12 @@ int launch_attn(const Kv4AttnArgs &a, cudaStream_t st) {
     return 1;
   if (w.whole) return 0;                         // nothing to join
   const int items = (w.by_pair ? (int)pairs : grid) * ROWS;
-  if (items <= 4 * 152)
-    return launch_behind(kv4_join_kernel<8>, dim3((unsigned)items), kJoinThreads, 0, st, a, ROWS, items);
-  return launch_behind(kv4_join_kernel<1>, dim3((unsigned)((items + kJoinWarps - 1) / kJoinWarps)), kJoinThreads, 0,
-                       st, a, ROWS, items);
+  const auto join = [&](auto kernel, int a_block) {
+    return launch_behind(kernel, dim3((unsigned)((items + a_block - 1) / a_block)), kJoinThreads, 0, st, a, ROWS, items);
+  };
+  if (items <= 2 * 152) return join(kv4_join_kernel<8, 8>, 1);
+  if (items <= 4 * 152) return join(kv4_join_kernel<8, 4>, 1);
+  return join(kv4_join_kernel<1, 4>, kJoinWarps);
 }
 
 template <int ROWS>
