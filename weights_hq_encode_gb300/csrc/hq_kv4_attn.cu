@@ -388,8 +388,8 @@ __device__ Piece find_piece(const Kv4AttnArgs &a) {
 // 16 sequences x 32768 tokens x 8 heads, 4 query rows a head: 108 us, 5.1 TB/s,
 // 75% of the copy rate; the copies alone take 98 us, the rest is what instruction
 // issue (about 293 a warp for 16 tokens, 54% of the cycles) does not hide.  One
-// sequence of 131072 tokens: 37 us, of which 15 do not depend on its length (the
-// first tile's way 4, the end and the join 6).  With 16 query rows a head, 24
+// sequence of 131072 tokens: 34.5 us, of which 13 do not depend on its length (the
+// first tile's way 4, the end and the join 5).  With 16 query rows a head, 24
 // ragged sessions of 4093 tokens take 42 us (join included), bound by the latency of
 // 8 warps a multiprocessor (issue 42%, tensor cores 51%).
 template <int kRows, bool CAP, bool MASS>

@@ -307,7 +307,7 @@ def _launch(cache, call, stream, *args) -> int:
     """A library call with the cache's device current, on `stream` or that device's current one."""
     index = cache._index
     raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:       # the cache's tensors have initialised CUDA
         return call(*args, raw)
     with torch.cuda.device(index):
         return call(*args, raw)
