@@ -1,0 +1,154 @@
+"""The 4-bit window cache's attention at scores, queries, keys and caps of any size
+against its reference (oracle/kv4.py).
+
+A score beyond 2^24 (in log2 units) has no fraction left in fp32, and its own
+error is large.  What must not depend on it: an output is a weighted mean of
+rows of V.  Where all weights are known - one token, equal scores, equal rows of
+V, one score far above the others - only the value side's error is left, as
+tests/test_kv4_gpu.py derives it, in the norm of an output row (u = 2^-24, A =
+sum p |V'| in the transformed domain, s V's scales, T tokens):
+  |d out| <= (34 T / 16 + 100) u |A| + 600 u sqrt(128) sum p s.
+Equal scores have to come out equal for that.  They do for a query whose
+transform is +-1 in every coordinate: its fp16 parts are exact, so that every
+token's score is one and the same chain of roundings."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv4 as R
+from test_kv4_gpu import MASK, U, Cache, attend, hq, queries  # noqa: F401  (hq: a fixture)
+
+pytestmark = pytest.mark.gpu
+
+LN2 = float(np.log(2.0))
+SCORES = [1.7e7, -1.7e7, 5e7, 5e8, -5e8, 2.0 ** 60, 2.0 ** 100]     # in log2 units
+ROWS = [3, 4, 8, 16]                             # query rows a head: blocks of 4, 8 and 16
+
+
+def unit_query():
+    """A query of one coordinate whose transform is exactly +-1 in fp32."""
+    a = np.float32(np.sqrt(128.0))
+    near = np.array([a, np.nextafter(a, np.float32(0)), np.nextafter(a, np.float32(99))], np.float32)
+    exact = near[near * np.float32(0.08838834764831845) == 1]
+    assert len(exact)
+    q = np.zeros(128, np.float32)
+    q[5] = exact[0]
+    return q
+
+
+def fill(C, k, v):
+    """Sequence b of the cache gets K and V rows k[b], v[b] [tokens, 128] for every head."""
+    for b in range(len(C.lens)):
+        wide = [np.repeat(np.asarray(x[b], np.float32)[:, None], C.nh, 1) for x in (k, v)]
+        R.append(C.pages, C.table, *wide, [b] * C.lens[b], range(C.lens[b]), MASK)
+    C.upload()
+
+
+def raw_score(C, b, t, q):
+    """q . Khat of head 0 in 64 bits."""
+    return float(R.back(R.rotated(C.pages, C.table, b, t + 1, 0), MASK)[0, t] @ q.astype(np.float64))
+
+
+def value_bound(size, scales, T):
+    return (34 * T / 16 + 100) * U * np.linalg.norm(size, axis=-1) + 600 * U * np.sqrt(128.0) * scales
+
+
+def check_mean(C, got, weights):
+    """Every output row of sequence b is the mean of the head's rows of V by weights[b]."""
+    out = got[0].double().cpu().numpy()
+    G = out.shape[2] // C.nh
+    for b, n in enumerate(C.lens):
+        V = R.rotated(C.pages, C.table, b, n, 1)
+        s = np.concatenate([R.raw_rows(C.pages, p, 1)[1] for p in C.table[b, :-(-n // C.page)]], 1)[:, :n]
+        p = weights[b]
+        for h in range(C.nh):
+            want = R.back(p @ V[h], MASK)
+            tol = value_bound(p @ np.abs(V[h]), float(p @ s[h].astype(np.float64)), n)
+            err = np.linalg.norm(out[b, :, h * G:(h + 1) * G] - want, axis=-1)
+            assert (err <= tol).all(), (b, h, err.max() / tol)
+
+
+def check_lse(got, want, zeta):
+    """Scores' own errors, below 330 u of zeta = |scale| |q| max s (max(|c|, 7.5 sqrt(128)))."""
+    d = np.abs(got[1].double().cpu().numpy() - want)
+    assert (d <= 340 * U * (zeta + abs(want)) + 1e-5).all()
+
+
+@pytest.mark.parametrize("G", ROWS)
+@pytest.mark.parametrize("width", [1, 64])
+def test_one_token_is_its_value(hq, G, width):
+    """Blocks that end a row themselves, for a narrow table and for a wide one."""
+    rng = np.random.default_rng(100 + G)
+    sizes = [0.03, 0.5, 1.0, 2.0 ** 15]          # V's scales
+    C = Cache(hq, rng, [1] * 4, 2, 16, width=width, empty=True)
+    q = unit_query()
+    k = rng.standard_normal((1, 128))
+    k[0, 5] = 3.0                                # a score that is no small rest of its addends
+    fill(C, [k] * 4, [2.6 * a * rng.standard_normal((1, 128)) for a in sizes])
+    raw = raw_score(C, 0, 0, q)
+    dq = torch.from_numpy(np.broadcast_to(q, (4, 1, 2 * G, 128)).copy()).cuda()
+    for z in SCORES:
+        for cap in (0.0, 4e8):
+            got = attend(hq, C, dq, z * LN2 / raw, cap, torch.float32)
+            check_mean(C, got, [np.ones(1)] * 4)
+            want = z * LN2 if cap == 0 else cap * np.tanh(z * LN2 / cap)
+            check_lse(got, want, 100.0 * abs(z))
+    assert int(C.status) == 0
+
+
+@pytest.mark.parametrize("G", ROWS)
+@pytest.mark.parametrize("lens,width", [([600, 37], 38), ([700, 37], 44), ([700, 37], 200), ([3000, 1], 188)])
+def test_equal_scores_give_the_mean(hq, G, lens, width):
+    """All weights equal, beside V's scales that rise 2^20-fold along one sequence and fall along the
+    other: in one block, and in several whose sums are joined."""
+    rng = np.random.default_rng(200 + G)
+    C = Cache(hq, rng, lens, 2, 16, width=width, empty=True)
+    q = unit_query()
+    k = rng.standard_normal(128)
+    k[5] = 3.0
+    rise = [0.03 * 2.0 ** (20.0 * np.arange(n) / n) for n in lens]
+    rise[1] = rise[1][::-1]
+    fill(C, [np.broadcast_to(k, (n, 128)) for n in lens],
+         [rng.standard_normal((n, 128)) * r[:, None] for n, r in zip(lens, rise)])
+    raw = raw_score(C, 0, 0, q)
+    dq = torch.from_numpy(np.broadcast_to(q, (2, 1, 2 * G, 128)).copy()).cuda()
+    for z in [3.0] + SCORES:
+        got = attend(hq, C, dq, z * LN2 / raw, 0.0, torch.float32)
+        check_mean(C, got, [np.full(n, 1.0 / n) for n in lens])
+
+
+@pytest.mark.parametrize("G", ROWS)
+def test_equal_values_are_the_output(hq, G):
+    """Any weights at all: rows of V that are all the same are the output."""
+    rng = np.random.default_rng(300 + G)
+    lens = [700, 90]
+    C = Cache(hq, rng, lens, 2, 16, width=50, empty=True)
+    v = rng.standard_normal((2, 128))
+    fill(C, [rng.standard_normal((n, 128)) for n in lens],
+         [np.broadcast_to(v[b], (n, 128)) for b, n in enumerate(lens)])
+    q = queries(rng, 2, 1, 2 * G, "f32")
+    for scale in (1.0, 1e6, -1e7, 1e8):
+        got = attend(hq, C, q, scale, 0.0, torch.float32)
+        check_mean(C, got, [np.full(n, 1.0 / n) for n in lens])
+
+
+@pytest.mark.parametrize("G", ROWS)
+def test_one_score_far_above_the_others(hq, G):
+    """Keys of one direction whose sizes fall by 5% a step: the first by far takes all the weight,
+    wherever it lies, whatever the scales of V beside it."""
+    rng = np.random.default_rng(400 + G)
+    lens = [700, 333, 45]
+    C = Cache(hq, rng, lens, 2, 16, width=60, empty=True)
+    k = rng.standard_normal(128)
+    k[5] = 3.0
+    q = unit_query()
+    rank = [np.minimum(rng.permutation(n), 100) for n in lens]
+    v = [rng.standard_normal((n, 128)) * 2.0 ** rng.uniform(-15, 15, (n, 1)) for n in lens]
+    fill(C, [k[None] * 1.05 ** -r[:, None] for r in rank], v)
+    tops = [int(np.argmin(r)) for r in rank]
+    sign = np.sign(raw_score(C, 0, tops[0], q))
+    dq = torch.from_numpy(np.broadcast_to(q, (3, 1, 2 * G, 128)).copy()).cuda()
+    raw = abs(raw_score(C, 0, tops[0], q))
+    for z in (1.7e7, 5e7, 5e8, 2.0 ** 60, 2.0 ** 100):
+        got = attend(hq, C, dq, sign * z * LN2 / raw, 0.0, torch.float32)
+        check_mean(C, got, [np.eye(n)[t] for n, t in zip(lens, tops)])

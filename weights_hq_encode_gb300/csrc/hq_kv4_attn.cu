@@ -192,14 +192,16 @@ __device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, float x[16], fl
 }
 
 // A row's sums over some of its tokens: l = sum 2^(z - m), and acc (kept
-// beside it) = sum 2^(z - mw) s (c - 7.5).
+// beside it) = sum 2^(z - m - e) s (c - 7.5).  m and e are whole numbers and apart:
+// from 2^24 on m has no bits left for e, which undoes the scaling of the
+// weights and has to be exact whatever the scores.
 struct RowStat {
-  float m, l, mw, pad;
+  float m, l, e, pad;
 };
 
-// acc / l at its own references: x 2^mw / (l 2^m), zeros where there is no weight.
-__device__ __forceinline__ void normalize(float x[16], float m, float mw, float l) {
-  const float f = ex2(__fmul_rn(__fsub_rn(mw, m), 0.5f));   // in two steps, each within range
+// acc / l at its own references: x 2^e / l, zeros where there is no weight.
+__device__ __forceinline__ void normalize(float x[16], float e, float l) {
+  const float f = ex2(__fmul_rn(e, 0.5f));       // in two steps, each within range
   const float g = l == 0.0f ? 0.0f : __fmul_rn(__fdiv_rn(1.0f, l), f);
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], g), f);
@@ -690,17 +692,42 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
           ft = fmaxf(ft, f[g][e]);
         }
       if (__any_sync(0xffffffffu, zt > 4.0f || __fmul_rn(st, ft) > 2048.0f)) {
+        // A row's first tokens, and a score 2^20 above all before it (whose weights are nothing beside it),
+        // start the row anew from that score, so that z - m below has a fraction left.
+        bool anew[kGroups][2] = {};
+        if (__any_sync(0xffffffffu, zt > 0x1p20f)) {
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mt = kNoMax;
+#pragma unroll
+              for (int un = 0; un < kUnits; ++un)
+#pragma unroll
+                for (int t = 0; t < kHalves; ++t) mt = fmaxf(mt, z[un][g][t][e]);
+#pragma unroll
+              for (int d = kApart; d < 32; d <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, d));
+              anew[g][e] = __fsub_rn(mt, m[g][e]) > 0x1p20f;
+              if (anew[g][e]) {
+                m[g][e] = ceilf(mt);
+                l[g][e] = 0.0f;
+                f[g][e] = 0x1p127f;              // no weight so far
+              }
+            }
+        }
 #pragma unroll
         for (int g = 0; g < kGroups; ++g)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+            // The largest z and z + log2 s, both beside m: a large z has no room for log2 s.
             float mt = kNoMax, ut = kNoMax;
 #pragma unroll
             for (int un = 0; un < kUnits; ++un)
 #pragma unroll
               for (int t = 0; t < kHalves; ++t) {
-                mt = fmaxf(mt, z[un][g][t][e]);
-                ut = fmaxf(ut, __fadd_rn(z[un][g][t][e], lg2(sv[un][t])));
+                const float zm = __fsub_rn(z[un][g][t][e], m[g][e]);
+                mt = fmaxf(mt, zm);
+                ut = fmaxf(ut, __fadd_rn(zm, lg2(sv[un][t])));
               }
 #pragma unroll
             for (int d = kApart; d < 32; d <<= 1) {
@@ -709,12 +736,12 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
             }
             // log2 f = 7 + m - the largest z + log2 s, that one rounded up
             const float lf = (float)((int)(__float_as_uint(f[g][e]) >> 23) - 127);
-            const float m2 = fmaxf(m[g][e], ceilf(mt));
-            const float u2 = fmaxf(__fadd_rn(__fsub_rn(m[g][e], lf), 7.0f), ceilf(ut));
-            const float l2 = fminf(fmaxf(__fadd_rn(__fsub_rn(m2, u2), 7.0f), -120.0f), 120.0f);
+            const float m2 = __fadd_rn(m[g][e], fmaxf(0.0f, ceilf(mt))), down = __fsub_rn(m[g][e], m2);
+            const float u2 = fmaxf(__fsub_rn(7.0f, lf), ceilf(ut));          // beside the old m
+            const float l2 = fminf(fmaxf(__fsub_rn(7.0f, __fadd_rn(u2, down)), -120.0f), 120.0f);
             const float f2 = __uint_as_float((uint32_t)((int)l2 + 127) << 23);
-            const float by = ex2(__fadd_rn(__fsub_rn(m[g][e], m2), __fsub_rn(l2, lf)));
-            l[g][e] = __fmul_rn(l[g][e], ex2(__fsub_rn(m[g][e], m2)));
+            const float by = anew[g][e] ? 0.0f : ex2(__fadd_rn(down, __fsub_rn(l2, lf)));
+            l[g][e] = __fmul_rn(l[g][e], ex2(down));
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               acc[g][k][e] = __fmul_rn(acc[g][k][e], by);
@@ -808,8 +835,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
         }
         if (n8 == 0 && !low)
           s_stat[warp][8 * g + e0 + e] =
-              RowStat{m[g][e], l[g][e],
-                      __fsub_rn(m[g][e], (float)((int)(__float_as_uint(f[g][e]) >> 23) - 127)), 0.0f};
+              RowStat{m[g][e], l[g][e], (float)(127 - (int)(__float_as_uint(f[g][e]) >> 23)), 0.0f};
       }
     }
     __syncthreads();
@@ -818,18 +844,18 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
       joins[a.by_pair ? seg.b * a.c.n_kv * a.row_tiles + seg.pair : blockIdx.x] =
           make_int4((int)(kv4_divide(seg.at_end - 1, piece.size) - blockIdx.x), blockIdx.x, seg.b, seg.pair);
     if (tid < 8 * kRows) {
-      float M = kNoMax, MW = kNoMax, L = 0.0f;
+      float M = kNoMax, E = kNoMax, L = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        M = fmaxf(M, s_stat[w][rr].m);
-        MW = fmaxf(MW, s_stat[w][rr].mw);
-      }
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_stat[w][rr].m);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) E = fmaxf(E, __fadd_rn(__fsub_rn(s_stat[w][rr].m, M), s_stat[w][rr].e));
 #pragma unroll
       for (int k = 0; k < 16; ++k) x[k] = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        L = __fmaf_rn(s_stat[w][rr].l, ex2(__fsub_rn(s_stat[w][rr].m, M)), L);
-        const float by = ex2(__fsub_rn(s_stat[w][rr].mw, MW));
+        const float down = __fsub_rn(s_stat[w][rr].m, M);
+        L = __fmaf_rn(s_stat[w][rr].l, ex2(down), L);
+        const float by = ex2(__fsub_rn(__fadd_rn(down, s_stat[w][rr].e), E));
         const float4 *src = reinterpret_cast<const float4 *>(s_acc + (w * kRows + rr) * kTile + 16 * r);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -841,7 +867,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
         }
       }
       if (whole) {
-        normalize(x, M, MW, L);
+        normalize(x, E, L);
         finish_row(a, x, s_tr + rr * kTrTile, r, sign_bits, live,
                    ((int64_t)seg.b * a.q_len + row_j) * a.Hq + row_hq);
         if (live && r == 0) finish_stats(a, seg.b, h, row, M, L);
@@ -850,7 +876,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
         float4 *dst = reinterpret_cast<float4 *>(a.part + (slot * kRows + rr) * kTile + 16 * r);
 #pragma unroll
         for (int c = 0; c < 4; ++c) dst[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
-        if (r == 0) reinterpret_cast<float4 *>(a.stat)[slot * kRows + rr] = make_float4(M, L, MW, 0.0f);
+        if (r == 0) reinterpret_cast<float4 *>(a.stat)[slot * kRows + rr] = make_float4(M, L, E, 0.0f);
       }
     }
     __syncthreads();                             // the ring and the statistics are free
@@ -901,6 +927,15 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, i
   if (job.x == 0 || row >= a.R) return;
   const float4 *stat = reinterpret_cast<const float4 *>(a.stat);
   const auto slot_of = [&](int i) { return (2 * ((int64_t)job.y + i) + (i == 0 ? 1 : 0)) * rows + rr; };
+  // A lane's first two references (the last ones again where there are fewer): asked for before the sums
+  // by 8 warps, behind them by one (one sequence of 131072 tokens 34.7 us, 35.8 the other way round; 24
+  // ragged sessions of 4093 tokens with 16 rows 41.6, 42.5).
+  float4 near, far;
+  const auto ask = [&] {
+    near = stat[slot_of(min(lane, job.x))];
+    far = stat[slot_of(min(lane + 32, job.x))];
+  };
+  if (WARPS > 1) ask();
   float4 s[AHEAD], v[AHEAD];
 #pragma unroll
   for (int k = 0; k < AHEAD; ++k) {
@@ -910,21 +945,24 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, i
       v[k] = reinterpret_cast<const float4 *>(a.part + slot_of(i) * kTile)[lane];
     }
   }
-  float M = kNoMax, MW = kNoMax, L = 0.0f;
-  for (int i = lane; i <= job.x; i += 32) {
-    const float4 st = stat[slot_of(i)];
-    M = fmaxf(M, st.x);
-    MW = fmaxf(MW, st.z);
-  }
+  if (WARPS == 1) ask();
+  // RowStat's m and e of the whole row, m first as e is taken beside it
+  float M = fmaxf(near.x, far.x), L = 0.0f;
+#pragma unroll 4
+  for (int i = lane + 64; i <= job.x; i += 32) M = fmaxf(M, stat[slot_of(i)].x);
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) {
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    MW = fmaxf(MW, __shfl_xor_sync(0xffffffffu, MW, d));
-  }
+  for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  const auto e_of = [&](const float4 &st) { return __fadd_rn(__fsub_rn(st.x, M), st.z); };
+  float E = fmaxf(e_of(near), e_of(far));
+#pragma unroll 4
+  for (int i = lane + 64; i <= job.x; i += 32) E = fmaxf(E, e_of(stat[slot_of(i)]));
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) E = fmaxf(E, __shfl_xor_sync(0xffffffffu, E, d));
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const auto add = [&](const float4 &st, const float4 &sums) {
-    L = __fmaf_rn(st.y, ex2(__fsub_rn(st.x, M)), L);
-    const float f = ex2(__fsub_rn(st.z, MW));
+    const float down = __fsub_rn(st.x, M);
+    L = __fmaf_rn(st.y, ex2(down), L);
+    const float f = ex2(__fsub_rn(__fadd_rn(down, st.z), E));
     x.x = __fmaf_rn(sums.x, f, x.x);
     x.y = __fmaf_rn(sums.y, f, x.y);
     x.z = __fmaf_rn(sums.z, f, x.z);
@@ -962,7 +1000,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, i
     const float4 q = reinterpret_cast<const float4 *>(s_x[warp] + 16 * r)[c];
     y[4 * c] = q.x; y[4 * c + 1] = q.y; y[4 * c + 2] = q.z; y[4 * c + 3] = q.w;
   }
-  normalize(y, M, MW, L);
+  normalize(y, E, L);
   const int j = row / a.G, hq = h * a.G + row % a.G;
   const uint32_t sign_bits = a.c.signs[r >> 1] >> (16 * (r & 1));
   finish_row(a, y, s_tr[warp / WARPS] + (lane >> 3) * kTrTile, r, sign_bits, lane < 8,
