@@ -152,3 +152,47 @@ def test_one_score_far_above_the_others(hq, G):
     for z in (1.7e7, 5e7, 5e8, 2.0 ** 60, 2.0 ** 100):
         got = attend(hq, C, dq, sign * z * LN2 / raw, 0.0, torch.float32)
         check_mean(C, got, [np.eye(n)[t] for n, t in zip(lens, tops)])
+
+
+# ------------------------------------------------------------------ accumulated weights
+# A weight is 2^(z - m) / l from the row's own m and l: 4 u for the power, u for the quotient and the
+# product, and l's sum with its terms' powers, below (T / 16 + 40) u; each of a head's G rows is one
+# more rounded addition.
+def mass_bound(T, G):
+    return (T / 16 + 50 + G) * U
+
+
+@pytest.mark.parametrize("G", ROWS)
+@pytest.mark.parametrize("lens,width", [([600, 37], 38), ([1, 16], 64), ([3000, 1], 188)])
+def test_mass_of_equal_scores(hq, G, lens, width):
+    """Every token of a row gets the same weight, whatever the scores; mass that was there stays."""
+    rng = np.random.default_rng(500 + G)
+    C = Cache(hq, rng, lens, 2, 16, width=width, empty=True)
+    q = unit_query()
+    k = rng.standard_normal(128)
+    k[5] = 3.0
+    fill(C, [np.broadcast_to(k, (n, 128)) for n in lens], [rng.standard_normal((n, 128)) for n in lens])
+    raw = raw_score(C, 0, 0, q)
+    dq = torch.from_numpy(np.broadcast_to(q, (2, 1, 2 * G, 128)).copy()).cuda()
+    for mass in (torch.zeros((2, 2, C.width * 16), device="cuda"),
+                 torch.rand((2, 2, C.width * 16), device="cuda")):
+        for z in [3.0, 1e5, 3e6] + SCORES:
+            M = attend(hq, C, dq, z * LN2 / raw, 0.0, torch.float32, mass)[2].double().cpu().numpy()
+            before = mass.double().cpu().numpy()
+            for b, n in enumerate(lens):
+                want = before[b, :, :n] + G / n
+                assert (np.abs(M[b, :, :n] - want) <= mass_bound(n, G) * G / n + U * want).all(), (z, b)
+
+
+@pytest.mark.parametrize("G", ROWS)
+def test_mass_of_any_scores_adds_up(hq, G):
+    """A row's weights add up to 1: random scores up to some 10^8, and one far above the others."""
+    rng = np.random.default_rng(600 + G)
+    lens = [700, 90]
+    C = Cache(hq, rng, lens, 2, 16, width=50)
+    q = queries(rng, 2, 1, 2 * G, "f32")
+    mass = torch.zeros((2, 2, C.width * 16), device="cuda")
+    for scale in (0.1, 1.0, 1e3, 1e5, -1e6, 1e7):
+        M = attend(hq, C, q, scale, 0.0, torch.float32, mass)[2].double().cpu().numpy()
+        for b, n in enumerate(lens):
+            assert (np.abs(M[b, :, :n].sum(-1) / G - 1) <= mass_bound(n, G)).all(), (scale, b)

@@ -77,8 +77,8 @@ int rows_call(const hq_kv4_cache *c, const void *k, const void *v, int kind, int
 }
 
 struct AttnSizes {
-  size_t part = 0, stat = 0, joins = 0, z = 0, row_lse = 0;
-  size_t total() const { return part + stat + joins + z + row_lse; }
+  size_t part = 0, stat = 0, joins = 0, z = 0, row_stat = 0;
+  size_t total() const { return part + stat + joins + z + row_stat; }
 };
 
 bool attn_sizes(const hq_kv4_cache *c, int q_len, int Hq, int want_mass, AttnSizes *s) {
@@ -92,7 +92,7 @@ bool attn_sizes(const hq_kv4_cache *c, int q_len, int Hq, int want_mass, AttnSiz
     const size_t cap = (size_t)c->table_width * c->page_tokens;
     if (cap != 0 && (size_t)rows > ((size_t)1 << 44) / cap) return false;
     s->z = round256((size_t)rows * cap * sizeof(float));
-    s->row_lse = round256((size_t)rows * sizeof(float));
+    s->row_stat = round256((size_t)rows * sizeof(float2));
   }
   return true;
 }
@@ -172,7 +172,7 @@ int hq_kv4_attention(const hq_kv4_cache *c, const int32_t *d_lengths, const void
   a.joins = reinterpret_cast<int *>(ws);
   ws += s.joins;
   a.z = reinterpret_cast<float *>(ws);
-  a.row_lse = reinterpret_cast<float *>(ws + s.z);
+  a.row_stat = reinterpret_cast<float2 *>(ws + s.z);
   a.status = d_status;
   return hq::launch_kv4_attention(a, reinterpret_cast<cudaStream_t>(stream)) == 0 ? HQ_OK : HQ_ERR_CUDA;
 }
