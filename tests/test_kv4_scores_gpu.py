@@ -155,9 +155,9 @@ def test_one_score_far_above_the_others(hq, G):
 
 
 # ------------------------------------------------------------------ accumulated weights
-# A weight is 2^(z - m) / l from the row's own m and l: 4 u for the power, u for the quotient and the
-# product, and l's sum with its terms' powers, below (T / 16 + 40) u; each of a head's G rows is one
-# more rounded addition.
+# A weight is 2^((z - m) - log2 l) from the row's own m and l: 4 u for the power, 17 u for log2 l (below
+# 16: a step of 16 u, and half of one for the difference, times ln 2), l's sum with its terms' powers
+# (T / 16 + 24) u, and one rounded addition for each of a head's G rows.
 def mass_bound(T, G):
     return (T / 16 + 50 + G) * U
 

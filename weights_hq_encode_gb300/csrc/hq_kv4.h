@@ -65,7 +65,7 @@ struct Kv4AttnArgs {
   float *stat;              // workspace: their references and sums of weights
   int *joins;               // workspace: what is left to be joined
   float *z;                 // workspace [n_seqs][n_kv][R][capacity] when mass is wanted
-  float2 *row_stat;         // workspace [n_seqs][n_kv][R]: a row's reference and 1 / its sum beside it
+  float2 *row_stat;         // workspace [n_seqs][n_kv][R]: a row's reference and log2 of its sum beside it
   uint32_t *status;
 };
 

@@ -208,11 +208,10 @@ __device__ __forceinline__ void normalize(float x[16], float e, float l) {
 }
 
 __device__ __forceinline__ void finish_stats(const Kv4AttnArgs &a, int b, int h, int row, float M, float L) {
-  const float l2 = L == 0.0f ? -INFINITY : __fadd_rn(M, log2f(L));
+  const float l2 = L == 0.0f ? -INFINITY : log2f(L);
   const int j = row / a.G, hq = h * a.G + row % a.G;
-  if (a.lse != nullptr) a.lse[((int64_t)b * a.q_len + j) * a.Hq + hq] = __fmul_rn(l2, kLn2);
-  if (a.mass_out != nullptr)
-    a.row_stat[((int64_t)b * a.c.n_kv + h) * a.R + row] = make_float2(M, L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L));
+  if (a.lse != nullptr) a.lse[((int64_t)b * a.q_len + j) * a.Hq + hq] = __fmul_rn(__fadd_rn(M, l2), kLn2);
+  if (a.mass_out != nullptr) a.row_stat[((int64_t)b * a.c.n_kv + h) * a.R + row] = make_float2(M, l2);
 }
 
 // Where a block's piece of the batch begins, and the piece's length: the
@@ -1009,9 +1008,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, i
   if (lane == 0) finish_stats(a, job.z, h, row, M, L);
 }
 
-// mass_out = mass_in + sum over the head's rows of 2^(z - m) / l, rows in order, four
-// tokens a thread.  m and l by themselves: from log2 of the whole sum, m + log2 l, large
-// scores would take the bits of log2 l (up to 0.3% of a weight at scores of 10^5).
+// mass_out = mass_in + sum over the head's rows of 2^((z - m) - log2 l), rows in order,
+// four tokens a thread.  m and log2 l by themselves: in their sum large scores would
+// take the bits of log2 l (up to 0.3% of a weight at scores of 10^5).
 constexpr int kMassThreads = 256;
 __global__ void __launch_bounds__(kMassThreads) kv4_mass_kernel(Kv4AttnArgs a) {
   follow_launch();
@@ -1027,11 +1026,11 @@ __global__ void __launch_bounds__(kMassThreads) kv4_mass_kernel(Kv4AttnArgs a) {
 #pragma unroll 4
   for (int row = 0; row < a.R; ++row) {
     const float4 v = *reinterpret_cast<const float4 *>(z + row * cap);
-    const float2 ml = stat[row];                 // m, 1 / l
+    const float2 ml = stat[row];
     const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (x[k] > -INFINITY || x[k] != x[k]) s[k] = __fmaf_rn(ex2(__fsub_rn(x[k], ml.x)), ml.y, s[k]);
+      if (x[k] > -INFINITY || x[k] != x[k]) s[k] = __fadd_rn(s[k], ex2(__fsub_rn(__fsub_rn(x[k], ml.x), ml.y)));
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
