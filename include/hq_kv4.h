@@ -118,7 +118,7 @@ size_t hq_kv4_attention_workspace_bytes(const hq_kv4_cache *c, int q_len, int Hq
  *   d_lengths   [n_seqs] int32, the new tokens included
  *   d_q         row (b, j, hq) starts at element b * q_seq_stride +
  *               j * q_token_stride + hq * q_head_stride; kind q_kind
- *   scale       finite; cap 0 (none) or finite and >= 2^-20
+ *   scale       finite; cap 0 (none) or 2^-20 .. 2^120
  *   d_out       [n_seqs][q_len][Hq][128] of out_kind, 16-byte aligned
  *   d_lse       [n_seqs][q_len][Hq] fp32, or NULL
  *   d_mass_in   [n_seqs][n_kv_heads][table_width * page_tokens] fp32, or NULL: zeros

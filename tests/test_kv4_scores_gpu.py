@@ -16,7 +16,7 @@ import pytest
 import torch
 
 from oracle import kv4 as R
-from test_kv4_gpu import MASK, U, Cache, attend, hq, queries  # noqa: F401  (hq: a fixture)
+from test_kv4_gpu import MASK, U, Cache, attend, check, hq, queries  # noqa: F401  (hq: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -196,3 +196,19 @@ def test_mass_of_any_scores_adds_up(hq, G):
         M = attend(hq, C, q, scale, 0.0, torch.float32, mass)[2].double().cpu().numpy()
         for b, n in enumerate(lens):
             assert (np.abs(M[b, :, :n].sum(-1) / G - 1) <= mass_bound(n, G)).all(), (scale, b)
+
+
+# ------------------------------------------------------------------ sizes of operands and caps
+@pytest.mark.parametrize("power", [-90, -40, 0, 40, 90])
+def test_queries_and_keys_of_any_size(hq, power):
+    """Queries 2^power large over keys 2^-power large, so that the scores are of ordinary size, under
+    caps from 2^-20 to 2^120 and without one; the bound is that of tests/test_kv4_gpu.py."""
+    rng = np.random.default_rng(700 + power)
+    lens = [333, 20]
+    C = Cache(hq, rng, lens, 2, 16, empty=True)
+    fill(C, [rng.standard_normal((n, 128)) * 2.0 ** -power for n in lens],
+         [rng.standard_normal((n, 128)) for n in lens])
+    for G in (4, 6):
+        q = queries(rng, 2, 1, 2 * G, "f32") * 2.0 ** power
+        for cap in (0.0, 2.0 ** -20, 1.0, 30.0, 2.0 ** 20, 2.0 ** 60, 2.0 ** 100, 2.0 ** 120):
+            check(C, q, 0.1, cap, attend(hq, C, q, 0.1, cap, torch.float32))

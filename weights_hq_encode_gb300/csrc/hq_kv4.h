@@ -52,8 +52,8 @@ struct Kv4AttnArgs {
   int kind, out_kind;
   int q_vec;
   int q_len, Hq, G, R;      // G query heads a KV head, R = q_len * G rows a KV head
-  float scale;              // softmax scale, and the cap of the scores (0: none)
-  float cap;
+  float scale;              // softmax scale
+  float cap, cap_l2, by_cap;   // cap of the scores (0: none), times log2(e), and 1 / cap
   void *out;                // [n_seqs][q_len][Hq][128]
   float *lse;               // [n_seqs][q_len][Hq] or nullptr
   const float *mass_in;     // [n_seqs][n_kv][capacity] or nullptr

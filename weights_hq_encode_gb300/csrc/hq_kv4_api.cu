@@ -12,6 +12,7 @@ namespace {
 using namespace hq;
 
 constexpr int64_t kMaxCapacity = (int64_t)1 << 30;
+constexpr float kMinCap = 0x1p-20f, kMaxCap = 0x1p120f;   // 1 / cap and cap log2(e) are normal numbers
 
 bool aligned(const void *ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
@@ -134,7 +135,7 @@ int hq_kv4_attention(const hq_kv4_cache *c, const int32_t *d_lengths, const void
                      size_t ws_bytes, uint32_t *d_status, hq_stream_t stream) {
   AttnSizes s;
   if (!cache_ok(c) || !kind_ok(q_kind) || !kind_ok(out_kind) || !d_status || !std::isfinite(scale) ||
-      !std::isfinite(cap) || cap < 0.0f || (cap > 0.0f && cap < 0x1p-20f) || (d_mass_in && !d_mass_out) ||
+      !(cap == 0.0f || (cap >= kMinCap && cap <= kMaxCap)) || (d_mass_in && !d_mass_out) ||
       !attn_sizes(c, q_len, Hq, d_mass_out != nullptr, &s))
     return HQ_ERR_INVALID;
   if (c->n_seqs == 0) return HQ_OK;
@@ -159,6 +160,8 @@ int hq_kv4_attention(const hq_kv4_cache *c, const int32_t *d_lengths, const void
   a.R = q_len * a.G;
   a.scale = scale;
   a.cap = cap;
+  a.cap_l2 = cap * 1.4426950408889634f;
+  a.by_cap = cap > 0.0f ? 1.0f / cap : 0.0f;
   a.out = d_out;
   a.lse = d_lse;
   a.mass_in = d_mass_in;

@@ -83,10 +83,12 @@ __device__ __forceinline__ void code_pairs(uint32_t x, uint32_t factor, uint32_t
   p[2] = centred(y & 0x000F000Fu, factor, 0xA380A380u);
   p[3] = centred(y, factor, 0xB3F8B3F8u);
 }
-// cap tanh(y) of two values: y's sign and 1 - 2 / (1 + e^2|y|) from 1/4 on; below, where
-// that is off by 2^-23 beside a small value, y - y^3 / 3 + 2 y^5 / 15 - 17 y^7 / 315, whose rest
-// is less than 3.4e-7 of it.
-__device__ __forceinline__ uint64_t cap_tanh(uint64_t yy, float cap) {
+// cap log2(e) tanh(y), y = z / cap, of two values: y's sign and 1 - 2 / (1 + e^2|y|) from 1/4 on; below,
+// where that is off by 2^-23 beside a small value, y - y^3 / 3 + 2 y^5 / 15 - 17 y^7 / 315, whose rest
+// is less than 3.4e-7 of it.  y is formed from z: with 1 / cap in the multipliers of a score's parts,
+// small queries over large keys under a large cap left fp32's range on the way.
+__device__ __forceinline__ uint64_t cap_tanh(float z0, float z1, const Kv4AttnArgs &a) {
+  const uint64_t yy = pk2(__fmul_rn(z0, a.by_cap), __fmul_rn(z1, a.by_cap));
   const uint64_t y2 = mul2(yy, yy);
   uint64_t t = fma2(y2, pk2(-17.0f / 315.0f, -17.0f / 315.0f), pk2(2.0f / 15.0f, 2.0f / 15.0f));
   t = fma2(y2, t, pk2(-1.0f / 3.0f, -1.0f / 3.0f));
@@ -98,7 +100,7 @@ __device__ __forceinline__ uint64_t cap_tanh(uint64_t yy, float cap) {
   for (int e = 0; e < 2; ++e) {
     const float ey = ex2(__fmul_rn(fabsf(y[e]), 2.0f * kLog2e));
     const float far = copysignf(__fsub_rn(1.0f, __fdividef(2.0f, __fadd_rn(ey, 1.0f))), y[e]);
-    p[e] = __fmul_rn(cap, fabsf(y[e]) < 0.25f ? p[e] : far);
+    p[e] = __fmul_rn(a.cap_l2, fabsf(y[e]) < 0.25f ? p[e] : far);
   }
   return pk2(p[0], p[1]);
 }
@@ -530,7 +532,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
         }
       }
       if (r == 0) {
-        s_mul[rr] = CAP ? __fmul_rn(__fdiv_rn(a.scale, a.cap), inv) : __fmul_rn(__fmul_rn(a.scale, kLog2e), inv);
+        s_mul[rr] = __fmul_rn(CAP ? a.scale : __fmul_rn(a.scale, kLog2e), inv);
         s_seen[rr] = max(0, len - a.q_len + row_j + 1);
       }
     }
@@ -549,7 +551,6 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
       m_other[g] = mul2(mul, pk2(k_other, k_other));
     }
     const int seen_all = len - a.q_len + row0 / a.G + 1;    // the least of any row here
-    const float cap_l2 = CAP ? __fmul_rn(a.cap, kLog2e) : 0.0f;
 
     // sums: l of 2^(z - m), acc of w (c - 7.5) 2^-9, w = 2^(z - m) s f, f a power of two a row;
     // acc of odd dimensions with 16 times theirs and the even one's before them
@@ -635,8 +636,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
             }
             float *const zz = z[un][g][t];
             uint64_t y = mul2(fma2(other, m_other[g], mul2(own, m_own[g])), pk2(sk, sk));
-            if (CAP) y = cap_tanh(y, cap_l2);
             upk2(y, zz[0], zz[1]);
+            if (CAP) upk2(cap_tanh(zz[0], zz[1], a), zz[0], zz[1]);
           }
         }
       }
