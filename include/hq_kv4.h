@@ -114,11 +114,15 @@ size_t hq_kv4_attention_workspace_bytes(const hq_kv4_cache *c, int q_len, int Hq
  * are held in fp32; the contractions run on fp16 tensor-core operands, each
  * query value and each weight split into two fp16 parts (|x - hi - lo| <=
  * 2^-22 |x| + 2^-25 of the row's power-of-two scale), the codes being exact
- * in fp16: an fp32-level result.  The order of all sums is fixed.
+ * in fp16: an fp32-level result.  The order of all sums is fixed.  Scores may
+ * be of any size: a row stays a weighted mean of V's rows, with weights that
+ * add up to 1, while |q|, |scale| |q| and |scale| |q| |Khat| (norms) are below
+ * 2^110; beyond, and for a query that is not finite, that row may come out
+ * non-finite.
  *   d_lengths   [n_seqs] int32, the new tokens included
  *   d_q         row (b, j, hq) starts at element b * q_seq_stride +
  *               j * q_token_stride + hq * q_head_stride; kind q_kind
- *   scale       finite; cap 0 (none) or 2^-20 .. 2^120
+ *   scale       at most 2^120 in magnitude; cap 0 (none) or 2^-20 .. 2^120
  *   d_out       [n_seqs][q_len][Hq][128] of out_kind, 16-byte aligned
  *   d_lse       [n_seqs][q_len][Hq] fp32, or NULL
  *   d_mass_in   [n_seqs][n_kv_heads][table_width * page_tokens] fp32, or NULL: zeros

@@ -15,3 +15,12 @@ def test_caps(hq, cap, taken):
     """cap log2(e) and 1 / cap have to be normal fp32 numbers: above 2.36e38 the first was infinite."""
     got = call_attention(hq, cache(hq, n_seqs=0), cap=cap)
     assert got == (hq.HQ_OK if taken else hq.HQ_ERR_INVALID)
+
+
+@pytest.mark.parametrize("scale,taken", [
+    (0.0, True), (0.1, True), (-2.0 ** 120, True), (2.0 ** 120, True), (2.0 ** 120 * 1.001, False),
+    (2.0 ** 127, False), (-FLT_MAX, False), (FLT_MAX, False), (float("nan"), False)])
+def test_scales(hq, scale, taken):
+    """scale log2(e) has to be finite: above 2.36e38 every score was infinite or NaN."""
+    got = call_attention(hq, cache(hq, n_seqs=0), scale=scale)
+    assert got == (hq.HQ_OK if taken else hq.HQ_ERR_INVALID)

@@ -212,3 +212,21 @@ def test_queries_and_keys_of_any_size(hq, power):
         q = queries(rng, 2, 1, 2 * G, "f32") * 2.0 ** power
         for cap in (0.0, 2.0 ** -20, 1.0, 30.0, 2.0 ** 20, 2.0 ** 60, 2.0 ** 100, 2.0 ** 120):
             check(C, q, 0.1, cap, attend(hq, C, q, 0.1, cap, torch.float32))
+
+
+@pytest.mark.parametrize("G", ROWS)
+def test_the_largest_scale(hq, G):
+    """Large scales beside small queries: scores of ordinary size, and of some 10^10."""
+    rng = np.random.default_rng(800 + G)
+    C = Cache(hq, rng, [100, 7], 2, 16)
+    q = queries(rng, 2, 1, 2 * G, "f32") * 2.0 ** -90
+    for scale in (2.0 ** 86, 2.0 ** 120):
+        got = attend(hq, C, q, scale, 0.0, torch.float32)
+        if scale < 2.0 ** 100:
+            check(C, q, scale, 0.0, got)
+        for b, n in enumerate(C.lens):           # inside the hull of V's rows
+            V = R.rotated(C.pages, C.table, b, n, 1)
+            s = np.concatenate([R.raw_rows(C.pages, p, 1)[1] for p in C.table[b, :-(-n // 16)]], 1)[:, :n]
+            hull = np.abs(R.back(V, MASK)).max()
+            tol = value_bound(V, s, n).max()
+            assert (got[0][b].double().abs() <= hull + tol).all()     # NaN fails as well

@@ -12,7 +12,8 @@ namespace {
 using namespace hq;
 
 constexpr int64_t kMaxCapacity = (int64_t)1 << 30;
-constexpr float kMinCap = 0x1p-20f, kMaxCap = 0x1p120f;   // 1 / cap and cap log2(e) are normal numbers
+// so that 1 / cap and cap log2(e) are normal numbers, and scale log2(e) is finite
+constexpr float kMinCap = 0x1p-20f, kMaxCap = 0x1p120f, kMaxScale = 0x1p120f;
 
 bool aligned(const void *ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
@@ -134,7 +135,7 @@ int hq_kv4_attention(const hq_kv4_cache *c, const int32_t *d_lengths, const void
                      float *d_lse, const float *d_mass_in, float *d_mass_out, void *d_ws,
                      size_t ws_bytes, uint32_t *d_status, hq_stream_t stream) {
   AttnSizes s;
-  if (!cache_ok(c) || !kind_ok(q_kind) || !kind_ok(out_kind) || !d_status || !std::isfinite(scale) ||
+  if (!cache_ok(c) || !kind_ok(q_kind) || !kind_ok(out_kind) || !d_status || !(std::fabs(scale) <= kMaxScale) ||
       !(cap == 0.0f || (cap >= kMinCap && cap <= kMaxCap)) || (d_mass_in && !d_mass_out) ||
       !attn_sizes(c, q_len, Hq, d_mass_out != nullptr, &s))
     return HQ_ERR_INVALID;
