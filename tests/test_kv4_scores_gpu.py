@@ -230,3 +230,36 @@ def test_the_largest_scale(hq, G):
             hull = np.abs(R.back(V, MASK)).max()
             tol = value_bound(V, s, n).max()
             assert (got[0][b].double().abs() <= hull + tol).all()     # NaN fails as well
+
+
+# ------------------------------------------------------------------ size of the error
+# A score is 8 steps of the tensor cores over centred codes: 16 products, each of at most 17/16 |q'| |c - 7.5|,
+# and the sum so far.  A step may cut each of the 17 addends by 2 u of the largest, and no partial sum is
+# beyond |q'| |c - 7.5|: with 30 u for the query's transform and parts, the multipliers and the scale,
+#   |dz| <= (30 + 8 x 34 x 17/16) u zeta <= 320 u zeta,   zeta = |scale| |q| max |Khat|,
+# where tests/test_kv4_gpu.py still counts uncentred codes (30 u zeta + 294 u zeta_codes, some 3 times as much).
+# These are worst cases; a loss of precision shows earlier in all rows together.  With scores of rms 1 the
+# largest addend is about the partial sum, below the score itself, so a step's 17 cuts are
+# sqrt(17) 2 u / sqrt(3) = 4.8 u and 8 steps 14 u; they are independent from token to token, so that an
+# output's norm is off by 14 u.  The value side adds T / 64 steps of 4.8 u a warp to a sum
+# that grows to the output's size, below 14 u for T = 500.
+# sqrt(14^2 + 14^2) u = 20 u is the limit; as every largest addend is counted at the full score, a kernel of
+# centred codes stays below it (5 to 10 u), one of uncentred codes, whose partial sums are 7.5 |sum q'| and
+# more, does not (33 to 43 u).
+@pytest.mark.parametrize("G", ROWS)
+def test_errors_of_all_rows_together(hq, G):
+    rng = np.random.default_rng(900 + G)
+    lens = [500, 467]
+    C = Cache(hq, rng, lens, 2, 16, empty=True)
+    fill(C, *[[rng.standard_normal((n, 128)) for n in lens] for _ in range(2)])
+    q = queries(rng, 2, 1, 2 * G, "f32", size=1.0)
+    scale = 128 ** -0.5
+    out, lse, _ = attend(hq, C, q, scale, 0.0, torch.float32)
+    ref = R.attention(C.pages, C.table, lens, q.double().cpu().numpy(), MASK, scale)
+    err = np.linalg.norm(out.double().cpu().numpy() - ref["out"], axis=-1)
+    score = 320 * U * ref["zeta"]
+    bound = ((2 * score + (34 * max(lens) / 16 + 100) * U) * np.linalg.norm(ref["size"], axis=-1) +
+             600 * U * np.sqrt(128.0) * ref["scales"])
+    assert (err <= bound).all()
+    assert (np.abs(lse.double().cpu().numpy() - ref["lse"]) <= score + (max(lens) / 16 + 50) * U).all()
+    assert np.linalg.norm(err) <= 20 * U * np.linalg.norm(ref["out"])
