@@ -294,23 +294,30 @@ def run(state):
     return (_run_own if own else _run_plain)(state)
 
 
+def _done(code):
+    """A call that the library refused, or could not launch, is no pass."""
+    if code != 0:
+        raise RuntimeError(f"the library returned {code}")
+
+
 def _run_own(s):
     from weights_hq_encode_gb300 import hq
     op = s["case"]["op"]
     if op == "append":
-        hq.hq_kv4_append(s["cache"], s["k"], s["v"], s["seq"], s["pos"], s["status"])
-        hq.hq_kv4_read(s["cache"], s["seq"], s["pos"], *s["rows"], s["status"])
+        _done(hq.hq_kv4_append(s["cache"], s["k"], s["v"], s["seq"], s["pos"], s["status"]))
+        _done(hq.hq_kv4_read(s["cache"], s["seq"], s["pos"], *s["rows"], s["status"]))
         return s["rows"]
     if op == "read":
-        hq.hq_kv4_read(s["cache"], s["seq"], s["pos"], *s["rows"], s["status"])
+        _done(hq.hq_kv4_read(s["cache"], s["seq"], s["pos"], *s["rows"], s["status"]))
         return s["rows"]
     if op == "attend":
-        hq.hq_kv4_attention(s["cache"], s["lengths"], s["q"], s["scale"], s["case"]["cap"],
-                            s["out"], s["lse"], s["mass"], s["mass_out"], s["ws"], s["status"])
+        _done(hq.hq_kv4_attention(s["cache"], s["lengths"], s["q"], s["scale"], s["case"]["cap"],
+                                  s["out"], s["lse"], s["mass"], s["mass_out"], s["ws"],
+                                  s["status"]))
         return [s["out"], s["lse"]] + ([s["mass_out"]] if s["mass"] is not None else [])
-    hq.hq_kv4_evict(s["cache"], s["lengths"], s["mass"], s["new_cache"], s["case"]["recent"],
-                    s["kept"], s["new_lengths"], s["new_mass"], s["status"])
-    hq.hq_kv4_read(s["new_cache"], s["seq"], s["pos"], *s["rows"], s["status"])
+    _done(hq.hq_kv4_evict(s["cache"], s["lengths"], s["mass"], s["new_cache"], s["case"]["recent"],
+                          s["kept"], s["new_lengths"], s["new_mass"], s["status"]))
+    _done(hq.hq_kv4_read(s["new_cache"], s["seq"], s["pos"], *s["rows"], s["status"]))
     return [s["kept"], s["new_lengths"], s["new_mass"], *s["rows"]]
 
 
