@@ -60,7 +60,7 @@ enum { HQ_T_BF16 = 0, HQ_T_F32 = 1, HQ_T_F16 = 2 };
  *                 sequence's length are not read
  *   d_signs       [4] uint32: the sign mask of every tile (hq_make_layer_signs)
  * table_width * page_tokens, a sequence's capacity, is at most 2^30, and the
- * pool holds fewer than 2^28 units (527 GB). */
+ * pool holds fewer than 2^28 units (567 GB). */
 typedef struct hq_kv4_cache {
   void *d_pages;
   int64_t n_pages;
@@ -100,7 +100,10 @@ int hq_kv4_read(const hq_kv4_cache *c, const int32_t *d_seq, const int32_t *d_po
                 int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
                 uint32_t *d_status, hq_stream_t stream);
 
-/* Bytes of device workspace hq_kv4_attention needs (0 for invalid sizes). */
+/* Bytes of device workspace hq_kv4_attention needs (0 for invalid sizes): at
+ * most 18 MB without mass.  With it, 4 bytes more for every query row and position
+ * that the table has room for, n_seqs * q_len * Hq * table_width * page_tokens,
+ * whatever the lengths. */
 size_t hq_kv4_attention_workspace_bytes(const hq_kv4_cache *c, int q_len, int Hq, int want_mass);
 
 /* Attention of the last q_len tokens of every sequence over its cache, read
@@ -118,7 +121,8 @@ size_t hq_kv4_attention_workspace_bytes(const hq_kv4_cache *c, int q_len, int Hq
  * be of any size: a row stays a weighted mean of V's rows, with weights that
  * add up to 1, while |q|, |scale| |q| and |scale| |q| |Khat| (norms) are below
  * 2^110; beyond, and for a query that is not finite, that row may come out
- * non-finite.
+ * non-finite.  The cache is streamed once for every 16 query rows of a KV
+ * head, q_len * Hq / n_kv_heads: made for one to some tens of new tokens.
  *   d_lengths   [n_seqs] int32, the new tokens included
  *   d_q         row (b, j, hq) starts at element b * q_seq_stride +
  *               j * q_token_stride + hq * q_head_stride; kind q_kind
@@ -155,7 +159,8 @@ int hq_kv4_attention(const hq_kv4_cache *c, const int32_t *d_lengths, const void
  *                  mass; entries from the new length on are left as they were
  * d_kept, d_new_lengths and d_new_mass overlap no input (new lengths or masses
  * in the place of the old ones are refused).  d_status is OR-ed
- * with HQ_ERR_PAGE. */
+ * with HQ_ERR_PAGE; what d_kept, d_new_lengths and d_new_mass count then
+ * includes rows that were left out of dst, so dst is not to be used. */
 int hq_kv4_evict(const hq_kv4_cache *src, const int32_t *d_lengths, const float *d_mass,
                  const hq_kv4_cache *dst, int budget, int recent, int32_t *d_kept,
                  int32_t *d_new_lengths, float *d_new_mass, uint32_t *d_status,

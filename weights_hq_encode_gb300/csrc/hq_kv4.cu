@@ -193,8 +193,9 @@ __device__ __forceinline__ void store4(char *to, const float v[4], const uint32_
 // exact (+-1 times half-integers, sums below 2^10 in fp16 and fp32), so the
 // one rounding is that of the product with the scale; and a lane ends with
 // dimensions 8 n8 + 2 c4 and the next, and the same + 64: whole 128-byte
-// stores.  262144 entries to bf16: 37.5 us, 25 of them the memory's, bound by the
-// issue of 81 instructions an entry (56% of the cycles).  The codec's transform
+// stores.  262144 entries to bf16: 37.5 us, 25 of them the memory's.  The first stall is
+// the codes' loads, of which registers let a warp ask for four entries at a time (5.0
+// cycles an instruction); 81 instructions an entry issue in 55% of the cycles.  The codec's transform
 // in registers and shared memory instead takes 330 for 4 rows, 68 us.
 constexpr int kReadBatch = 4;                    // entries of a warp at a time
 template <int KIND, bool VEC>

@@ -44,11 +44,17 @@ struct Shape {
 // Work of one (sequence, head, row tile) beyond its units, in units: the
 // blocks split the batch into equal pieces of units + kSegmentCost.  Rotating
 // its queries and adding up its sums takes a block 4 to 5 us, in which it streams
-// 16 to 30 units (24 ragged sessions of 4093 tokens with 16 rows: 46.5 us with a cost of 8,
-// 42.4 with 16, 41.9 with 24, 42.0 with 32).
+// 16 to 30 units.  Costs of 8 / 16 / 24 / 32 in us, without a cap: 24 ragged sessions of 4093 tokens 26.5 / 23.5 /
+// 23.4 / 23.5 with 4 rows, 32.1 / 28.2 / 27.5 / 26.7 with 8, 43.4 / 39.5 / 38.8 / 38.0 with 16; one of 131072
+// tokens 35.3 / 33.7 / 34.9 / 35.1 with 4 rows, 41.8 / 41.0 / 42.4 / 42.4 with 8, 63.0 / 61.6 / 62.8 / 63.0
+// with 16; 16 of 32768 tokens 108.5 / 107.4 / 110 / 112 with 4 rows.
 constexpr int kSegmentCost = 24, kMinPiece = 40;
-// A batch whose longest sequence is this short is not split inside sequences:
-// a join would take longer than the units it spreads.
+// Where the table has room for no span (units + kSegmentCost) longer than this, and
+// all (sequence, head, row tile) triples fit at once, each gets a block and nothing is joined: a join takes
+// longer than the units it spreads.  The lengths are not known to the launch, so a wider table
+// takes the other path, whatever the lengths (one session of 77 tokens: 5.5 us, and 7.1 to 7.4 with a table
+// for more than 640 tokens).  On that path pieces are no shorter than the longest span
+// up to this, so that a triple is cut once at most.
 constexpr int kWholeSpan = 64;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -385,17 +391,21 @@ __device__ Piece find_piece(const Kv4AttnArgs &a) {
 // block and parts in columns).  The codes are unpacked in registers,
 // straight into operand fragments; that is why these are not tcgen05
 // products, whose operands would first have to be stored to shared memory as
-// fp16, four times the bytes that were read: 1 KB of 16-bit K and V a token
-// against the 128 bytes a cycle that shared memory takes, 16 cycles for reading and
-// writing a token beside the 5 to 6 in which memory delivers it.
+// fp16, four times the bytes that were read: 512 bytes of K and V a token and head,
+// written and read 1 KB, 8 cycles at the 128 bytes a cycle that shared memory takes.  Memory
+// delivers a token in 6, and with 4 rows this kernel takes 8 (16 x 32768 tokens).  With 16 rows it takes 19,
+// and there the choice is not shown to be the better one.
 //
-// 16 sequences x 32768 tokens x 8 heads, 4 query rows a head: 108 us, 5.1 TB/s,
+// Every 16 rows of a head stream and unpack all its tokens again, those that none of the rows sees among
+// them: many new tokens at once are right but slow (512 over 32768 tokens, 8 heads x 4 rows: 1.59 ms).
+//
+// 16 sequences x 32768 tokens x 8 heads, 4 query rows a head: 109 us, 5.1 TB/s,
 // 75% of the copy rate; the copies alone take 98 us, the rest is what instruction
 // issue (about 293 a warp for 16 tokens, 54% of the cycles) does not hide.  One
-// sequence of 131072 tokens: 34.5 us, of which 13 do not depend on its length (the
+// sequence of 131072 tokens: 34.8 us, of which 13 do not depend on its length (the
 // first tile's way 4, the end and the join 5).  With 16 query rows a head, 24
 // ragged sessions of 4093 tokens take 42 us (join included), bound by the latency of
-// 8 warps a multiprocessor (issue 42%, tensor cores 51%).
+// 8 warps a multiprocessor (issue 41%, tensor cores 49%).
 template <int kRows, bool CAP, bool MASS>
 __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_kernel(Kv4AttnArgs a) {
   constexpr bool kWide = kRows > 4;              // high and low parts in products of their own
@@ -912,7 +922,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
 // 57 blocks a row) with 8 sums ahead 34.5 us in all, with 4 36.9, with 32 warps
 // 35.5; 128 x 4 rows with 4 ahead 42.7 (attention of 16 ragged sessions of 8192 tokens,
 // with mass), with 8 (registers for half the blocks) 44.7, with one warp 44.9;
-// 128 x 16 rows (16 x 4096 tokens) with one 40.3, with 8 44.9.
+// 128 x 16 rows (16 x 4096 tokens) with one 40.3, with 8 44.9.  (References in one number then.)
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 template <int WARPS, int AHEAD>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4AttnArgs a, int rows, int items) {
