@@ -154,6 +154,35 @@ def test_one_score_far_above_the_others(hq, G):
         check_mean(C, got, [np.eye(n)[t] for n, t in zip(lens, tops)])
 
 
+@pytest.mark.parametrize("G", ROWS)
+@pytest.mark.parametrize("lens,width", [([600, 90], 38), ([2000, 90], 130)])
+def test_scores_that_climb(hq, G, lens, width):
+    """Scores that go from far below to far above zero along the tokens, by steps below and above
+    what starts a row anew: three equal ones at the end share the weight."""
+    rng = np.random.default_rng(450 + G)
+    C = Cache(hq, rng, lens, 2, 16, width=width, empty=True)
+    k = rng.standard_normal(128)
+    k[5] = 3.0
+    q = unit_query()
+    steps = np.array([-1.0, -2.0 ** -4, -2.0 ** -9, 2.0 ** -12, 2.0 ** -6, 2.0 ** -2, 2.0 ** -1])
+    size = [steps[np.arange(n) * len(steps) // n] for n in lens]
+    shares = []
+    for a in size:
+        a[[-1, -2, -40]] = 1.0
+        shares.append((a == 1.0) / 3.0)
+    fill(C, [k[None] * a[:, None] for a in size],
+         [rng.standard_normal((n, 128)) * 2.0 ** rng.uniform(-15, 15, (n, 1)) for n in lens])
+    raw = raw_score(C, 0, lens[0] - 1, q)
+    dq = torch.from_numpy(np.broadcast_to(q, (2, 1, 2 * G, 128)).copy()).cuda()
+    mass = torch.zeros((2, 2, C.width * 16), device="cuda")
+    for z in (1e4, 1e6, 3e6, 1.7e7, 5e8, 2.0 ** 60, 2.0 ** 100):
+        got = attend(hq, C, dq, z * LN2 / raw, 0.0, torch.float32, mass)
+        check_mean(C, got, shares)
+        M = got[2].double().cpu().numpy()
+        for b, n in enumerate(lens):
+            assert (np.abs(M[b, :, :n] - G * shares[b]) <= mass_bound(n, G) * G * shares[b]).all()
+
+
 # ------------------------------------------------------------------ accumulated weights
 # A weight is 2^((z - m) - log2 l) from the row's own m and l: 4 u for the power, 17 u for log2 l (below
 # 16: a step of 16 u, and half of one for the difference, times ln 2), l's sum with its terms' powers
