@@ -1,6 +1,8 @@
 // hq_kv4_step.cu -- what a serving step does to the 4-bit window cache's
 // bookkeeping (include/hq_kv4.h): pages and slots for sequences that grow or
 // shrink, and the accepted path of a tree of drafted tokens.
+#include <atomic>
+
 #include <cuda_runtime.h>
 
 #include "hq_kv4.h"
@@ -286,16 +288,32 @@ __global__ void __launch_bounds__(32 * kAcceptWarps) kv4_accept_kernel(Kv4Accept
 
 }  // namespace
 
+namespace {
+
+// Lets the larger kernel have the shared memory of the most sequences, once a device and the same
+// whatever the batch: 48 KB, what is there without asking, are for its static part too.
+bool room_for_resize() {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev < 64 && done[dev].load()) return true;
+  if (cudaFuncSetAttribute(kv4_resize_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           3 * HQ_KV4_MAX_RESIZE * (int)sizeof(int)) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  if (dev < 64) done[dev].store(true);
+  return true;
+}
+
+}  // namespace
+
 int launch_kv4_resize(const Kv4ResizeArgs &a, cudaStream_t st) {
   const size_t smem = 3 * (size_t)a.n_seqs * sizeof(int);
   const int64_t entries = (int64_t)a.n_seqs * a.width, most = a.max_tokens / 4 > entries / 4 ? a.max_tokens / 4 : entries / 4;
   // by the entries of the lists, and of the table, of which any may change: a small block has short barriers
   if (a.n_seqs <= 512 && most <= 4096) return launch_behind(kv4_resize_kernel<256>, dim3(1), 256, smem, st, a);
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(kv4_resize_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem) != cudaSuccess) {
-    cudaGetLastError();
-    return 1;
-  }
+  if (!room_for_resize()) return 1;
   Kv4ResizeArgs w = a;
   w.sums = 0;
   const int64_t want = most / 1024 + 1;
