@@ -176,7 +176,10 @@ __device__ int64_t check_starts(const PromptArgs &a, int first, int step) {
 }
 
 // The list of units, longest first (a counting sort by blocks of keys): a unit
-// times the KV heads makes that many items.  A warp a sequence, a lane a unit.  Where
+// times the KV heads makes that many items.  A warp a sequence, a lane a unit.  Units that
+// the sort does not tell apart come as their warps do where items are dealt out whole.  Where they
+// may be cut, the place in the list decides at which key, and so the order of a row's sums: there such
+// units keep the batch's order, ranked by one warp, 32 at a time.  Where
 // there are no more items than blocks of the grid, those find them by themselves
 // (prompt of 77 tokens, 32 heads: 8 us, 12 with a list).
 constexpr int kPrepThreads = 1024, kBuckets = 1024;
@@ -185,6 +188,8 @@ __global__ void __launch_bounds__(kPrepThreads)
   __shared__ int s_at[kBuckets];
   __shared__ int s_warp[32];
   __shared__ int s_end[kSplitUnits + 1];         // blocks of keys up to a unit's end
+  __shared__ int s_first[kSplitUnits];           // a sequence's first unit, in the batch's order
+  __shared__ uint16_t s_rank[kSplitUnits];       // a unit's bucket, then its place in the list
   __shared__ int s_most;
   __shared__ unsigned long long s_units;
   follow_launch();
@@ -202,6 +207,27 @@ __global__ void __launch_bounds__(kPrepThreads)
     if (tid == 0) plan->count = plan->per = 0;
     return;
   }
+  if (split) {                                   // no more sequences than units: a thread two of them
+    static_assert(kSplitUnits <= 2 * kPrepThreads, "a thread two sequences or units");
+    int u[2] = {0, 0};
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (2 * tid + k < a.n_seqs) u[k] = units_of(tiles_of(rows_of(a.starts, 2 * tid + k, a.n_tokens, &bad)), a.G);
+    int incl = u[0] + u[1];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int first = incl - u[0] - u[1];
+    for (int w = 0; w < warp; ++w) first += s_warp[w];
+    if (2 * tid < a.n_seqs) s_first[2 * tid] = first;
+    if (2 * tid + 1 < a.n_seqs) s_first[2 * tid + 1] = first + u[0];
+    __syncthreads();
+  }
   const auto walk = [&](auto &&put) {
     for (int b = warp; b < a.n_seqs; b += kPrepThreads / 32) {
       bool bad = false;
@@ -209,11 +235,14 @@ __global__ void __launch_bounds__(kPrepThreads)
       const int units = units_of(tiles_of(qr), a.G);
       for (int u = lane; u < units; u += 32) {
         const Item x = item_of(qr, kr, a.G, u);
-        put(kBuckets - 1 - min(kBuckets - 1, item_blocks(x)), x);
+        put(kBuckets - 1 - min(kBuckets - 1, item_blocks(x)), x, split ? s_first[b] + u : 0);
       }
     }
   };
-  walk([&](int bucket, const Item &) { atomicAdd(&s_at[bucket], 1); });
+  walk([&](int bucket, const Item &, int number) {
+    atomicAdd(&s_at[bucket], 1);
+    if (split) s_rank[number] = (uint16_t)bucket;
+  });
   __syncthreads();
   const int mine = s_at[tid];
   int incl = mine;
@@ -230,9 +259,21 @@ __global__ void __launch_bounds__(kPrepThreads)
   if (tid == kBuckets - 1) s_end[0] = before + incl;
   __syncthreads();
   const int count = s_end[0];
+  if (split && warp == 0) {
+    for (int n0 = 0; n0 < count; n0 += 32) {
+      const bool is = n0 + lane < count;
+      const int bucket = is ? s_rank[n0 + lane] : kBuckets;
+      const uint32_t same = __match_any_sync(0xffffffffu, bucket);
+      const int from = is ? s_at[bucket] : 0;
+      __syncwarp();
+      if (is) s_rank[n0 + lane] = (uint16_t)(from + __popc(same & ((1u << lane) - 1u)));
+      if (is && same >> lane == 1u) s_at[bucket] = from + __popc(same);     // the last of them
+      __syncwarp();
+    }
+  }
   __syncthreads();
-  walk([&](int bucket, const Item &x) {
-    const int at = atomicAdd(&s_at[bucket], 1);
+  walk([&](int bucket, const Item &x, int number) {
+    const int at = split ? s_rank[number] : atomicAdd(&s_at[bucket], 1);
     list[at] = x;
     if (split) s_end[at + 1] = item_blocks(x);
   });
