@@ -35,7 +35,9 @@ size_t hq_prompt_attention_workspace_bytes(int n_seqs, int64_t n_tokens, int Hq,
  * A row that sees nothing gets zeros and lse -inf.  Scores, weights and sums
  * are held in fp32; the products run on the tensor cores with fp32 sums, for
  * which each weight is rounded once to the inputs' type, as the tensor cores take
- * it.  The order of all sums is fixed.  Rows before starts[0] and behind the last
+ * it: by at most half a step (bf16 2^-8, fp16 2^-11 of it), and in fp16 by up
+ * to 2^-35 of the row's largest weight (2^-25 where scores pass 10^7).  The order of
+ * all sums is fixed.  Rows before starts[0] and behind the last
  * sequence are left as they were.  K and V of a sequence are to be finite:
  * a value that is not reaches rows of the same sequence up to 127 before its
  * own, but no other sequence.

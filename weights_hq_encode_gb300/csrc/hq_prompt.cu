@@ -9,9 +9,9 @@
 //   O += P V         P from tensor memory (in S's place), V from shared memory
 // Warps 0 .. 3 and 4 .. 7 are the two tiles' rows, warp 8 asks for copies, warp 9 for
 // products, which run while one tile's softmax overlaps the other tile's products.  The
-// reference is the maximum of a row's first scores and moves only when a weight
-// passes it by 2^60 (2^14 in fp16), so O, which then has to be read and scaled, is left
-// alone nearly always.
+// reference is taken from the maximum of a row's first scores and moves only when a weight
+// passes 2^60 (bf16; 2^15 in fp16), so O, which then has to be read and scaled, is left
+// alone nearly always (bf16) or mostly (fp16).
 //
 // 16384 tokens, 32 heads on 8, bf16: 1.40 ms, 1.57 PFLOP/s, 83% of the rate measured for
 // cuBLAS in a burst and 94% of what it sustains.  128 keys take a block 3000 to 3200 cycles: a tile's
@@ -47,11 +47,13 @@ constexpr int kHalfBytes = kTileBytes / 2;
 constexpr int kOutBytes = 32 * 128;              // of a warp, on the way out: 32 rows of 64 dimensions
 constexpr int kSmem = (2 + kStages) * kTileBytes + 8 * kOutBytes + 1024;     // 1024: alignment
 constexpr uint32_t kIdesc = umma_idesc_f16(kPromptRows, kKeys);
-// log2 of what a weight may pass the reference by: what its type holds beside the sums.
-constexpr float kSlackBf16 = 60.0f, kSlackF16 = 14.0f;
-// log2 of what a reference is put above the maximum that it is taken from in fp16, whose smaller
-// weights have room below: fewer moves for 2^-19 of the largest weight as the least step.
-constexpr float kMarginF16 = 6.0f;
+// log2 of the weight that a reference gives the score it is taken from, and of the largest weight that does not
+// move it.  In fp16 weights keep their 11 bits down to 2^-14, so the row's largest weight is held at 2^10 to 2^15: those
+// of 2^-24 of it and more are rounded by 2^-11 of themselves, smaller ones by up to 2^-35 of the largest.  (Prompt
+// of 16384 tokens whose scores climb by some tens, fp16, us: 2024; 1984 from 2^8 on, 1947 from 2^6, 1822 from 1, 1738 with
+// 2^-6 to 2^14, where one heavy key of small value over 16384 others left 9% of the outputs' size as an error.)
+template <int KIND> constexpr float kFirst = KIND == HQ_T_BF16 ? 0.0f : 10.0f;
+template <int KIND> constexpr float kMost = KIND == HQ_T_BF16 ? 60.0f : 15.0f;
 
 // What a block does next: two tiles (A, B) that share K and V.
 struct Item {
@@ -635,8 +637,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t staged = ring + kStages * kTileBytes + warp * kOutBytes;
     const float c = factor_of<CAP>(a);
     const float scale = fabsf(a.scale), by_cap = CAP ? __fdiv_rn(1.0f, a.cap) : 0.0f, cap_l2 = __fmul_rn(a.cap, kLog2e);
-    constexpr float slack = KIND == HQ_T_BF16 ? kSlackBf16 : kSlackF16;
-    const float margin = KIND == HQ_T_F16 && c > 0x1p-60f ? __fdiv_rn(kMarginF16, c) : 0.0f;
+    constexpr float most_weight = kMost<KIND>;
+    // The reference that gives a score the weight 2^kFirst; 1 from 2^24 on, where scores have no place for it.
+    const float margin = c > 0x1p-60f ? __fdiv_rn(-kFirst<KIND>, c) : 0.0f;
+    const auto ref_of = [&](float score) {
+      return fabsf(__fmul_rn(score, c)) < 0x1p24f ? __fadd_rn(score, margin) : score;
+    };
     const float to_y = fminf(__fmul_rn(scale, by_cap), 3e38f), to_l2 = __fmul_rn(scale, kLog2e);
     uint32_t steps = 0, used = 0;
     Walk walk(a, plan, list);
@@ -681,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t sum[2];
         // Moves the reference for rows whose scores' maximum passed it by too much, and scales what there is.
         const auto move = [&](float most, bool far) {
-          const float now = far ? __fadd_rn(most, margin) : m;
+          const float now = far ? ref_of(most) : m;
           if (j > lo) {
             const float by = m == now ? 1.0f : m == -INFINITY ? 0.0f : ex2(__fmul_rn(__fsub_rn(m, now), c));
             l2 = mul2(l2, pk2(by, by));
@@ -711,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
           const float most = fmaxf(top[0], top[1]);
-          const bool far = j == lo || __fsub_rn(most, m) > slack;
+          const bool far = j == lo || __fsub_rn(most, m) > most_weight;
           if (__any_sync(0xffffffffu, mine && far)) move(most, far);
           again = true;
         }
@@ -733,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!CAP && !less) take(now, 32 * k);
             if (!CAP) top_of(now, top);
             if (k == 0) {
-              if (j == lo && !again) m = __fadd_rn(fmaxf(top[0], top[1]), margin);
+              if (j == lo && !again) m = ref_of(fmaxf(top[0], top[1]));
               const float from = less || m == -INFINITY ? 0.0f : m, mc = __fmul_rn(from, c);
               m2 = pk2(from, from);
               mc2 = pk2(-mc, -mc);
@@ -751,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (again) break;
           // Once more where a weight passed the reference by too much; and where c m is so large that its
           // rounding, the same for the whole row, matters by itself: there m is taken off the scores first.
-          const bool far = __fmul_rn(__fsub_rn(fmaxf(top[0], top[1]), m), c) > slack;
+          const bool far = __fmul_rn(__fsub_rn(fmaxf(top[0], top[1]), m), c) > most_weight;
           const float size = fabsf(__fmul_rn(m, c));
           const bool large = size >= 0x1p20f && size < INFINITY;
           if (!__any_sync(0xffffffffu, mine && (far || large))) break;
