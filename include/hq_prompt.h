@@ -40,7 +40,9 @@ size_t hq_prompt_attention_workspace_bytes(int n_seqs, int64_t n_tokens, int Hq,
  * all sums is fixed.  Rows before starts[0] and behind the last
  * sequence are left as they were.  K and V of a sequence are to be finite:
  * a value that is not reaches rows of the same sequence up to 127 before its
- * own, but no other sequence.
+ * own, but no other sequence.  In bf16 the magnitudes of V that a row sees are to come to
+ * less than 2^96 in every dimension (beyond, that row may come out non-finite), and parts of
+ * an output below 2^-96 may be lost.
  *   d_starts     [n_seqs + 1] int32, ascending, at most n_tokens
  *   d_k_starts   the same for K and V, at most n_k_tokens; NULL: d_starts, and
  *                n_k_tokens must be n_tokens

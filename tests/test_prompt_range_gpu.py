@@ -76,3 +76,22 @@ def test_equal_sequences_cut_into_pieces(hq, case):
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
     if case > 0:
         check(q, k, v, starts, k_starts, 128 ** -0.5, cap, first)
+
+
+@pytest.mark.parametrize("value", [2.0 ** 80, 2.0 ** 68, 1.0, 2.0 ** -80])
+def test_values_of_any_size(hq, value):
+    """Values far from 1 under scores that climb and fall by up to 85 in steps of any size, many of
+    them equal, whole prompts and pieces."""
+    rng = np.random.default_rng(75)
+    d = rng.standard_normal(128)
+    d /= np.linalg.norm(d)
+    for n, m, up in ((900, 900, 19.0), (900, 900, -19.0), (900, 900, 42.0), (900, 900, 0.0), (5, 9000, 42.0), (5, 9000, 0.0)):
+        q = np.broadcast_to(d, (n, 4, 128)) + 0.03 * rng.standard_normal((n, 4, 128))
+        k = up * np.linspace(-1, 1, m)[:, None, None] * d + 0.5 * rng.standard_normal((m, 2, 128))
+        v = value * rng.standard_normal((m, 2, 128))
+        q, k, v = (torch.from_numpy(x).to(torch.bfloat16).cuda() for x in (q, k, v))
+        for cap in (0.0, 64.0):
+            starts, k_starts = [0, n], None if n == m else [0, m]
+            got = call(hq, q, k, v, starts, k_starts, 1.0, cap)
+            assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()
+            check(q, k, v, starts, k_starts, 1.0, cap, got, {0, 1, 4, 130, 513, n - 1})

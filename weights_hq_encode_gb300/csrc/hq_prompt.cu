@@ -10,7 +10,7 @@
 // Warps 0 .. 3 and 4 .. 7 are the two tiles' rows, warp 8 asks for copies, warp 9 for
 // products, which run while one tile's softmax overlaps the other tile's products.  The
 // reference is taken from the maximum of a row's first scores and moves only when a weight
-// passes 2^60 (bf16; 2^15 in fp16), so O, which then has to be read and scaled, is left
+// passes 2^60 (bf16; 2^5 in fp16) times that score's, so O, which then has to be read and scaled, is left
 // alone nearly always (bf16) or mostly (fp16).
 //
 // 16384 tokens, 32 heads on 8, bf16: 1.40 ms, 1.57 PFLOP/s, 83% of the rate measured for
@@ -52,8 +52,12 @@ constexpr uint32_t kIdesc = umma_idesc_f16(kPromptRows, kKeys);
 // of 2^-24 of it and more are rounded by 2^-11 of themselves, smaller ones by up to 2^-35 of the largest.  (Prompt
 // of 16384 tokens whose scores climb by some tens, fp16, us: 2024; 1984 from 2^8 on, 1947 from 2^6, 1822 from 1, 1738 with
 // 2^-6 to 2^14, where one heavy key of small value over 16384 others left 9% of the outputs' size as an error.)
-template <int KIND> constexpr float kFirst = KIND == HQ_T_BF16 ? 0.0f : 10.0f;
-template <int KIND> constexpr float kMost = KIND == HQ_T_BF16 ? 60.0f : 15.0f;
+// In bf16 weights keep their bits whatever their size; what has to fit fp32 are the sums of weights and values: 2^30
+// above the reference they do while V's magnitudes come to less than 2^97, 2^-30 below it they keep parts of 2^-96 of an
+// output.  (The same prompt in bf16: 1402; 1472 with 2^-20 to 2^20, 1554 with 2^-15 to 2^15, 1959 with 1 to 2^8; 1399 with
+// 1 to 2^60, where values from 2^68 on came out infinite.)
+template <int KIND> constexpr float kFirst = KIND == HQ_T_BF16 ? -30.0f : 10.0f;
+template <int KIND> constexpr float kMost = KIND == HQ_T_BF16 ? 30.0f : 15.0f;
 
 // What a block does next: two tiles (A, B) that share K and V.
 struct Item {
