@@ -7,9 +7,13 @@ import sys
 
 import numpy as np
 import pytest
+import torch
 
+from oracle import kv4 as R
+from oracle import serving as S
+from test_kv4_gpu import DT, HALF_STEP, MASK, U, Cache
 from test_kv4_gpu import hq  # noqa: F401  (the fixture)
-from test_serving_gpu import Pool
+from test_serving_gpu import Pool, room, tree, trees
 
 pytestmark = pytest.mark.gpu
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -35,3 +39,57 @@ def test_resize_of_many_sequences_first(hq, B):
     got = subprocess.run([sys.executable, "-c", code], env=dict(os.environ, PYTHONPATH=path), cwd=HERE,
                          capture_output=True, text=True, timeout=300)
     assert got.returncode == 0, got.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ tree attention
+def check(C, lens, parents, q, scale, cap, got, kind="f32", wide=False, least=0.0):
+    """`wide`: the kernel of 128-row tiles ran, which rounds a weight once to fp16 for outputs of 16
+    bits: by 2^-11 of it and 2^-25 beside 2^6 and more of the row's largest.  `least`: what fp32 has no room for."""
+    ref = S.tree(C.pages, C.table, lens, parents, q.double().cpu().numpy(), MASK, scale, cap)
+    out, lse = (t.double().cpu().numpy() for t in got)
+    steps = ((np.array(lens) + q.shape[1]) / 16)[:, None, None]
+    score = 30 * U * ref["zeta"] + 566 * U * ref["zeta_codes"] + 8 * U * np.minimum(cap, 4 * ref["zeta"])
+    tol = ((2 * score + (68 * steps + 100) * U) * np.linalg.norm(ref["size"], axis=-1) +
+           1200 * U * np.sqrt(128.0) * ref["scales"]) + least
+    if kind != "f32" and wide:
+        tol += 2.0 ** -11 * np.linalg.norm(ref["size"], axis=-1)
+    rounding = HALF_STEP[kind] * np.linalg.norm(ref["out"], axis=-1) * 1.01
+    err = np.linalg.norm(out - ref["out"], axis=-1)
+    assert (err <= tol + rounding).all(), (err / (tol + rounding + 1e-300)).max()
+    empty = np.isneginf(ref["lse"])
+    assert not out[empty].any() and np.array_equal(np.isneginf(lse), empty)
+    d = np.abs(lse[~empty] - ref["lse"][~empty])
+    assert (d <= (score + (2 * steps + 24) * U)[~empty] + 4 * U * np.abs(ref["lse"][~empty])).all()
+
+
+def rows_for(C, k, v):
+    """The same rows k, v [tokens][nh][128] for every sequence."""
+    for b in range(len(C.lens)):
+        R.append(C.pages, C.table, k.astype(np.float32), v.astype(np.float32), [b] * len(k), range(len(k)), MASK)
+    C.upload()
+
+
+@pytest.mark.parametrize("n,G", [(4, 4), (48, 4)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("value,up", [(0.0, 200), (2.0 ** -60, 100)])
+def test_tree_scores_of_rows_without_value(hq, n, G, out, value, up):
+    """Values of zero, or of 2^-160 of those before, under scores far above all before them; values under scores
+    a little below those.  (Weights below 2^-126 of the largest are none in fp32.)"""
+    rng = np.random.default_rng(81)
+    m, nh = 1500, 2
+    C = Cache(hq, rng, [m + n] * 2, nh, 16, width=room(2, nh, n * G, 16, 98), empty=True)
+    k, v = (rng.standard_normal((m + n, nh, 128)) for _ in range(2))
+    d = rng.standard_normal(128)
+    d /= np.linalg.norm(d)
+    k[128:900] += up * d                         # from a block of 128 tokens on
+    k[900:] += (up - 3) * d
+    v[128:900] *= value
+    v[:128] *= 2.0 ** 100 if value else 1.0
+    rows_for(C, k, v)
+    parents = trees(rng, 2, n, "random")
+    q = torch.from_numpy((d + 0.02 * rng.standard_normal((2, n, nh * G, 128))).astype(np.float32)).cuda()
+    for lens in ([m, m], [600, 700], [m, 850]):  # the last with no other value near the largest score
+        got = tree(hq, C, lens, parents, q, 1.0, 0.0, DT[out])
+        assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all() and int(C.status) == 0
+        check(C, lens, parents, q, 1.0, 0.0, got, out, wide=n * G > 32,
+              least=1e-36 if value == 0 else 2.0 ** -126 * 2.0 ** 100 * 128 * 24)       # 128 rows of norm 24 at most

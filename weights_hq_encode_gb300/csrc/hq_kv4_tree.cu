@@ -580,12 +580,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(Kv4AttnArgs a) {
         top = fmaxf(top, S.top[s][half ^ 1][row]);
         // The references move only when a weight 2^(z - m) s f might pass 2^15 by the block's largest s; f
         // then holds the row's largest weight so far near 2^7, or, where the block's scales are within 2^5 of one
-        // another, no more than that below.
+        // another, no more than that below.  And they move before 2^(z - m), or that times s, leaves fp32: scales may
+        // be 0, or far below those that f was taken from.
         {
           const float4 tops = S.sv_top[slot], lows = S.sv_low[slot];
           const float sv_top = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
           const float lg_top = lg2(sv_top);
-          const bool need = k == 0 || __fadd_rn(__fadd_rn(__fsub_rn(top, m), lg_top), lf) > 14.5f;
+          const float up = __fsub_rn(top, m), up_s = __fadd_rn(up, lg_top);
+          const bool need = k == 0 || __fadd_rn(up_s, lf) > 14.5f || up > 60.0f || up_s > 126.0f;
           if (__any_sync(0xffffffffu, need)) {
             const float sv_low = fminf(fminf(lows.x, lows.y), fminf(lows.z, lows.w));
             const float now = need ? fmaxf(m, ceilf(top)) : m;
