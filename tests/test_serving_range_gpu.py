@@ -11,7 +11,7 @@ import torch
 
 from oracle import kv4 as R
 from oracle import serving as S
-from test_kv4_gpu import DT, HALF_STEP, MASK, U, Cache
+from test_kv4_gpu import DT, HALF_STEP, MASK, U, Cache, queries
 from test_kv4_gpu import hq  # noqa: F401  (the fixture)
 from test_serving_gpu import Pool, room, tree, trees
 
@@ -93,3 +93,38 @@ def test_tree_scores_of_rows_without_value(hq, n, G, out, value, up):
         assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all() and int(C.status) == 0
         check(C, lens, parents, q, 1.0, 0.0, got, out, wide=n * G > 32,
               least=1e-36 if value == 0 else 2.0 ** -126 * 2.0 ** 100 * 128 * 24)       # 128 rows of norm 24 at most
+
+
+@pytest.mark.parametrize("n,G", [(4, 4), (48, 4)])
+@pytest.mark.parametrize("value", [1.0, 2.0 ** 119, 2.0 ** -100])
+def test_tree_keys_and_values_of_any_size(hq, n, G, value):
+    """Keys up to 2^119 under small queries or scales, tiny ones under large ones: scores of a few units."""
+    rng = np.random.default_rng(82)
+    m, nh = 700, 2
+    parents = trees(rng, 2, n, "random")
+    for key, query, scale in ((118, -80, 2.0 ** -40), (119, -10, 2.0 ** -111), (114, -84, 2.0 ** -32), (-104, 90, 2.0 ** 12),
+                              (-100, 40, 2.0 ** 58), (-100, 0, 2.0 ** 98)):
+        C = Cache(hq, rng, [m + n] * 2, nh, 16, width=room(2, nh, n * G, 16, 47), empty=True)
+        k, v = (rng.standard_normal((m + n, nh, 128)) for _ in range(2))
+        rows_for(C, k * 2.0 ** key, v * value)
+        q = queries(rng, 2, n, nh * G, "f32", size=1.0)
+        q = (q.double() * 2.0 ** query).float()
+        for cap in (0.0, 8.0):
+            got = tree(hq, C, [m, 300], parents, q, scale, cap, torch.float32)
+            check(C, [m, 300], parents, q, scale, cap, got)
+            assert int(C.status) == 0
+
+
+@pytest.mark.parametrize("n,G", [(4, 4), (48, 4)])
+def test_tree_no_scale_over_large_keys(hq, n, G):
+    """A scale of 0, or next to it, over keys of any size: equal weights."""
+    rng = np.random.default_rng(84)
+    m, nh = 500, 2
+    parents = trees(rng, 2, n, "random")
+    C = Cache(hq, rng, [m + n] * 2, nh, 16, width=room(2, nh, n * G, 16, 47), empty=True)
+    k, v = (rng.standard_normal((m + n, nh, 128)) for _ in range(2))
+    rows_for(C, k * 2.0 ** 119, v)
+    q = queries(rng, 2, n, nh * G, "f32", size=1.0)
+    for scale in (0.0, -0.0, 1e-45):
+        check(C, [m, 300], parents, q, scale, 0.0, tree(hq, C, [m, 300], parents, q, scale, 0.0, torch.float32))
+    assert int(C.status) == 0

@@ -46,6 +46,10 @@ constexpr int kTileBytes = kRows * kTile * 2, kHalfBytes = kTileBytes / 2;      
 constexpr int kSegmentCost = 96;
 constexpr int kMaxBlocks = 160;                  // of a launch
 constexpr int kScaleSlots = 4;                   // blocks of tokens whose scales are kept
+// K's scales, below 2^122 as those of rows whose transform is finite, are brought down by this and a row's multiplier
+// up, so that a product, below 2^16, times a scale stays within fp32.  (Scales below 2^-116 lose 2^-150 of 2^-10, a score
+// less than 2^-23: |scale| |q| is below 2^110.)
+constexpr float kKeyScale = 0x1p-10f;
 constexpr int kSeenWords = HQ_KV4_MAX_DRAFTS / 32, kSeenRow = kSeenWords + 1;   // a word apart: no bank twice
 constexpr uint32_t kIdesc = umma_idesc_f16(kRows, kTokens);
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemQ = 384;       // columns: S twice, O, q' hi and lo
@@ -321,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(Kv4AttnArgs a) {
           bool none = token >= len || !((valid >> (t >> 4)) & 1u);
           if (!none && draft >= 0) none = !((S.there[draft >> 5] >> (draft & 31)) & 1u);   // what lies there is no scale
           const float sv = none ? 0.0f : bf16_to_f32((uint16_t)sv_bits);
-          S.sk[slot][t] = none ? 0.0f : bf16_to_f32((uint16_t)sk_bits);
+          S.sk[slot][t] = none ? 0.0f : __fmul_rn(bf16_to_f32((uint16_t)sk_bits), kKeyScale);
           S.sv[slot][t] = sv;
           // bits of nonnegative floats order as they do
           const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(sv));
@@ -484,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(Kv4AttnArgs a) {
             st16(to, make_uint4(hi[0], hi[1], hi[2], hi[3]));
             st16(to + 256, make_uint4(lo[0], lo[1], lo[2], lo[3]));
           }
-          if (r8 == 0) S.mul[rr] = fmaxf(fabsf(__fmul_rn(__fmul_rn(CAP ? a.scale : __fmul_rn(a.scale, kLog2e), inv), 0x1p-6f)), 0x1p-126f);   // not 0: -inf stays -inf
+          if (r8 == 0)
+            S.mul[rr] = fmaxf(fabsf(__fmul_rn(__fmul_rn(CAP ? a.scale : __fmul_rn(a.scale, kLog2e), inv), 0x1p-6f / kKeyScale)), 0x1p-149f);   // not 0: -inf stays -inf
         }
         if (pass & 1) {
           rows_sync();
