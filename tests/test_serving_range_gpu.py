@@ -128,3 +128,25 @@ def test_tree_no_scale_over_large_keys(hq, n, G):
     for scale in (0.0, -0.0, 1e-45):
         check(C, [m, 300], parents, q, scale, 0.0, tree(hq, C, [m, 300], parents, q, scale, 0.0, torch.float32))
     assert int(C.status) == 0
+
+
+@pytest.mark.parametrize("n,G", [(4, 4), (48, 4)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("bits", [0x7FFF, 0xFFFF, 0x7F80, 0xFF80, 0xBF80, 0x7F7F, 0x0001, 0x0000])
+def test_tree_behind_padding_holds_no_scales(hq, n, G, out, bits):
+    """Drafts whose path leads to padding get no weight and give none, whatever lies in their places: NaN,
+    infinities, negative, huge and tiny values for scales."""
+    rng = np.random.default_rng(80)
+    lens, nh = [300, 77], 2
+    C = Cache(hq, rng, [m + n for m in lens], nh, 16, width=room(2, nh, n * G, 16, 22))
+    parents = [[-1, -2, 1] + [0] * (n - 3), [-1] * (n - 2) + [-2, n - 2]]
+    for b, j in ((0, 1), (0, 2), (1, n - 2), (1, n - 1)):
+        t = lens[b] + j
+        unit = C.pages[C.table[b, t // 16], :, 0]
+        for at in (2048, 2080):
+            unit[:, at + 2 * (t % 16):at + 2 * (t % 16) + 2] = (bits & 255, bits >> 8)
+    C.upload()
+    q = queries(rng, 2, n, nh * G, "f32")
+    got = tree(hq, C, lens, parents, q, 0.1, 0.0, DT[out])
+    assert int(C.status) == hq.HQ_ERR_PAGE
+    check(C, lens, parents, q, 0.1, 0.0, got, out, wide=n * G > 32)

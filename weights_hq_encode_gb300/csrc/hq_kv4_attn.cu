@@ -484,7 +484,9 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kRows>::blocks) kv4_attn_k
             bool none = !((got >> un) & 1u) || at >= len;
             const int draft = TREE && at < len ? max(0, at - committed) : 0;
             if constexpr (TREE) none = none || (at >= committed && !((s_tree.there[draft >> 5] >> (draft & 31)) & 1u));
-            if (none) sv[un][t] = 0.0f;          // what lies there is no scale
+            // what lies there is no scale, nor need it be behind padding: those of rows that a row sees are not negative, and
+            // finite.  A finite one is no matter, as its weights are 0
+            if (none || (TREE && at >= committed && !(sv[un][t] >= 0.0f && sv[un][t] < INFINITY))) sv[un][t] = 0.0f;
 #pragma unroll
             for (int g = 0; g < kGroups; ++g)
 #pragma unroll

@@ -323,7 +323,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(Kv4AttnArgs a) {
         {
           const int token = (u_lo + kBlockUnits * k) * kUnit + t, draft = token - committed;
           bool none = token >= len || !((valid >> (t >> 4)) & 1u);
-          if (!none && draft >= 0) none = !((S.there[draft >> 5] >> (draft & 31)) & 1u);   // what lies there is no scale
+          // what lies in the place of padding, or of a draft behind padding, may be no scale: those of rows that a row sees
+          // are not negative, and finite.  A finite one is no matter, as its weights are 0
+          if (!none && draft >= 0) none = !((S.there[draft >> 5] >> (draft & 31)) & 1u) || sv_bits >= 0x7F80u;
           const float sv = none ? 0.0f : bf16_to_f32((uint16_t)sv_bits);
           S.sk[slot][t] = none ? 0.0f : __fmul_rn(bf16_to_f32((uint16_t)sk_bits), kKeyScale);
           S.sv[slot][t] = sv;
