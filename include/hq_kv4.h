@@ -210,7 +210,8 @@ size_t hq_kv4_tree_attention_workspace_bytes(const hq_kv4_cache *c, int q_len, i
  * tree, and itself.  Formulas and types are those of hq_kv4_attention, lse and
  * out likewise, and so is the precision, but for outputs of 16 bits with more than
  * 32 rows a KV head, q_len * Hq / n_kv_heads, over tables with room for many tokens:
- * their weights are rounded once to fp16, by at most 2^-11 of them.
+ * their weights are rounded once to fp16, by at most 2^-11 of them and 2^-31 of the
+ * row's largest weight times the largest of V's scales.
  *   d_lengths   [n_seqs] int32: committed tokens, without the drafts
  *   d_parents   [n_seqs][q_len] int32: the draft that j follows, below j; -1: the
  *               last committed token; -2: j is padding.  Padding gets zeros and lse

@@ -13,6 +13,7 @@ from oracle import kv4 as R
 from oracle import serving as S
 from test_kv4_gpu import DT, HALF_STEP, MASK, U, Cache, queries
 from test_kv4_gpu import hq  # noqa: F401  (the fixture)
+from test_kv4_scores_gpu import LN2, SCORES, fill, raw_score, unit_query
 from test_serving_gpu import Pool, room, tree, trees
 
 pytestmark = pytest.mark.gpu
@@ -44,7 +45,7 @@ def test_resize_of_many_sequences_first(hq, B):
 # ------------------------------------------------------------------ tree attention
 def check(C, lens, parents, q, scale, cap, got, kind="f32", wide=False, least=0.0):
     """`wide`: the kernel of 128-row tiles ran, which rounds a weight once to fp16 for outputs of 16
-    bits: by 2^-11 of it and 2^-25 beside 2^6 and more of the row's largest.  `least`: what fp32 has no room for."""
+    bits, by 2^-11 of it (and 2^-31 of the row's largest, which is not counted here).  `least`: what fp32 has no room for."""
     ref = S.tree(C.pages, C.table, lens, parents, q.double().cpu().numpy(), MASK, scale, cap)
     out, lse = (t.double().cpu().numpy() for t in got)
     steps = ((np.array(lens) + q.shape[1]) / 16)[:, None, None]
@@ -150,3 +151,72 @@ def test_tree_behind_padding_holds_no_scales(hq, n, G, out, bits):
     got = tree(hq, C, lens, parents, q, 0.1, 0.0, DT[out])
     assert int(C.status) == hq.HQ_ERR_PAGE
     check(C, lens, parents, q, 0.1, 0.0, got, out, wide=n * G > 32)
+
+
+@pytest.mark.parametrize("n,G", [(4, 4), (48, 4)])
+def test_tree_equal_and_lone_scores(hq, n, G):
+    """Scores beyond 2^24, all equal or one far above the others: outputs are the means of V that they
+    stand for, V's scales rising 2^20-fold along one sequence and falling along the other."""
+    rng = np.random.default_rng(83)
+    lens, nh = [1500, 300], 2
+    full = [m + n for m in lens]
+    C = Cache(hq, rng, full, nh, 16, width=room(2, nh, n * G, 16, 98), empty=True)
+    q = unit_query()
+    k = rng.standard_normal(128)
+    k[5] = 3.0
+    rise = [0.03 * 2.0 ** (20.0 * np.arange(m) / m) for m in full]
+    rise[1] = rise[1][::-1]
+    v = [rng.standard_normal((m, 128)) * r[:, None] for m, r in zip(full, rise)]
+    dq = torch.from_numpy(np.broadcast_to(q, (2, n, nh * G, 128)).copy()).cuda()
+    for lone in (None, 0, 700, 1100):
+        rows = [np.broadcast_to(k, (m, 128)).copy() for m in full]
+        if lone is not None:
+            for b in range(2):
+                rows[b][min(lone, lens[b] - 1)] *= 2.0
+        fill(C, rows, v)
+        raw = raw_score(C, 0, 1, q)
+        for z in [3.0] + SCORES:
+            if lone is not None and z < 1e4:
+                continue
+            got = tree(hq, C, lens, [[-1] * n] * 2, dq, z * LN2 / raw, 0.0, torch.float32)
+            out = got[0].double().cpu().numpy()
+            for b in range(2):
+                V = R.back(R.rotated(C.pages, C.table, b, full[b], 1), MASK)
+                size = np.abs(R.rotated(C.pages, C.table, b, full[b], 1))
+                s = np.concatenate([R.raw_rows(C.pages, p, 1)[1] for p in C.table[b, :-(-full[b] // 16)]], 1)
+                for j in range(n):
+                    p = np.zeros(full[b])
+                    if lone is None:
+                        p[:lens[b]] = p[lens[b] + j] = 1.0 / (lens[b] + 1)
+                    else:
+                        p[min(lone, lens[b] - 1)] = 1.0
+                    for h in range(nh):
+                        tol = ((68 * full[b] / 16 + 100) * U * np.linalg.norm(p @ size[h]) +
+                               1200 * U * np.sqrt(128.0) * (p @ s[h, :full[b]].astype(np.float64)))
+                        err = np.linalg.norm(out[b, j, h * G:(h + 1) * G] - p @ V[h], axis=-1)
+                        assert (err <= tol).all(), (lone, z, b, j, err.max() / tol)
+    assert int(C.status) == 0
+
+
+SIZES = [  # committed lengths, nh, G, drafts, page, cap, q type, out type
+    ([300, 1, 64], 2, 8, 3, 48, 30.0, "bf16", "bf16"),                    # 24 rows a head
+    ([130, 2, 77], 3, 4, 8, 32, 0.0, "f16", "f16"),                       # 32
+    ([257, 31], 2, 5, 13, 64, 0.0, "f32", "f16"),                         # 65
+    ([1100, 40, 0], 1, 4, 64, 64, 0.0, "f16", "bf16"),                    # 256
+]
+
+
+@pytest.mark.parametrize("case,wide", [(i, w) for i, c in enumerate(SIZES) for w in (False, True)
+                                       if not w or c[2] * c[3] > 32])
+def test_tree_weights_in_two_parts(hq, case, wide):
+    """Outputs of 16 bits: the kernel of 16-row tiles rounds nothing but them."""
+    lens, nh, G, n, page, cap, dq, do = SIZES[case]
+    rng = np.random.default_rng(90 + case)
+    parents = trees(rng, len(lens), n, "random")
+    width = -(-(max(lens) + n) // page)
+    C = Cache(hq, rng, [a + n for a in lens], nh, page,
+              width=room(len(lens), nh, n * G, page, width) if wide else width)
+    q = queries(rng, len(lens), n, nh * G, dq)
+    got = tree(hq, C, lens, parents, q, 128 ** -0.5, cap, DT[do])
+    assert int(C.status) == 0
+    check(C, lens, parents, q, 128 ** -0.5, cap, got, do, wide=wide)

@@ -119,7 +119,7 @@ __device__ __forceinline__ void swap_if(bool c, uint32_t &a, uint32_t &b) {
   a = x;
 }
 // (x0, x1) = hi + lo as fp16 pairs, hi with 11 of their bits: x misses hi + lo by 2^-22 of it and
-// 2^-25, which is 2^-32 of a row's largest weight.
+// 2^-25, which is up to 2^-31 of a row's largest weight times the largest of V's scales, as f holds that at 2^6 and more.
 __device__ __forceinline__ void split_cut(float x0, float x1, uint32_t &hi, uint32_t &lo) {
   const float h0 = __uint_as_float(__float_as_uint(x0) & 0xFFFFE000u), h1 = __uint_as_float(__float_as_uint(x1) & 0xFFFFE000u);
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(h1), "f"(h0));
@@ -128,7 +128,7 @@ __device__ __forceinline__ void split_cut(float x0, float x1, uint32_t &hi, uint
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(l1), "f"(l0));
 }
 
-// SPLIT: weights in two parts, for fp32 outputs; else rounded once to fp16, by at most 2^-11 of them.
+// SPLIT: weights in two parts, for fp32 outputs; else rounded once to fp16, by at most 2^-11 of them and the same 2^-25.
 template <bool CAP, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(Kv4AttnArgs a) {
   extern __shared__ unsigned char s_raw[];
