@@ -57,12 +57,12 @@ size_t hq_prompt_attention_workspace_bytes(int n_seqs, int64_t n_tokens, int Hq,
  *   d_lse        [n_tokens][Hq] fp32, or NULL
  *   d_ws         >= hq_prompt_attention_workspace_bytes(), 256-byte aligned;
  *                calls that may overlap need workspaces of their own
- * scale * q . K[t] is to be finite in fp32.  n_seqs, n_kv_heads and Hq are at most
- * 65535, n_tokens and n_k_tokens below 2^31 - 1024, and so are the 128-row tiles of
- * all heads.  *d_status is OR-ed with HQ_ERR_PAGE for starts outside their range or
- * not ascending: they count as the nearest valid ones, and what the rows of such
- * sequences get is not defined; nor is any row's where the sequences come to more
- * 128-row tiles than n_tokens rows can have. */
+ * q . K[t] and scale * q . K[t] are to be finite in fp32.  n_seqs, n_kv_heads and
+ * Hq are at most 65535, n_tokens and n_k_tokens below 2^31 - 1024, and so are the
+ * 128-row tiles of all heads.  *d_status is OR-ed with HQ_ERR_PAGE for starts
+ * outside their range or not ascending: they count as the nearest valid ones, and what
+ * the rows of such sequences get is not defined; nor is any row's where the sequences
+ * come to more 128-row tiles than n_tokens rows can have. */
 int hq_prompt_attention(const int32_t *d_starts, const int32_t *d_k_starts, int n_seqs,
                         const void *d_q, int64_t q_token_stride, int64_t q_head_stride,
                         int64_t n_tokens, int Hq, const void *d_k, int64_t k_token_stride,

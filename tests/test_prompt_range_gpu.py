@@ -95,3 +95,13 @@ def test_values_of_any_size(hq, value):
             got = call(hq, q, k, v, starts, k_starts, 1.0, cap)
             assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()
             check(q, k, v, starts, k_starts, 1.0, cap, got, {0, 1, 4, 130, 513, n - 1})
+
+
+def test_no_scale_over_large_products(hq):
+    """A scale of 0, or next to it, over products up to fp32's limit: equal weights."""
+    rng = np.random.default_rng(76)
+    q, k = (torch.from_numpy(rng.standard_normal((300, h, 128)) * s).to(torch.bfloat16).cuda()
+            for h, s in ((4, 2.0 ** 61), (2, 2.0 ** 60)))
+    v = torch.from_numpy(rng.standard_normal((300, 2, 128))).to(torch.bfloat16).cuda()
+    for scale, cap in ((0.0, 0.0), (-0.0, 0.0), (1e-45, 0.0), (0.0, 5.0)):
+        check(q, k, v, [0, 300], None, scale, cap, call(hq, q, k, v, [0, 300], None, scale, cap))

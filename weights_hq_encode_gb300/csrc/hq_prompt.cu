@@ -361,11 +361,11 @@ struct Bars {
   uint64_t patch;
 };
 
-// What scores are multiplied by to be exponents of 2.  Not 0: -inf stays -inf.
+// What scores are multiplied by to be exponents of 2.  Not 0: -inf stays -inf, and no finite score is anything.
 template <bool CAP>
 __device__ __forceinline__ float factor_of(const PromptArgs &a) {
   const float c = fabsf(__fmul_rn(a.scale, kLog2e));
-  return CAP ? 1.0f : c == 0.0f ? 0x1p-126f : c;
+  return CAP ? 1.0f : c == 0.0f ? 0x1p-149f : c;
 }
 __device__ __forceinline__ float lse_of(float m, float l, float c) {
   return l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(__fmul_rn(m, c), log2f(l)), kLn2);
