@@ -13,9 +13,9 @@
 // passes 2^60 (bf16; 2^5 in fp16) times that score's, so O, which then has to be read and scaled, is left
 // alone nearly always (bf16) or mostly (fp16).
 //
-// 16384 tokens, 32 heads on 8, bf16: 1.40 ms, 1.57 PFLOP/s, 83% of the rate measured for
-// cuBLAS in a burst and 94% of what it sustains.  128 keys take a block 3000 to 3200 cycles: a tile's
-// softmax 1300 (450 instructions a warp; exponentials alone 512), both products 1330, of 1024 at
+// 16384 tokens, 32 heads on 8, bf16: 1.40 ms, 1.57 PFLOP/s, one call a graph's replay, 83% of the rate measured for
+// cuBLAS in a burst and 94% of what it sustains; call after call 1.47 to 1.50 ms, 1.48 PFLOP/s.  128 keys take a block 3000 to
+// 3200 cycles: a tile's softmax 1300 (450 instructions a warp; exponentials alone 512), both products 1330, of 1024 at
 // the pipe's full rate, and the waits between; the other tile is half a turn behind.
 #include <cuda.h>
 #include <cuda_bf16.h>
